@@ -20,7 +20,9 @@ from . import _lib
 from ._lib import MOE_BF16, MOE_F32, MOE_FP8, MOE_MXFP8, MlpDesc, MoeError, check, lib, ptr_table
 
 __all__ = [
-    "moe_route_topk", "moe_router_logits", "moe_route_topk_bwd", "moe_router_bwd", "moe_permute", "moe_unpermute_combine", "mxfp8_quantize",
+    "moe_route_topk", "moe_router_logits", "moe_route_topk_bwd", "moe_router_bwd", "moe_balance_loss",
+    "moe_balance_loss_bwd", "moe_pre_norm", "moe_pre_norm_bwd", "moe_post_norm", "moe_post_norm_bwd",
+    "moe_permute", "moe_unpermute_combine", "mxfp8_quantize",
     "fp8_tensor_quantize", "mxfp8_quantize_colwise", "fp8_tensor_quantize_colwise", "mxfp8_pack_weight_bwd",
     "fp8_tensor_pack_weight_bwd", "mxfp8_quantize_weights", "fp8_tensor_quantize_weights",
     "moe_grouped_mlp_fwd", "moe_grouped_mlp_bwd", "moe_grouped_linear", "moe_grouped_gate_up_swiglu", "gemm_workspace",
@@ -46,6 +48,26 @@ def _need_cuda(*ts):
                 raise ValueError("tensors must live on the GPU")
             if not t.is_contiguous():
                 raise ValueError("tensors must be contiguous")
+
+
+def _need(fn, ref, *ts):
+    """Every given tensor on ref's GPU and contiguous."""
+    dev = ref.device
+    for t in (ref, *ts):
+        if t is not None:
+            if t.device != dev or not t.is_cuda:
+                raise ValueError(f"{fn}: tensors must live on one GPU")
+            if not t.is_contiguous():
+                raise ValueError(f"{fn}: tensors must be contiguous")
+
+
+def _launch(fn, dev, *args):
+    """Call entry point fn (its last argument, the stream, added) with dev as the current device."""
+    if torch.cuda.current_device() == dev.index:
+        check(fn, getattr(lib(), fn)(*args, _stream(dev)))
+    else:
+        with torch.cuda.device(dev):
+            check(fn, getattr(lib(), fn)(*args, _stream(dev)))
 
 
 def _workspace(nbytes, device):
@@ -111,6 +133,197 @@ def moe_router_bwd(x: torch.Tensor, w_router: torch.Tensor, d_logits: torch.Tens
     check("moe_router_bwd", lib().moe_router_bwd(_p(x), _p(w_router), _p(d_logits), _p(dx_in), T, H, E, _p(dx),
                                                  _p(dw), _p(ws), ws.numel(), _stream(x.device)))
     return dx, dw
+
+
+def _seq_len(fn, T, seq_len):
+    L = seq_len if seq_len is not None else max(T, 1)
+    if L < 1 or T % L:
+        raise ValueError(f"{fn}: seq_len must divide the number of tokens")
+    return L
+
+
+def _check_mask(fn, mask, T):
+    if mask is not None and (mask.dtype not in (torch.uint8, torch.bool) or mask.shape != (T,)):
+        raise ValueError(f"{fn}: mask must be bool or uint8 [T]")
+
+
+def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, balance_coef: float, z_coef: float = 0.0,
+                     seq_len: int | None = None, mask: torch.Tensor | None = None):
+    """Load-balance loss (with z-loss) of router logits [T, E] float32 routed to topk_idx [T, k] int32.
+
+    Returns (loss [3] float32: loss, mean balance term, mean z term; counts [T / seq_len, E] int32;
+    tokens [T / seq_len + 1] int32: counted tokens per sequence, then the sequences that have any).
+    seq_len: tokens per sequence (default: one loss over all T); mask [T]: 0 leaves a token out."""
+    _need("moe_balance_loss", logits, topk_idx, mask)
+    T, E = logits.shape
+    if logits.dtype != torch.float32 or topk_idx.dtype != torch.int32 or topk_idx.shape[0] != T:
+        raise ValueError("moe_balance_loss: logits [T, E] must be float32 and topk_idx [T, k] int32")
+    _check_mask("moe_balance_loss", mask, T)
+    L = _seq_len("moe_balance_loss", T, seq_len)
+    dev = logits.device
+    counts = torch.empty((T // L, E), dtype=torch.int32, device=dev)
+    tokens = torch.empty(T // L + 1, dtype=torch.int32, device=dev)
+    loss = torch.empty(3, dtype=torch.float32, device=dev)
+    ws = _workspace(workspace_size(_lib.MOE_OP_BALANCE_LOSS, None, L, T, E), dev)
+    _launch("moe_balance_loss", dev, _p(logits), _p(topk_idx), _p(mask), T, E, topk_idx.shape[1], L, balance_coef,
+            z_coef, _p(counts), _p(tokens), _p(loss), _p(ws), ws.numel())
+    return loss, counts, tokens
+
+
+def moe_balance_loss_bwd(logits: torch.Tensor, counts: torch.Tensor, tokens: torch.Tensor, k: int,
+                         balance_coef: float, z_coef: float = 0.0, seq_len: int | None = None,
+                         mask: torch.Tensor | None = None, d_loss: torch.Tensor | None = None,
+                         d_logits_in: torch.Tensor | None = None, d_logits: torch.Tensor | None = None) -> torch.Tensor:
+    """Gradient of moe_balance_loss's loss[0] in the logits, times d_loss ([1] float32, default 1), plus
+    d_logits_in ([T, E] float32, default 0): d_logits [T, E] float32 (may be d_logits_in itself)."""
+    _need("moe_balance_loss_bwd", logits, counts, tokens, mask, d_loss, d_logits_in, d_logits)
+    T, E = logits.shape
+    _check_mask("moe_balance_loss_bwd", mask, T)
+    L = _seq_len("moe_balance_loss_bwd", T, seq_len)
+    for t, shape in ((d_logits_in, logits.shape), (d_logits, logits.shape)):
+        if t is not None and (t.dtype != torch.float32 or t.shape != shape):
+            raise ValueError("moe_balance_loss_bwd: d_logits_in and d_logits must be float32 [T, E]")
+    if (logits.dtype != torch.float32 or counts.dtype != torch.int32 or counts.shape != (T // L, E)
+            or tokens.dtype != torch.int32 or tokens.numel() != T // L + 1
+            or (d_loss is not None and (d_loss.dtype != torch.float32 or d_loss.numel() != 1))):
+        raise ValueError("moe_balance_loss_bwd: logits and d_loss must be float32, counts and tokens the forward's")
+    if d_logits is None:
+        d_logits = torch.empty_like(logits)
+    _launch("moe_balance_loss_bwd", logits.device, _p(logits), _p(counts), _p(tokens), _p(mask), T, E, k, L,
+            balance_coef, z_coef, _p(d_loss), _p(d_logits_in), _p(d_logits))
+    return d_logits
+
+
+def _norm_dtype(fn, x, *same):
+    if x.dtype not in (torch.float32, torch.bfloat16) or x.dim() != 2:
+        raise ValueError(f"{fn}: rows must be a 2-D float32 or bfloat16 tensor")
+    for t in same:
+        if t is not None and t.dtype != x.dtype:
+            raise ValueError(f"{fn}: all tensors but rstd and the maps must share one dtype")
+    return _DT[x.dtype]
+
+
+def _gate_args(fn, gate, gate_group, T, H):
+    """(kind, group) of a gate tensor: [T] per token, [G, H] one row for every gate_group tokens."""
+    if gate is None:
+        return _lib.MOE_GATE_NONE, 1
+    if gate.dim() == 1:
+        if gate.shape[0] != T:
+            raise ValueError(f"{fn}: a gate per token must be [T]")
+        return _lib.MOE_GATE_TOKEN, 1
+    group = gate_group if gate_group is not None else max(1, -(-T // max(gate.shape[0], 1)))
+    if gate.dim() != 2 or gate.shape[1] != H or group < 1 or (T > 0 and gate.shape[0] != -(-T // group)):
+        raise ValueError(f"{fn}: a channel gate must be [ceil(T / gate_group), H]")
+    return _lib.MOE_GATE_CHANNEL, group
+
+
+def _check_rows(fn, row_id_map, T, k):
+    if row_id_map is None:
+        if k != 1:
+            raise ValueError(f"{fn}: k > 1 needs row_id_map")
+    elif row_id_map.dtype != torch.int32 or row_id_map.numel() != T * k:
+        raise ValueError(f"{fn}: row_id_map must be int32 [T * k]")
+
+
+def moe_pre_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, save_rstd: bool = False):
+    """RMS norm of the rows of x [T, H] (bf16 or float32) with weight [H]: y, or (y, rstd [T]) with save_rstd."""
+    _need("moe_pre_norm", x, weight)
+    dt = _norm_dtype("moe_pre_norm", x, weight)
+    T, H = x.shape
+    if weight.shape != (H,):
+        raise ValueError("moe_pre_norm: weight must be [H]")
+    y = torch.empty_like(x)
+    rstd = torch.empty(T, dtype=torch.float32, device=x.device) if save_rstd else None
+    _launch("moe_pre_norm", x.device, _p(x), _p(weight), dt, T, H, eps, _p(y), _p(rstd))
+    return (y, rstd) if save_rstd else y
+
+
+def _norm_workspace(T, H, kind, group, dev):
+    return _workspace(workspace_size(_lib.MOE_OP_NORM_BWD, MlpDesc(1, H, 1, 0, 0, 0, 0), 0, T, kind,
+                                     max(1, min(group, T))), dev)
+
+
+def moe_pre_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
+                     dx_in: torch.Tensor | None = None, dx_in_scale: float = 1.0, dx: torch.Tensor | None = None):
+    """Backward of moe_pre_norm -> (dx [T, H] = dx_in_scale * dx_in + the norm's gradient, dweight [H] float32)."""
+    _need("moe_pre_norm_bwd", x, dy, weight, rstd, dx_in, dx)
+    dt = _norm_dtype("moe_pre_norm_bwd", x, dy, weight, dx_in, dx)
+    T, H = x.shape
+    if weight.shape != (H,) or rstd.dtype != torch.float32 or rstd.shape != (T,):
+        raise ValueError("moe_pre_norm_bwd: weight must be [H] and rstd float32 [T]")
+    for t in (dy, dx_in, dx):
+        if t is not None and t.shape != x.shape:
+            raise ValueError("moe_pre_norm_bwd: dy, dx_in and dx must have x's shape")
+    if dx is None:
+        dx = torch.empty_like(x)
+    dw = torch.empty(H, dtype=torch.float32, device=x.device)
+    ws = _norm_workspace(T, H, _lib.MOE_GATE_NONE, 1, x.device)
+    _launch("moe_pre_norm_bwd", x.device, _p(dy), _p(x), _p(weight), _p(rstd), _p(dx_in), dx_in_scale, dt, T, H,
+            _p(dx), _p(dw), _p(ws), ws.numel())
+    return dx, dw
+
+
+def moe_post_norm(y: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, row_id_map: torch.Tensor | None = None,
+                  k: int = 1, gate: torch.Tensor | None = None, gate_group: int | None = None,
+                  residual_scale: float = 1.0, eps: float = 1e-6, save_for_bwd: bool = False,
+                  next_weight: torch.Tensor | None = None, out: torch.Tensor | None = None):
+    """out = residual_scale * x + gate * RMSNorm(c) * weight with c[t] the sum of token t's k rows of y
+    (through row_id_map, as moe_unpermute_combine) or y[t] itself without a map.
+
+    gate: None, [T] (per token) or [ceil(T / gate_group), H] (one row for every gate_group consecutive tokens;
+    default: T over the gate's rows). Returns a dict with out, and c and rstd with save_for_bwd, and
+    y_next and rstd_next (moe_pre_norm of out) with next_weight. out may be x."""
+    _need("moe_post_norm", x, y, weight, row_id_map, gate, next_weight, out)
+    dt = _norm_dtype("moe_post_norm", x, y, weight, gate, next_weight, out)
+    T, H = x.shape
+    _check_rows("moe_post_norm", row_id_map, T, k)
+    kind, group = _gate_args("moe_post_norm", gate, gate_group, T, H)
+    if y.shape != (T * k, H) or weight.shape != (H,) or (next_weight is not None and next_weight.shape != (H,)):
+        raise ValueError("moe_post_norm: y must be [T * k, H] and the weights [H]")
+    if out is not None and out.shape != x.shape:
+        raise ValueError("moe_post_norm: out must have x's shape")
+    dev = x.device
+    r = dict(out=out if out is not None else torch.empty_like(x))
+    if save_for_bwd:
+        r["c"] = torch.empty_like(x)
+        r["rstd"] = torch.empty(T, dtype=torch.float32, device=dev)
+    if next_weight is not None:
+        r["y_next"] = torch.empty_like(x)
+        r["rstd_next"] = torch.empty(T, dtype=torch.float32, device=dev)
+    _launch("moe_post_norm", dev, _p(y), _p(row_id_map), k, _p(x), _p(weight), kind, _p(gate), group, residual_scale,
+            _p(next_weight), dt, T, H, eps, _p(r["out"]), _p(r.get("c")), _p(r.get("rstd")), _p(r.get("y_next")),
+            _p(r.get("rstd_next")))
+    return r
+
+
+def moe_post_norm_bwd(dout: torch.Tensor, c: torch.Tensor, rstd: torch.Tensor, weight: torch.Tensor,
+                      row_id_map: torch.Tensor | None = None, k: int = 1, gate: torch.Tensor | None = None,
+                      gate_group: int | None = None, dy: torch.Tensor | None = None):
+    """Backward of moe_post_norm: a dict with dy [T * k, H] (the gradient of every row, in y's order; rows no slot
+    points at are left as they were), dweight [H] float32 and dgate (float32, the gate's shape, with a gate)."""
+    _need("moe_post_norm_bwd", dout, c, rstd, weight, row_id_map, gate, dy)
+    dt = _norm_dtype("moe_post_norm_bwd", dout, c, weight, gate, dy)
+    T, H = dout.shape
+    _check_rows("moe_post_norm_bwd", row_id_map, T, k)
+    kind, group = _gate_args("moe_post_norm_bwd", gate, gate_group, T, H)
+    if c.shape != dout.shape or weight.shape != (H,) or rstd.dtype != torch.float32 or rstd.shape != (T,):
+        raise ValueError("moe_post_norm_bwd: c must have dout's shape, weight [H] and rstd float32 [T]")
+    if dy is None:
+        dy = torch.empty((T * k, H), dtype=dout.dtype, device=dout.device)
+    elif dy.shape != (T * k, H):
+        raise ValueError("moe_post_norm_bwd: dy must be [T * k, H]")
+    dev = dout.device
+    dw = torch.empty(H, dtype=torch.float32, device=dev)
+    dgate = None
+    if gate is not None:
+        dgate = (torch.empty if T > 0 else torch.zeros)(gate.shape, dtype=torch.float32, device=dev)
+    ws = _norm_workspace(T, H, kind, group, dev)
+    _launch("moe_post_norm_bwd", dev, _p(dout), _p(c), _p(rstd), _p(weight), kind, _p(gate), group, _p(row_id_map), k,
+            dt, T, H, _p(dy), _p(dw), _p(dgate), _p(ws), ws.numel())
+    r = dict(dy=dy, dweight=dw)
+    if gate is not None:
+        r["dgate"] = dgate
+    return r
 
 
 def moe_permute(x: torch.Tensor, topk_idx: torch.Tensor, topk_prob: torch.Tensor | None, E: int,

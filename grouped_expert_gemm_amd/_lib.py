@@ -14,6 +14,8 @@ LIB_PATH = os.path.join(HERE, "libmoe.so")
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_LAUNCH = range(5)
 MOE_F32, MOE_BF16, MOE_MXFP8, MOE_FP8 = 0, 1, 2, 3
 MOE_OP_PERMUTE, MOE_OP_MLP_FWD, MOE_OP_MLP_BWD, MOE_OP_GROUPED_GEMM, MOE_OP_ROUTER_BWD = 0, 1, 2, 3, 4
+MOE_OP_BALANCE_LOSS, MOE_OP_NORM_BWD = 5, 6
+MOE_GATE_NONE, MOE_GATE_TOKEN, MOE_GATE_CHANNEL = 0, 1, 2
 MOE_MAX_EXPERTS = 256
 
 # every symbol include/moe.h declares
@@ -23,6 +25,8 @@ EXPORTS = (
     "fp8_tensor_quantize_colwise", "fp8_tensor_pack_weight_bwd",
     "mxfp8_pack_weight_bwd", "mxfp8_quantize_weights", "fp8_tensor_quantize_weights",
     "moe_grouped_mlp_fwd", "moe_grouped_mlp_bwd", "moe_grouped_linear", "moe_grouped_gate_up_swiglu",
+    "moe_balance_loss", "moe_balance_loss_bwd",
+    "moe_pre_norm", "moe_pre_norm_bwd", "moe_post_norm", "moe_post_norm_bwd",
     "moe_workspace_size",
     "moe_status_str", "moe_last_error",
 )
@@ -44,6 +48,7 @@ _lock = threading.Lock()
 _lib = None
 
 vp, i64, c_int, sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_size_t
+f32 = ctypes.c_float
 PP = ctypes.POINTER(ctypes.c_void_p)
 
 
@@ -77,6 +82,13 @@ def _declare(lib):
         "moe_grouped_linear": [c_int, i64, c_int, c_int, c_int, vp, PP, vp, vp, vp, sz, vp],
         "moe_grouped_gate_up_swiglu": [c_int, i64, c_int, c_int, c_int, vp, vp, PP, PP, vp, vp, vp, vp, vp, vp, sz,
                                        vp],
+        "moe_balance_loss": [vp, vp, vp, i64, c_int, c_int, i64, f32, f32, vp, vp, vp, vp, sz, vp],
+        "moe_balance_loss_bwd": [vp, vp, vp, vp, i64, c_int, c_int, i64, f32, f32, vp, vp, vp, vp],
+        "moe_pre_norm": [vp, vp, c_int, i64, c_int, f32, vp, vp, vp],
+        "moe_pre_norm_bwd": [vp, vp, vp, vp, vp, f32, c_int, i64, c_int, vp, vp, vp, sz, vp],
+        "moe_post_norm": [vp, vp, c_int, vp, vp, c_int, vp, i64, f32, vp, c_int, i64, c_int, f32, vp, vp, vp, vp, vp,
+                          vp],
+        "moe_post_norm_bwd": [vp, vp, vp, vp, c_int, vp, i64, vp, c_int, c_int, i64, c_int, vp, vp, vp, vp, sz, vp],
         "moe_workspace_size": [c_int, ctypes.POINTER(MlpDesc), i64, i64, c_int, c_int, ctypes.POINTER(sz)],
     }
     for name, args in sig.items():

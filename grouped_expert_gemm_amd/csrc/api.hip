@@ -85,6 +85,16 @@ extern "C" moe_status moe_workspace_size(moe_op op, const moe_mlp_desc* desc, in
         return fail(MOE_ERR_INVALID_ARG, "moe_workspace_size(ROUTER_BWD): desc NULL or bad T/E/H");
       *bytes = router_bwd_workspace_bytes(T, desc->H, desc->E);
       return MOE_OK;
+    case MOE_OP_BALANCE_LOSS:
+      if (T < 0 || E < 1 || E > MOE_MAX_EXPERTS || R < 1 || T % R != 0)
+        return fail(MOE_ERR_INVALID_ARG, "moe_workspace_size(BALANCE_LOSS): bad T/E or seq_len (R)");
+      *bytes = balance_workspace_bytes(T, R, E);
+      return MOE_OK;
+    case MOE_OP_NORM_BWD:
+      if (!desc || T < 0 || desc->H < 1 || E < MOE_GATE_NONE || E > MOE_GATE_CHANNEL || (E == MOE_GATE_CHANNEL && k < 1))
+        return fail(MOE_ERR_INVALID_ARG, "moe_workspace_size(NORM_BWD): desc NULL or bad T/H, gate kind (E) or group (k)");
+      *bytes = norm_bwd_workspace_bytes(T, desc->H, E, k);
+      return MOE_OK;
   }
   return fail(MOE_ERR_INVALID_ARG, "moe_workspace_size: unknown op");
 }

@@ -19,6 +19,8 @@ size_t mlp_fwd_workspace_bytes(const moe_mlp_desc& d, int64_t R);
 size_t mlp_bwd_workspace_bytes(const moe_mlp_desc& d, int64_t R);
 size_t grouped_gemm_workspace_bytes();  // split-K tail area of one grouped GEMM call
 size_t router_bwd_workspace_bytes(int64_t T, int H, int E);  // dW token-chunk partials
+size_t balance_workspace_bytes(int64_t T, int64_t seq_len, int E);  // partial sums of moe_balance_loss
+size_t norm_bwd_workspace_bytes(int64_t T, int H, int gate_kind, int64_t gate_group);  // column partials
 
 // mxfp8 quantisation launcher used by the forward (weights and activations)
 moe_status launch_mxfp8_quantize(const void* in_bf16, int64_t rows, int64_t cols, uint8_t* e4m3,

@@ -120,6 +120,50 @@ moe_status moe_router_bwd(const void* x, const void* w_router, const float* d_lo
                           size_t workspace_bytes, void* stream);
 
 /*
+ * Load-balance loss of the router with an optional z-loss term, and the number of tokens
+ * each expert was given. A router trained on the task alone sends most tokens to a few
+ * experts, whose row groups then set the grouped GEMMs' time; this loss is added to the
+ * task's to keep the groups even.
+ * The T tokens are T / seq_len sequences of seq_len consecutive tokens (seq_len = T: one
+ * loss over the whole batch). For a sequence with N counted tokens, p = softmax of a
+ * token's logits and lse their log-sum-exp:
+ *   counts[e] = slots of its counted tokens that hold expert e,  f_e = counts[e] / (k N)
+ *   B = E sum_e f_e mean_t p[t, e]   (1 for even loads),   Z = mean_t lse[t]^2
+ *   loss = mean over the sequences with N > 0 of (balance_coef B + z_coef Z), 0 if none
+ *   logits   [T, E] float32; topk_idx [T, k] int32 (moe_route_topk's; an id out of [0, E)
+ *            is not counted, a repeated one counts each time)
+ *   mask     [T] uint8 or NULL: a token whose byte is 0 (padding) is not counted and its
+ *            logits are not read. A token whose logits are all -infinity is not counted.
+ *   counts   [T / seq_len, E] int32 (out)
+ *   tokens   [T / seq_len + 1] int32 (out): counted tokens of each sequence, then the
+ *            number of sequences that have any
+ *   loss     [3] float32 (out): loss, mean B, mean Z
+ * float32 arithmetic, sums in a fixed order. T = 0 writes loss and tokens[0] = 0.
+ * workspace: moe_workspace_size(MOE_OP_BALANCE_LOSS, NULL, seq_len, T, E, 0) bytes (seq_len
+ * in the place of R), 256-byte aligned.
+ * Limits: 1 <= k <= E <= MOE_MAX_EXPERTS, T % seq_len == 0, T * k < 2^31.
+ */
+moe_status moe_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* mask, int64_t T, int E,
+                            int k, int64_t seq_len, float balance_coef, float z_coef, int32_t* counts,
+                            int32_t* tokens, float* loss, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Gradient of moe_balance_loss in the logits (the counts are piecewise constant):
+ *   d_logits[t, e] = d_logits_in[t, e] + g / (S' N) p[t, e] *
+ *                    (balance_coef E (f_e - sum_e' f_e' p[t, e']) + 2 z_coef lse[t])
+ * with N the token's sequence's counted tokens and S' the sequences that have any; a token
+ * that was not counted gets d_logits_in alone.
+ *   counts, tokens: of the forward call with the same arguments
+ *   d_loss: ONE float32 in device memory, the gradient g of loss[0], or NULL for 1
+ *   d_logits_in [T, E] float32 or NULL for 0 (moe_route_topk_bwd's output, say); may equal
+ *   d_logits [T, E] float32 (out, every entry written)
+ */
+moe_status moe_balance_loss_bwd(const float* logits, const int32_t* counts, const int32_t* tokens,
+                                const uint8_t* mask, int64_t T, int E, int k, int64_t seq_len, float balance_coef,
+                                float z_coef, const float* d_loss, const float* d_logits_in, float* d_logits,
+                                void* stream);
+
+/*
  * Token permutation into per-expert groups. Source: split_sizes of GroupedLinear
  * (Challenge 1) and the per-expert row gather of the baseline loop; token
  * permutation before the grouped GEMM is also named in the PyTorch-native MoE
@@ -181,6 +225,83 @@ moe_status moe_permute_noalloc(const void* x, const uint8_t* x_scale, moe_dtype 
 moe_status moe_unpermute_combine(const void* y_perm, moe_dtype dt, const int32_t* row_id_map,
                                  const float* weights, int64_t T, int H, int k, void* out,
                                  void* stream);
+
+/*
+ * RMS norm before the expert block (the pre-norm of a decoder layer, whose output feeds
+ * moe_router_logits and moe_permute):
+ *   r[t] = 1 / sqrt(mean_h x[t, h]^2 + eps),   y[t, h] = x[t, h] r[t] weight[h]
+ *   x, y [T, H], weight [H], all dtype dt (F32 or BF16, rounded to nearest even)
+ *   rstd [T] float32 (out, may be NULL): r, for moe_pre_norm_bwd
+ * float32 arithmetic. Rows whose bytes are a multiple of 16, with 16-byte aligned pointers,
+ * go through 16-byte accesses; any other H and element alignment works, slower.
+ * Limits: 1 <= H <= 16384, eps > 0, T < 2^31; magnitudes below 2^63 (their squares are
+ * summed in float32; a row beyond that normalises to 0, one with an infinity to NaN there).
+ */
+moe_status moe_pre_norm(const void* x, const void* weight, moe_dtype dt, int64_t T, int H, float eps, void* y,
+                        float* rstd, void* stream);
+
+/*
+ * Backward of moe_pre_norm, joined with the residual path's gradient. With n = x r and
+ * a = dy weight:
+ *   dx[t, h]   = dx_in_scale dx_in[t, h] + r (a - n mean_h(a n))
+ *   dweight[h] = sum_t dy[t, h] n[t, h]                       (float32)
+ *   dy, x, dx [T, H], weight [H], dx_in [T, H] or NULL for 0, all dtype dt; dx may equal
+ *   dx_in or dy. rstd: of the forward. T = 0 writes dweight = 0.
+ * Column sums are added in a fixed order over runs of tokens (a function of T alone).
+ * workspace: moe_workspace_size(MOE_OP_NORM_BWD, desc with H, 0, T, 0, 0) bytes, 256-byte
+ * aligned. Limits as for moe_pre_norm.
+ */
+moe_status moe_pre_norm_bwd(const void* dy, const void* x, const void* weight, const float* rstd, const void* dx_in,
+                            float dx_in_scale, moe_dtype dt, int64_t T, int H, void* dx, float* dweight,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* What a gate value of moe_post_norm is shared by. */
+typedef enum {
+  MOE_GATE_NONE = 0,   /* no gate: 1 */
+  MOE_GATE_TOKEN = 1,  /* gate [T]: one value a token, all channels */
+  MOE_GATE_CHANNEL = 2 /* gate [ceil(T / gate_group), H]: one row for every gate_group consecutive tokens
+                          (gate_group >= T: a scale per channel; a sequence's length: a row per sequence) */
+} moe_gate;
+
+/*
+ * Norm after the expert block, fused with the combine of each token's rows, the block's
+ * gate, the scaled residual and the next block's norm:
+ *   c[t]   = sum_j y[row_id_map[t*k + j]]   (slot order, float32; -1 entries skipped), or
+ *            y[t] with row_id_map NULL and k = 1 (a block whose output is not permuted)
+ *   r[t]   = 1 / sqrt(mean_h c[t, h]^2 + eps)
+ *   out    = residual_scale x + gate (c r weight)
+ *   y_next = moe_pre_norm(out, next_weight)   (reads out as stored; only with next_weight)
+ * The routing weights are those folded into ScaledSwiGLU (the unweighted combine).
+ *   y [T*k, H] (or [T, H]), x, out [T, H], weight, next_weight [H], gate: all dtype dt
+ *   c [T, H] dtype dt and rstd [T] float32 (out, either may be NULL): for the backward; c
+ *     is the float32 sum rounded once, while out comes from the unrounded sum
+ *   y_next [T, H] dtype dt, rstd_next [T] float32 (out, may be NULL)
+ * out may equal x. Limits: 1 <= H <= 16384, 1 <= k <= 16, T * k < 2^31, eps > 0.
+ */
+moe_status moe_post_norm(const void* y, const int32_t* row_id_map, int k, const void* x, const void* weight,
+                         moe_gate gate_kind, const void* gate, int64_t gate_group, float residual_scale,
+                         const void* next_weight, moe_dtype dt, int64_t T, int H, float eps, void* out, void* c,
+                         float* rstd, void* y_next, float* rstd_next, void* stream);
+
+/*
+ * Backward of moe_post_norm (without its next norm, whose backward is moe_pre_norm_bwd on
+ * out). With n = c r and a = dout n:
+ *   dweight[h] = sum_t gate a                                  (float32)
+ *   dgate      = a weight, summed over what shares the gate value: [T] over h, or
+ *                [ceil(T / gate_group), H] over the group's tokens (float32, may be NULL)
+ *   d[t]       = r (dout gate weight - n mean_h(dout gate weight n))
+ *   dy[row_id_map[t*k + j]] = d[t] for every slot (rows of dropped slots and past them are
+ *   not written), or dy[t] = d[t] without row_id_map
+ * The residual's gradient is residual_scale dout: moe_pre_norm_bwd adds it (dx_in, dx_in_scale).
+ *   dout, c [T, H], weight [H], gate, dy: dtype dt; c, rstd of the forward
+ * T = 0 writes dweight = 0. Column sums in a fixed order.
+ * workspace: moe_workspace_size(MOE_OP_NORM_BWD, desc with H, R = 0, T, E = gate_kind,
+ * k = min(gate_group, T)) bytes, 256-byte aligned. Limits as for moe_post_norm.
+ */
+moe_status moe_post_norm_bwd(const void* dout, const void* c, const float* rstd, const void* weight,
+                             moe_gate gate_kind, const void* gate, int64_t gate_group, const int32_t* row_id_map,
+                             int k, moe_dtype dt, int64_t T, int H, void* dy, float* dweight, float* dgate,
+                             void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * MXFP8 block quantisation of a bf16 matrix along its rows. Source: Challenge 2
@@ -459,7 +580,10 @@ typedef enum {
   MOE_OP_MLP_FWD = 1,  /* desc and R used */
   MOE_OP_MLP_BWD = 2,  /* desc and R used */
   MOE_OP_GROUPED_GEMM = 3, /* moe_grouped_linear / moe_grouped_gate_up_swiglu; no argument used */
-  MOE_OP_ROUTER_BWD = 4    /* moe_router_bwd: desc (E, H) and T used */
+  MOE_OP_ROUTER_BWD = 4,   /* moe_router_bwd: desc (E, H) and T used */
+  MOE_OP_BALANCE_LOSS = 5, /* T and E used, R = seq_len; desc may be NULL */
+  MOE_OP_NORM_BWD = 6      /* moe_pre_norm_bwd / moe_post_norm_bwd: desc (H) and T used, E = gate kind,
+                              k = gate_group (at most T; only with MOE_GATE_CHANNEL) */
 } moe_op;
 
 /* Workspace bytes an operation needs (0 is possible). bytes is a [host] pointer. */
