@@ -17,17 +17,18 @@ import ctypes
 import torch
 
 from . import _lib
-from ._lib import MOE_BF16, MOE_F32, MOE_FP8, MOE_MXFP8, MlpDesc, MoeError, check, lib, ptr_table
+from ._lib import MOE_BF16, MOE_F32, MOE_FP8, MOE_MXFP4, MOE_MXFP8, MlpDesc, MoeError, check, lib, ptr_table
 
 __all__ = [
     "moe_route_topk", "moe_router_logits", "moe_route_topk_bwd", "moe_router_bwd", "moe_balance_loss",
     "moe_balance_loss_bwd", "moe_pre_norm", "moe_pre_norm_bwd", "moe_post_norm", "moe_post_norm_bwd",
-    "moe_permute", "moe_unpermute_combine", "mxfp8_quantize",
+    "moe_permute", "moe_unpermute_combine", "mxfp8_quantize", "mxfp4_quantize", "mxfp4_dequantize",
+    "moe_grouped_linear_mxfp4",
     "fp8_tensor_quantize", "mxfp8_quantize_colwise", "fp8_tensor_quantize_colwise", "mxfp8_pack_weight_bwd",
     "fp8_tensor_pack_weight_bwd", "mxfp8_quantize_weights", "fp8_tensor_quantize_weights",
     "moe_grouped_mlp_fwd", "moe_grouped_mlp_bwd", "moe_grouped_linear", "moe_grouped_gate_up_swiglu", "gemm_workspace",
     "workspace_size", "MoeError", "lib",
-    "MOE_F32", "MOE_BF16", "MOE_MXFP8", "MOE_FP8",
+    "MOE_F32", "MOE_BF16", "MOE_MXFP8", "MOE_FP8", "MOE_MXFP4",
 ]
 
 _DT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16, torch.uint8: MOE_MXFP8}
@@ -330,8 +331,10 @@ def moe_permute(x: torch.Tensor, topk_idx: torch.Tensor, topk_prob: torch.Tensor
                 x_scale: torch.Tensor | None = None, row_id_map: torch.Tensor | None = None):
     """Group the (token, slot) pairs by expert.
 
-    Returns a dict with x_perm [R, H], x_perm_scale (MXFP8 only), prob_perm [R],
+    Returns a dict with x_perm [R, H], x_perm_scale (MXFP8 and MXFP4 only), prob_perm [R],
     split_sizes [E], offsets [E+1], row_id_map [T*k], src_token [R].
+    uint8 codes come with x_scale, a byte per 32 values: MXFP8 where a byte of x is one
+    value, MXFP4 where it is two.
     With ``row_id_map`` given, only x is gathered with that map (topk_idx gives k).
     """
     _need_cuda(x, topk_idx, topk_prob, x_scale, row_id_map)
@@ -341,7 +344,9 @@ def moe_permute(x: torch.Tensor, topk_idx: torch.Tensor, topk_prob: torch.Tensor
     dt = _DT[x.dtype]
     dev = x.device
     x_perm = torch.empty((R, H), dtype=x.dtype, device=dev)
-    xps = torch.empty((R, H // 32), dtype=torch.uint8, device=dev) if dt == MOE_MXFP8 else None
+    if dt == MOE_MXFP8 and x_scale is not None and x_scale.shape[-1] * 16 == H:
+        dt, H = MOE_MXFP4, 2 * H   # two codes a byte
+    xps = torch.empty((R, H // 32), dtype=torch.uint8, device=dev) if dt in (MOE_MXFP8, MOE_MXFP4) else None
     if row_id_map is not None:
         check("moe_permute", lib().moe_permute(_p(x), _p(x_scale), dt, T, H, E, k, None, None, 1, _p(x_perm),
                                                _p(xps), None, None, None, _p(row_id_map), None, None, 0,
@@ -383,6 +388,33 @@ def mxfp8_quantize(x: torch.Tensor):
     scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=x.device)
     check("mxfp8_quantize", lib().mxfp8_quantize(_p(x2), rows, cols, _p(codes), _p(scales), _stream(x.device)))
     return codes.reshape(x.shape), scales.reshape(*x.shape[:-1], cols // 32)
+
+
+def mxfp4_quantize(x: torch.Tensor):
+    """bf16 [..., cols] -> (E2M1 codes uint8 [..., cols/2], two a byte, the even one in the low
+    nibble; E8M0 scales uint8 [..., cols/32])."""
+    _need("mxfp4_quantize", x)
+    if x.dtype != torch.bfloat16 or x.dim() < 1:
+        raise ValueError("mxfp4_quantize takes bfloat16")
+    cols = x.shape[-1]
+    rows = x.numel() // cols if cols else 0
+    codes = torch.empty((*x.shape[:-1], cols // 2), dtype=torch.uint8, device=x.device)
+    scales = torch.empty((*x.shape[:-1], cols // 32), dtype=torch.uint8, device=x.device)
+    _launch("mxfp4_quantize", x.device, _p(x), rows, cols, _p(codes), _p(scales))
+    return codes, scales
+
+
+def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor) -> torch.Tensor:
+    """MXFP4 codes [..., cols/2] and scales [..., cols/32] -> their values, bf16 [..., cols]."""
+    _need("mxfp4_dequantize", codes, scales)
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or scales.shape != (*codes.shape[:-1],
+                                                                                     codes.shape[-1] // 16):
+        raise ValueError("mxfp4_dequantize: codes must be uint8 [..., cols/2] and scales uint8 [..., cols/32]")
+    cols = 2 * codes.shape[-1]
+    rows = codes.numel() // codes.shape[-1] if cols else 0
+    out = torch.empty((*codes.shape[:-1], cols), dtype=torch.bfloat16, device=codes.device)
+    _launch("mxfp4_dequantize", codes.device, _p(codes), _p(scales), rows, cols, _p(out))
+    return out
 
 
 def fp8_tensor_quantize(x: torch.Tensor):
@@ -513,7 +545,104 @@ def _experts(w):
     return list(w)
 
 
-_COMPUTE = {"f32": MOE_F32, "bf16": MOE_BF16, "mxfp8": MOE_MXFP8, "fp8": MOE_FP8}
+def _weight_table(fn, w, dev):
+    """Per-expert weights, one tensor [E, ...] or a list -> (pointer table, what keeps it alive, E, shape, dtype).
+    One tensor's pointers are a stride apart, so a call does not touch E slices."""
+    if isinstance(w, torch.Tensor):
+        if w.device != dev or not w.is_contiguous():
+            raise ValueError(f"{fn}: weights must be contiguous and live on the rows' GPU")
+        table, keep = _lib.strided_table(w.data_ptr(), w.shape[0], w.stride(0) * w.element_size())
+        return table, keep, w.shape[0], tuple(w.shape[1:]), w.dtype
+    w = list(w)
+    for t in w:
+        if t.device != dev or not t.is_contiguous() or t.shape != w[0].shape or t.dtype != w[0].dtype:
+            raise ValueError(f"{fn}: the experts' weights must be contiguous, alike, and live on the rows' GPU")
+    table, keep = ptr_table([t.data_ptr() for t in w])
+    return table, keep, len(w), tuple(w[0].shape), w[0].dtype
+
+
+def _mxfp4_rows(fn, x, x_scale):
+    """(act dtype, K) of rows given in bf16 [R, K], or as MXFP4 codes [R, K/2] with scales [R, K/32]."""
+    if x.dim() != 2:
+        raise ValueError(f"{fn}: rows must be 2-D")
+    if x.dtype == torch.bfloat16:
+        return MOE_BF16, x.shape[1]
+    if x.dtype != torch.uint8 or x_scale is None or x_scale.dtype != torch.uint8 \
+            or x_scale.shape != (x.shape[0], x.shape[1] // 16):
+        raise ValueError(f"{fn}: rows must be bfloat16 [R, K], or MXFP4 codes uint8 [R, K/2] with scales uint8 [R, K/32]")
+    return MOE_MXFP4, 2 * x.shape[1]
+
+
+def _mxfp4_weight(fn, w, scale, N, K, dev, masters=False):
+    """Tables of E weights [N, K] given as MXFP4 codes [E, N, K/2] with scales [E, N, K/32] (or, where
+    masters are taken, bf16 [E, N, K]) -> (codes table, scale table, storage dtype, E, N, what to keep)."""
+    t, keep, E, shape, dtype = _weight_table(fn, w, dev)
+    if masters and dtype == torch.bfloat16:
+        if len(shape) != 2 or shape[1] != K or (N is not None and shape[0] != N):
+            raise ValueError(f"{fn}: weight shapes do not fit the rows")
+        return t, None, MOE_BF16, E, shape[0], keep
+    if scale is None:
+        raise ValueError(f"{fn}: MXFP4 weights need their scales")
+    ts, keep_s, Es, sshape, sdtype = _weight_table(fn, scale, dev)
+    if dtype != torch.uint8 or sdtype != torch.uint8 or Es != E or len(shape) != 2 or shape[1] * 2 != K \
+            or sshape != (shape[0], K // 32) or (N is not None and shape[0] != N):
+        raise ValueError(f"{fn}: MXFP4 weights must be uint8 codes [N, K/2] with uint8 scales [N, K/32] per expert")
+    return t, ts, MOE_MXFP4, E, shape[0], (keep, keep_s)
+
+
+def _check_offsets(fn, offsets, E):
+    if offsets.dtype != torch.int32 or offsets.numel() != E + 1:
+        raise ValueError(f"{fn}: offsets must be int32 [E + 1]")
+
+
+def moe_grouped_linear_mxfp4(x: torch.Tensor, w, w_scale, offsets: torch.Tensor, x_scale: torch.Tensor | None = None,
+                             out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """GroupedLinear with MXFP4 weights: y[r] = x[r] W_e^T for the rows of expert e, y [R, N] bf16.
+
+    x: bf16 [R, K] (quantised in the call) or MXFP4 codes uint8 [R, K/2] with x_scale [R, K/32];
+    w [E, N, K/2] codes with w_scale [E, N, K/32], or a list of per-expert tensors each."""
+    fn = "moe_grouped_linear_mxfp4"
+    _need(fn, x, offsets, x_scale, out, workspace)
+    act, K = _mxfp4_rows(fn, x, x_scale)
+    dev, R = x.device, x.shape[0]
+    t, ts, _, E, N, keep = _mxfp4_weight(fn, w, w_scale, None, K, dev)
+    _check_offsets(fn, offsets, E)
+    if out is None:
+        out = torch.empty((R, N), dtype=torch.bfloat16, device=dev)
+    elif out.dtype != torch.bfloat16 or out.shape != (R, N):
+        raise ValueError(f"{fn}: out must be bfloat16 [R, N]")
+    need = workspace_size(_lib.MOE_OP_LINEAR_MXFP4, MlpDesc(E, K, N, MOE_MXFP4, act, MOE_MXFP4, 0), R)
+    ws = workspace if workspace is not None and workspace.numel() >= need else _workspace(need, dev)
+    _launch(fn, dev, E, R, K, N, act, _p(x), _p(x_scale), t, ts, _p(offsets), _p(out), _p(ws), ws.numel())
+    del keep
+    return out
+
+
+def _mlp_fwd_mxfp4(x, w_gate_up, w_down, offsets, prob, save_for_bwd, x_scale, w1_scale, w2_scale, out, workspace):
+    fn = "moe_grouped_mlp_fwd"
+    _need(fn, x, offsets, prob, x_scale, out, workspace)
+    act, H = _mxfp4_rows(fn, x, x_scale)
+    dev, R = x.device, x.shape[0]
+    t1, s1, wt, E, twoI, keep1 = _mxfp4_weight(fn, w_gate_up, w1_scale, None, H, dev, masters=True)
+    I = twoI // 2
+    t2, s2, wt2, E2, _, keep2 = _mxfp4_weight(fn, w_down, w2_scale, H, I, dev, masters=True)
+    _check_offsets(fn, offsets, E)
+    if wt2 != wt or E2 != E or twoI % 2 or prob.dtype != torch.float32 or prob.numel() != R:
+        raise ValueError(f"{fn}: weights must share E and storage, prob_perm must be float32 [R]")
+    if out is None:
+        out = torch.empty((R, H), dtype=torch.bfloat16, device=dev)
+    elif out.dtype != torch.bfloat16 or out.shape != (R, H):
+        raise ValueError(f"{fn}: out must be bfloat16 [R, H]")
+    desc = MlpDesc(E, H, I, MOE_MXFP4, act, wt, int(save_for_bwd))
+    need = workspace_size(_lib.MOE_OP_MLP_FWD, desc, R)
+    ws = workspace if workspace is not None and workspace.numel() >= need else _workspace(need, dev)
+    _launch(fn, dev, ctypes.byref(desc), R, _p(x), _p(x_scale), t1, t2, s1, s2, _p(offsets), _p(prob), _p(out), None,
+            None, _p(ws), ws.numel())
+    del keep1, keep2
+    return out
+
+
+_COMPUTE = {"f32": MOE_F32, "bf16": MOE_BF16, "mxfp8": MOE_MXFP8, "fp8": MOE_FP8, "mxfp4": MOE_MXFP4}
 
 
 def moe_grouped_mlp_fwd(x_perm: torch.Tensor, w_gate_up, w_down, offsets: torch.Tensor, prob_perm: torch.Tensor,
@@ -522,11 +651,15 @@ def moe_grouped_mlp_fwd(x_perm: torch.Tensor, w_gate_up, w_down, offsets: torch.
                         workspace: torch.Tensor | None = None):
     """Grouped MLP forward on permuted rows. Returns y_perm, or (y_perm, z, h) with save_for_bwd.
 
-    compute: "f32", "bf16", "mxfp8" or "fp8" (per-tensor scales). For mxfp8 and fp8,
-    x_perm may be bf16 (quantised in the call) or uint8 codes with x_perm_scale; weights
-    may be bf16 master weights (quantised in the call) or uint8 codes with per-expert
-    scale tensors (fp8: one float32 scale tensor per expert weight).
+    compute: "f32", "bf16", "mxfp8", "fp8" (per-tensor scales) or "mxfp4" (forward only).
+    For mxfp8, fp8 and mxfp4, x_perm may be bf16 (quantised in the call) or uint8 codes with
+    x_perm_scale; weights may be bf16 master weights (quantised in the call) or uint8 codes
+    with per-expert scale tensors (fp8: one float32 scale tensor per expert weight; mxfp4:
+    codes [E, N, K/2] and scales [E, N, K/32] of mxfp4_quantize).
     """
+    if compute == "mxfp4":
+        return _mlp_fwd_mxfp4(x_perm, w_gate_up, w_down, offsets, prob_perm, save_for_bwd, x_perm_scale,
+                              w_gate_up_scale, w_down_scale, out, workspace)
     w1 = _experts(w_gate_up)
     w2 = _experts(w_down)
     E = len(w1)

@@ -12,9 +12,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmoe.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_LAUNCH = range(5)
-MOE_F32, MOE_BF16, MOE_MXFP8, MOE_FP8 = 0, 1, 2, 3
+MOE_F32, MOE_BF16, MOE_MXFP8, MOE_FP8, MOE_MXFP4 = 0, 1, 2, 3, 4
 MOE_OP_PERMUTE, MOE_OP_MLP_FWD, MOE_OP_MLP_BWD, MOE_OP_GROUPED_GEMM, MOE_OP_ROUTER_BWD = 0, 1, 2, 3, 4
-MOE_OP_BALANCE_LOSS, MOE_OP_NORM_BWD = 5, 6
+MOE_OP_BALANCE_LOSS, MOE_OP_NORM_BWD, MOE_OP_LINEAR_MXFP4 = 5, 6, 7
 MOE_GATE_NONE, MOE_GATE_TOKEN, MOE_GATE_CHANNEL = 0, 1, 2
 MOE_MAX_EXPERTS = 256
 
@@ -27,6 +27,7 @@ EXPORTS = (
     "moe_grouped_mlp_fwd", "moe_grouped_mlp_bwd", "moe_grouped_linear", "moe_grouped_gate_up_swiglu",
     "moe_balance_loss", "moe_balance_loss_bwd",
     "moe_pre_norm", "moe_pre_norm_bwd", "moe_post_norm", "moe_post_norm_bwd",
+    "mxfp4_quantize", "mxfp4_dequantize", "moe_grouped_linear_mxfp4",
     "moe_workspace_size",
     "moe_status_str", "moe_last_error",
 )
@@ -89,6 +90,9 @@ def _declare(lib):
         "moe_post_norm": [vp, vp, c_int, vp, vp, c_int, vp, i64, f32, vp, c_int, i64, c_int, f32, vp, vp, vp, vp, vp,
                           vp],
         "moe_post_norm_bwd": [vp, vp, vp, vp, c_int, vp, i64, vp, c_int, c_int, i64, c_int, vp, vp, vp, vp, sz, vp],
+        "mxfp4_quantize": [vp, i64, i64, vp, vp, vp],
+        "mxfp4_dequantize": [vp, vp, i64, i64, vp, vp],
+        "moe_grouped_linear_mxfp4": [c_int, i64, c_int, c_int, c_int, vp, vp, PP, PP, vp, vp, vp, sz, vp],
         "moe_workspace_size": [c_int, ctypes.POINTER(MlpDesc), i64, i64, c_int, c_int, ctypes.POINTER(sz)],
     }
     for name, args in sig.items():
@@ -116,6 +120,12 @@ def check(fn_name: str, status: int):
     if status != MOE_OK:
         L = lib()
         raise MoeError(fn_name, status, f"{L.moe_status_str(status).decode()}: {L.moe_last_error().decode()}")
+
+
+def strided_table(base, n, stride):
+    """ptr_table of n pointers, stride bytes apart."""
+    arr = (ctypes.c_void_p * n)(*range(base, base + n * stride, stride)) if stride else (ctypes.c_void_p * n)(*[base] * n)
+    return ctypes.cast(arr, PP), arr
 
 
 def ptr_table(ptrs):

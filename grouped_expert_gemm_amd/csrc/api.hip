@@ -4,6 +4,7 @@
 
 #include "common.h"
 #include "internal.h"
+#include "mxfp4.h"
 
 namespace moe {
 
@@ -94,6 +95,12 @@ extern "C" moe_status moe_workspace_size(moe_op op, const moe_mlp_desc* desc, in
       if (!desc || T < 0 || desc->H < 1 || E < MOE_GATE_NONE || E > MOE_GATE_CHANNEL || (E == MOE_GATE_CHANNEL && k < 1))
         return fail(MOE_ERR_INVALID_ARG, "moe_workspace_size(NORM_BWD): desc NULL or bad T/H, gate kind (E) or group (k)");
       *bytes = norm_bwd_workspace_bytes(T, desc->H, E, k);
+      return MOE_OK;
+    case MOE_OP_LINEAR_MXFP4:
+      if (!desc || R < 0 || desc->E < 1 || desc->E > MOE_MAX_EXPERTS || desc->H < 1 || desc->I < 1 ||
+          (desc->act != MOE_BF16 && desc->act != MOE_MXFP4))
+        return fail(MOE_ERR_INVALID_ARG, "moe_workspace_size(LINEAR_MXFP4): desc NULL or bad R/E/K/N/act");
+      *bytes = mx4::linear_workspace_bytes(desc->E, R, desc->H, desc->I, desc->act);
       return MOE_OK;
   }
   return fail(MOE_ERR_INVALID_ARG, "moe_workspace_size: unknown op");

@@ -10,6 +10,7 @@
 #include "gemm_f32.h"
 #include "gemm_mx.h"
 #include "internal.h"
+#include "mxfp4.h"
 
 namespace moe {
 
@@ -19,6 +20,7 @@ static bool is_act_ok(const moe_mlp_desc& d) {
     case MOE_BF16: return d.act == MOE_BF16 && d.wt == MOE_BF16;
     case MOE_MXFP8: return (d.act == MOE_BF16 || d.act == MOE_MXFP8) && (d.wt == MOE_BF16 || d.wt == MOE_MXFP8);
     case MOE_FP8: return (d.act == MOE_BF16 || d.act == MOE_FP8) && (d.wt == MOE_BF16 || d.wt == MOE_FP8);
+    case MOE_MXFP4: return (d.act == MOE_BF16 || d.act == MOE_MXFP4) && (d.wt == MOE_BF16 || d.wt == MOE_MXFP4);
   }
   return false;
 }
@@ -26,7 +28,8 @@ static bool is_act_ok(const moe_mlp_desc& d) {
 moe_status validate_desc(const moe_mlp_desc& d, bool backward) {
   if (d.E < 1 || d.E > MOE_MAX_EXPERTS) return fail(MOE_ERR_INVALID_ARG, "grouped MLP: E out of [1, 256]");
   if (d.H < 1 || d.I < 1) return fail(MOE_ERR_INVALID_ARG, "grouped MLP: H and I must be positive");
-  if (d.compute != MOE_F32 && d.compute != MOE_BF16 && d.compute != MOE_MXFP8 && d.compute != MOE_FP8)
+  if (d.compute != MOE_F32 && d.compute != MOE_BF16 && d.compute != MOE_MXFP8 && d.compute != MOE_FP8 &&
+      d.compute != MOE_MXFP4)
     return fail(MOE_ERR_INVALID_ARG, "grouped MLP: bad compute dtype");
   if (!is_act_ok(d)) return fail(MOE_ERR_INVALID_ARG, "grouped MLP: act/wt storage does not match compute dtype");
   if ((int64_t)d.H * d.I * 2 > 0x7FFFFFFFLL)
@@ -36,6 +39,12 @@ moe_status validate_desc(const moe_mlp_desc& d, bool backward) {
       return fail(MOE_ERR_UNSUPPORTED, "grouped MLP: bf16/fp8 kernels need H % 256 == 0 and I % 128 == 0");
     if (backward && d.I % 256 != 0)
       return fail(MOE_ERR_UNSUPPORTED, "grouped MLP backward: bf16 kernels need I % 256 == 0");
+  }
+  if (d.compute == MOE_MXFP4) {
+    if (backward || d.save_for_bwd)
+      return fail(MOE_ERR_UNSUPPORTED, "grouped MLP: MXFP4 has a forward only (save_for_bwd must be 0)");
+    const moe_status st = mx4::check_shape(d.E, d.H, d.I, "grouped MLP");
+    if (st != MOE_OK) return st;
   }
   if (backward && d.compute == MOE_FP8 && d.act != MOE_BF16)
     return fail(MOE_ERR_INVALID_ARG, "grouped MLP backward: per-tensor FP8 takes bf16 activations (and bf16 master "
@@ -62,6 +71,7 @@ size_t mlp_fwd_workspace_bytes(const moe_mlp_desc& d, int64_t R) {
       return b;
     }
     case MOE_FP8: return mx::fp8_tensor_workspace_bytes(d, R);
+    case MOE_MXFP4: return mx4::mlp_workspace_bytes(d, R);
   }
   return 0;
 }
@@ -224,6 +234,12 @@ extern "C" moe_status moe_grouped_mlp_fwd(const moe_mlp_desc* desc, int64_t R, c
   }
   if (d.compute == MOE_FP8 && d.act == MOE_FP8 && (!x_perm_scale || !aligned(x_perm_scale, 4)))
     return fail(MOE_ERR_INVALID_ARG, "moe_grouped_mlp_fwd: FP8 activations need a 4-byte aligned x_perm_scale");
+  if (d.compute == MOE_MXFP4 && d.wt == MOE_MXFP4) {
+    if ((st = check_table((const void* const*)w_gate_up_scale, d.E, 8, "moe_grouped_mlp_fwd(w_gate_up_scale)")) != MOE_OK) return st;
+    if ((st = check_table((const void* const*)w_down_scale, d.E, 8, "moe_grouped_mlp_fwd(w_down_scale)")) != MOE_OK) return st;
+  }
+  if (d.compute == MOE_MXFP4 && d.act == MOE_MXFP4 && (!x_perm_scale || !aligned(x_perm_scale, 8)))
+    return fail(MOE_ERR_INVALID_ARG, "moe_grouped_mlp_fwd: MXFP4 activations need an 8-byte aligned x_perm_scale");
   const size_t need = mlp_fwd_workspace_bytes(d, R);
   if (workspace_bytes < need) return fail(MOE_ERR_WORKSPACE, "moe_grouped_mlp_fwd: workspace too small");
   if (need > 0 && (!workspace || !aligned(workspace, 256)))
@@ -243,6 +259,9 @@ extern "C" moe_status moe_grouped_mlp_fwd(const moe_mlp_desc* desc, int64_t R, c
                                   (uint8_t*)workspace, s, d.save_for_bwd ? z_save : nullptr,
                                   d.save_for_bwd ? h_save : nullptr);
   }
+  if (d.compute == MOE_MXFP4)
+    return mx4::forward(d, R, x_perm, x_perm_scale, w_gate_up, w_down, w_gate_up_scale, w_down_scale, offsets, prob_perm,
+                        y_perm, (uint8_t*)workspace, s);
   if (d.compute == MOE_MXFP8) {
     return mx::forward(d, R, x_perm, x_perm_scale, w_gate_up, w_down, w_gate_up_scale, w_down_scale, offsets,
                        prob_perm, y_perm, (uint8_t*)workspace, s, d.save_for_bwd ? z_save : nullptr,

@@ -1,0 +1,54 @@
+// MXFP4 (E2M1 codes, one E8M0 scale per 32 values): quantisation helpers shared by the
+// quantiser and the GEMM epilogues, and the grouped MLP's host entry.
+#pragma once
+
+#include "common.h"
+
+namespace moe {
+namespace mx4 {
+
+constexpr uint32_t kNotFinite = 0x7F800000u;  // magnitude bits of infinity; above: NaN
+
+// E8M0 byte of a block whose largest magnitude has the float32 bits u: s + 127 with s the
+// smallest exponent that fits the maximum under 6 * 2^s, in [-127, 127]; 0 for an all-zero
+// block; 255 (E8M0's NaN) for a block that holds an infinity or a NaN.
+__device__ __forceinline__ int scale_byte(uint32_t u) {
+  if (u >= kNotFinite) return 255;
+  if (u == 0) return 0;
+  int e = (int)(u >> 23);
+  uint32_t m = u & 0x7FFFFFu;
+  if (e == 0) {  // subnormal: normalise
+    const int sh = __clz(m) - 8;
+    m = (m << sh) & 0x7FFFFFu;
+    e = 1 - sh;
+  }
+  // 6 = 1.5 * 2^2: the byte e - 2 if the significand is at most 1.5, else e - 1
+  const int b = m <= 0x400000u ? e - 2 : e - 1;
+  return b < 0 ? 0 : (b > 254 ? 254 : b);
+}
+
+// Eight E2M1 codes (value 0 in the low nibble) of f / 2^(byte - 127), |f| <= 6 * 2^(byte - 127):
+// ldexp is exact (or far below the smallest code's half), the conversion rounds to nearest,
+// ties to the even code, and keeps the sign of zero.
+__device__ __forceinline__ uint32_t pack8(const float* f, int byte) {
+  const int s = 127 - byte;
+  uint32_t w = 0;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, ldexpf(f[0], s), ldexpf(f[1], s), 1.f, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, ldexpf(f[2], s), ldexpf(f[3], s), 1.f, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, ldexpf(f[4], s), ldexpf(f[5], s), 1.f, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, ldexpf(f[6], s), ldexpf(f[7], s), 1.f, 3);
+  return byte == 255 ? 0u : w;
+}
+
+moe_status quantize(const void* in_bf16, int64_t rows, int64_t cols, uint8_t* e2m1, uint8_t* e8m0, hipStream_t s);
+
+moe_status check_shape(int E, int K, int N, const char* what);
+size_t mlp_workspace_bytes(const moe_mlp_desc& d, int64_t R);
+size_t linear_workspace_bytes(int E, int64_t R, int K, int N, moe_dtype act);
+moe_status forward(const moe_mlp_desc& d, int64_t R, const void* x_perm, const uint8_t* x_perm_scale,
+                   const void* const* w_gate_up, const void* const* w_down, const uint8_t* const* w_gate_up_scale,
+                   const uint8_t* const* w_down_scale, const int32_t* offsets, const float* prob_perm, void* y_perm,
+                   uint8_t* ws, hipStream_t s);
+
+}  // namespace mx4
+}  // namespace moe

@@ -1,0 +1,411 @@
+// MXFP4: quantisation, and the grouped GEMMs of experts whose weights are served in it.
+//
+// Elements are OCP E2M1 (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives), two a byte, the
+// even one in the low nibble; 32 consecutive values share one E8M0 scale 2^s, s the
+// smallest with max|block| <= 6 * 2^s (the rule mxfp8_quantize uses with 448).
+//
+// GEMM operands: gfx950's scaled MFMA takes 16 bytes a lane, 32 consecutive values of one
+// row and their block's scale. In v_mfma_scale_f32_16x16x128 lane l holds row l % 16 and
+// block l / 16 of the 128 values.
+//
+// grouped_gemm_rows_kernel: y = x W^T for few rows an expert, bound by the weights' bytes.
+// The weights go straight from memory to the MFMA, without LDS: a workgroup takes 32 output
+// columns (32 gate and 32 up rows with SwiGLU) of one expert, its four wavefronts every
+// fourth 256-value unit of K, and their partial products are added through LDS in wavefront
+// order. The next unit's weights are in flight while one is multiplied.
+#include <cstring>
+
+#include "common.h"
+#include "gemm_common.h"
+#include "internal.h"
+#include "mxfp4.h"
+
+namespace moe {
+namespace mx4 {
+
+using gemm::silu_f;
+
+constexpr int kMaxE = 128;  // experts per call (two pointer tables in the kernel arguments)
+constexpr int kUnit = 256;  // K values of one unit
+
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
+typedef int i32x8_t __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ i32x8_t wide(uint4 v) { return i32x8_t{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0}; }
+
+// ---------------------------------------------------------------------------
+// quantisation: HBM-bound, 2 bytes in, 17/32 out a value. Four lanes own a block (16 bytes
+// of bf16 each), whose largest magnitude two xor-shuffles find.
+// ---------------------------------------------------------------------------
+
+__global__ __launch_bounds__(256) void quantize_kernel(const uint4* __restrict__ in, int64_t nblocks,
+                                                       uint32_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  const int64_t total = nblocks * 4, stride = (int64_t)gridDim.x * blockDim.x;
+  const int64_t padded = (total + 63) / 64 * 64;  // whole wavefronts: every lane reaches the shuffles
+  for (int64_t q = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; q < padded; q += stride) {
+    const bool live = q < total;
+    const uint4 v = live ? in[q] : make_uint4(0, 0, 0, 0);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    float f[8];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+      top = max(top, max((w[i] << 16) & 0x7FFFFFFFu, w[i] & 0x7FFF0000u));
+    }
+    top = max(top, (uint32_t)__shfl_xor((int)top, 1));
+    top = max(top, (uint32_t)__shfl_xor((int)top, 2));
+    const int b = scale_byte(top);
+    if (live) {
+      codes[q] = pack8(f, b);
+      if ((q & 3) == 0) scales[q >> 2] = (uint8_t)b;
+    }
+  }
+}
+
+moe_status quantize(const void* in_bf16, int64_t rows, int64_t cols, uint8_t* e2m1, uint8_t* e8m0, hipStream_t s) {
+  const int64_t nblocks = rows * (cols / 32);
+  if (nblocks == 0) return MOE_OK;
+  int64_t grid = (nblocks * 4 + 255) / 256;
+  const int64_t most = (int64_t)num_cus() * 16;
+  if (grid > most) grid = most;
+  hipLaunchKernelGGL(quantize_kernel, dim3((unsigned)grid), dim3(256), 0, s, (const uint4*)in_bf16, nblocks,
+                     (uint32_t*)e2m1, e8m0);
+  return check_launch("mxfp4_quantize");
+}
+
+__global__ __launch_bounds__(256) void dequantize_kernel(const uint32_t* __restrict__ codes,
+                                                         const uint8_t* __restrict__ scales, int64_t words,
+                                                         uint4* __restrict__ out) {
+  const int64_t stride = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t q = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; q < words; q += stride) {
+    const uint32_t w = codes[q];
+    const int b = scales[q >> 2], s = b - 127;
+    auto pair = [&](auto i) -> uint32_t {
+      const auto v = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.f, decltype(i)::value);
+      const float nan = __uint_as_float(0x7FC00000u);
+      return b == 255 ? pack_bf16x2(nan, nan) : pack_bf16x2(ldexpf(v[0], s), ldexpf(v[1], s));
+    };
+    out[q] = make_uint4(pair(std::integral_constant<int, 0>{}), pair(std::integral_constant<int, 1>{}),
+                        pair(std::integral_constant<int, 2>{}), pair(std::integral_constant<int, 3>{}));
+  }
+}
+
+// ---------------------------------------------------------------------------
+// grouped GEMM, few rows an expert
+// ---------------------------------------------------------------------------
+
+enum { EP_STORE = 0, EP_SWIGLU = 1 };
+
+struct Params {
+  const uint8_t* tab[kMaxE];    // per-expert weight codes [N][K / 2]
+  const uint8_t* tab_s[kMaxE];  // per-expert weight scales [N][K / 32]
+  const uint8_t* q;             // row codes [R][K / 2]
+  const uint8_t* q_s;           // row scales [R][K / 32]
+  void* c;                      // STORE: bf16 [R][N]; SWIGLU: h codes [R][I / 2]
+  uint8_t* c_s;                 // SWIGLU: h scales [R][I / 32]
+  const int32_t* offsets;
+  const float* prob;
+  int64_t R;
+  int K, N, E, I;
+};
+
+// the rank-th expert that has rows, or -1: its rows are [beg, end). Offsets are kept inside
+// [0, R]; a wavefront looks at 64 experts at a time.
+__device__ __forceinline__ int find_expert(const int32_t* offsets, int E, int R, int rank, int& beg, int& end) {
+  const int lane = threadIdx.x & 63;
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    const int e = e0 + lane;
+    int b = 0, n = 0;
+    if (e < E) {
+      b = min(max(offsets[e], 0), R);
+      n = min(max(offsets[e + 1], b), R);
+    }
+    const uint64_t some = __ballot(n > b);
+    const int cnt = __popcll(some);
+    if (rank < cnt) {
+      const uint64_t below = some & ((1ull << lane) - 1);
+      const uint64_t hit = __ballot(n > b && __popcll(below) == rank);
+      const int src = __ffsll((unsigned long long)hit) - 1;
+      beg = __builtin_amdgcn_readfirstlane(__shfl(b, src));
+      end = __builtin_amdgcn_readfirstlane(__shfl(n, src));
+      return __builtin_amdgcn_readfirstlane(e0 + src);
+    }
+    rank -= cnt;
+  }
+  return -1;
+}
+
+template <int EP>
+__global__ __launch_bounds__(256) void grouped_gemm_rows_kernel(const Params prm) {
+  constexpr int NA = EP == EP_SWIGLU ? 4 : 2;   // 16-row weight tiles
+  constexpr int RT = 4;                         // 16-row tiles of x at a time
+  constexpr int LD = NA * 16 + 4;
+  __shared__ __attribute__((aligned(16))) float part[4][16][LD];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int l16 = lane & 15, g = lane >> 4;
+  int beg, end;
+  const int e = find_expert(prm.offsets, prm.E, (int)prm.R, blockIdx.y, beg, end);
+  if (e < 0) return;
+  const int K = prm.K, units = K / kUnit;
+  const int64_t ldc = K / 2, lds = K / 32;
+  const uint8_t* wc[NA];
+  const uint8_t* ws[NA];
+#pragma unroll
+  for (int a = 0; a < NA; ++a) {
+    const int n = EP == EP_SWIGLU ? (a >= 2 ? prm.I : 0) + blockIdx.x * 32 + (a & 1) * 16 + l16
+                                  : blockIdx.x * 32 + a * 16 + l16;
+    wc[a] = prm.tab[e] + (int64_t)n * ldc + g * 16;
+    ws[a] = prm.tab_s[e] + (int64_t)n * lds;
+  }
+  for (int r0 = beg; r0 < end; r0 += RT * 16) {
+    const int nrt = min(RT, (end - r0 + 15) / 16);
+    const uint8_t* xc[RT];
+    const uint8_t* xs[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      const int row = min(r0 + r * 16 + l16, end - 1);  // past the expert: any valid row, discarded
+      xc[r] = prm.q + row * ldc + g * 16;
+      xs[r] = prm.q_s + row * lds;
+    }
+    typedef float f4 __attribute__((ext_vector_type(4)));
+    f4 acc[NA][RT];
+#pragma unroll
+    for (int a = 0; a < NA; ++a)
+#pragma unroll
+      for (int r = 0; r < RT; ++r) acc[a][r] = f4{0.f, 0.f, 0.f, 0.f};
+    uint4 w[2][NA][2];
+    uint2 sw[2][NA];
+    auto load = [&](int u, uint4 (&c)[NA][2], uint2 (&s)[NA]) {
+#pragma unroll
+      for (int a = 0; a < NA; ++a) {
+        c[a][0] = *reinterpret_cast<const uint4*>(wc[a] + u * 128);
+        c[a][1] = *reinterpret_cast<const uint4*>(wc[a] + u * 128 + 64);
+        s[a] = *reinterpret_cast<const uint2*>(ws[a] + u * 8);
+      }
+    };
+    auto step = [&](int u, const uint4 (&c)[NA][2], const uint2 (&s)[NA]) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        if (r >= nrt) break;
+        const uint4 x0 = *reinterpret_cast<const uint4*>(xc[r] + u * 128);
+        const uint4 x1 = *reinterpret_cast<const uint4*>(xc[r] + u * 128 + 64);
+        const uint2 sx = *reinterpret_cast<const uint2*>(xs[r] + u * 8);
+#pragma unroll
+        for (int a = 0; a < NA; ++a) {
+          acc[a][r] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(c[a][0]), wide(x0), acc[a][r], 4, 4, 0,
+                                                                        (int)(s[a].x >> (8 * g)), 0, (int)(sx.x >> (8 * g)));
+          acc[a][r] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(c[a][1]), wide(x1), acc[a][r], 4, 4, 0,
+                                                                        (int)(s[a].y >> (8 * g)), 0, (int)(sx.y >> (8 * g)));
+        }
+      }
+    };
+    if (wave < units) load(wave, w[0], sw[0]);
+    for (int u = wave; u < units; u += 8) {
+      if (u + 4 < units) load(u + 4, w[1], sw[1]);
+      step(u, w[0], sw[0]);
+      if (u + 8 < units) load(u + 8, w[0], sw[0]);
+      if (u + 4 < units) step(u + 4, w[1], sw[1]);
+    }
+    // each 16-row tile: the four wavefronts' partial products, added in order
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      if (r >= nrt) break;
+#pragma unroll
+      for (int a = 0; a < NA; ++a) *reinterpret_cast<f4*>(&part[wave][l16][a * 16 + 4 * g]) = acc[a][r];
+      __syncthreads();
+      const int row = tid >> 4, cp = (tid & 15) * 2;
+      const int64_t mg = r0 + r * 16 + row;
+      auto sum = [&](int col) {
+        return (part[0][row][col] + part[1][row][col]) + (part[2][row][col] + part[3][row][col]);
+      };
+      const float v0 = sum(cp), v1 = sum(cp + 1);
+      if constexpr (EP == EP_STORE) {
+        if (mg < end)
+          *reinterpret_cast<uint32_t*>((bf16_t*)prm.c + mg * prm.N + blockIdx.x * 32 + cp) = pack_bf16x2(v0, v1);
+      } else {
+        const float p = prm.prob[mg < end ? mg : end - 1];
+        const float h0 = silu_f(v0) * sum(32 + cp) * p, h1 = silu_f(v1) * sum(32 + cp + 1) * p;
+        uint32_t top = max(__float_as_uint(h0) & 0x7FFFFFFFu, __float_as_uint(h1) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int m = 8; m >= 1; m >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m));
+        const int b = scale_byte(top);
+        if (mg < end) {
+          const uint32_t code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, ldexpf(h0, 127 - b), ldexpf(h1, 127 - b), 1.f, 0);
+          ((uint8_t*)prm.c)[mg * (prm.I / 2) + blockIdx.x * 16 + (tid & 15)] = b == 255 ? 0 : (uint8_t)code;
+          if ((tid & 15) == 0) prm.c_s[mg * (prm.I / 32) + blockIdx.x] = (uint8_t)b;
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+
+static size_t a256(size_t x) { return align_up(x, 256); }
+
+moe_status check_shape(int E, int K, int N, const char* what) {
+  if (E > kMaxE) return fail(MOE_ERR_UNSUPPORTED, std::string(what) + ": MXFP4 supports at most 128 experts");
+  if (K % 256 != 0 || N % 256 != 0)
+    return fail(MOE_ERR_UNSUPPORTED, std::string(what) + ": MXFP4 kernels need every GEMM size to be a multiple of 256");
+  return MOE_OK;
+}
+
+static void fill(Params& p, int E, int64_t R, int K, int N, const uint8_t* x, const uint8_t* xs, const uint8_t* const* w,
+                 const uint8_t* const* ws, const int32_t* offsets, void* c) {
+  std::memset(&p, 0, sizeof(p));
+  for (int e = 0; e < E; ++e) {
+    p.tab[e] = w[e];
+    p.tab_s[e] = ws[e];
+  }
+  p.q = x, p.q_s = xs, p.c = c, p.offsets = offsets, p.R = R, p.K = K, p.N = N, p.E = E;
+}
+
+static moe_status gate_up(Params& p, int I, const float* prob, uint8_t* hs, hipStream_t s) {
+  p.I = I, p.prob = prob, p.c_s = hs;
+  const int64_t experts = p.R < p.E ? p.R : p.E;
+  hipLaunchKernelGGL(grouped_gemm_rows_kernel<EP_SWIGLU>, dim3((unsigned)(I / 32), (unsigned)experts), dim3(256), 0, s, p);
+  return check_launch("MXFP4 gate_up + ScaledSwiGLU");
+}
+
+static moe_status linear(Params& p, hipStream_t s) {
+  const int64_t experts = p.R < p.E ? p.R : p.E;
+  hipLaunchKernelGGL(grouped_gemm_rows_kernel<EP_STORE>, dim3((unsigned)(p.N / 32), (unsigned)experts), dim3(256), 0, s, p);
+  return check_launch("MXFP4 grouped linear");
+}
+
+size_t mlp_workspace_bytes(const moe_mlp_desc& d, int64_t R) {
+  const size_t I = d.I, H = d.H, E = d.E;
+  size_t b = a256(R * I / 2) + a256(R * I / 32);
+  if (d.act == MOE_BF16) b += a256(R * H / 2) + a256(R * H / 32);
+  if (d.wt == MOE_BF16) b += E * (a256(I * H) + a256(2 * I * H / 32) + a256(H * I / 2) + a256(H * I / 32));
+  return b;
+}
+
+size_t linear_workspace_bytes(int E, int64_t R, int K, int N, moe_dtype act) {
+  return act == MOE_BF16 ? a256((size_t)R * K / 2) + a256((size_t)R * K / 32) : 0;
+}
+
+// workspace: h's codes and scales, x's if given in bf16, the weights' if given in bf16
+moe_status forward(const moe_mlp_desc& d, int64_t R, const void* x_perm, const uint8_t* x_perm_scale,
+                   const void* const* w_gate_up, const void* const* w_down, const uint8_t* const* w_gate_up_scale,
+                   const uint8_t* const* w_down_scale, const int32_t* offsets, const float* prob_perm, void* y_perm,
+                   uint8_t* ws, hipStream_t s) {
+  const int E = d.E, H = d.H, I = d.I;
+  moe_status st;
+  auto take = [&](size_t n) {
+    uint8_t* p = ws;
+    ws += a256(n);
+    return p;
+  };
+  uint8_t* hq = take((size_t)R * I / 2);
+  uint8_t* hs = take((size_t)R * I / 32);
+  const uint8_t* xq = (const uint8_t*)x_perm;
+  const uint8_t* xs = x_perm_scale;
+  if (d.act == MOE_BF16) {
+    uint8_t* a = take((size_t)R * H / 2);
+    uint8_t* b = take((size_t)R * H / 32);
+    if ((st = quantize(x_perm, R, H, a, b, s)) != MOE_OK) return st;
+    xq = a, xs = b;
+  }
+  const uint8_t* w1[kMaxE];
+  const uint8_t* w2[kMaxE];
+  const uint8_t* s1[kMaxE];
+  const uint8_t* s2[kMaxE];
+  for (int e = 0; e < E; ++e) {
+    if (d.wt == MOE_BF16) {
+      uint8_t* a = take((size_t)I * H);
+      uint8_t* b = take((size_t)2 * I * H / 32);
+      uint8_t* a2 = take((size_t)H * I / 2);
+      uint8_t* b2 = take((size_t)H * I / 32);
+      if ((st = quantize(w_gate_up[e], 2 * (int64_t)I, H, a, b, s)) != MOE_OK) return st;
+      if ((st = quantize(w_down[e], H, I, a2, b2, s)) != MOE_OK) return st;
+      w1[e] = a, s1[e] = b, w2[e] = a2, s2[e] = b2;
+    } else {
+      w1[e] = (const uint8_t*)w_gate_up[e], s1[e] = w_gate_up_scale[e];
+      w2[e] = (const uint8_t*)w_down[e], s2[e] = w_down_scale[e];
+    }
+  }
+  Params p;
+  fill(p, E, R, H, 2 * I, xq, xs, w1, s1, offsets, hq);
+  if ((st = gate_up(p, I, prob_perm, hs, s)) != MOE_OK) return st;
+  fill(p, E, R, I, H, hq, hs, w2, s2, offsets, y_perm);
+  return linear(p, s);
+}
+
+}  // namespace mx4
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status mxfp4_quantize(const void* in_bf16, int64_t rows, int64_t cols, uint8_t* e2m1, uint8_t* e8m0,
+                                     void* stream) {
+  if (rows < 0 || cols < 0) return fail(MOE_ERR_INVALID_ARG, "mxfp4_quantize: negative size");
+  if (cols % 32 != 0) return fail(MOE_ERR_INVALID_ARG, "mxfp4_quantize: cols % 32 != 0");
+  if (rows == 0 || cols == 0) return MOE_OK;
+  if (!in_bf16 || !e2m1 || !e8m0) return fail(MOE_ERR_INVALID_ARG, "mxfp4_quantize: NULL pointer");
+  if (!aligned(in_bf16, 16) || !aligned(e2m1, 4))
+    return fail(MOE_ERR_INVALID_ARG, "mxfp4_quantize: input must be 16-byte and codes 4-byte aligned");
+  return mx4::quantize(in_bf16, rows, cols, e2m1, e8m0, as_stream(stream));
+}
+
+extern "C" moe_status mxfp4_dequantize(const uint8_t* e2m1, const uint8_t* e8m0, int64_t rows, int64_t cols,
+                                       void* out_bf16, void* stream) {
+  if (rows < 0 || cols < 0) return fail(MOE_ERR_INVALID_ARG, "mxfp4_dequantize: negative size");
+  if (cols % 32 != 0) return fail(MOE_ERR_INVALID_ARG, "mxfp4_dequantize: cols % 32 != 0");
+  if (rows == 0 || cols == 0) return MOE_OK;
+  if (!e2m1 || !e8m0 || !out_bf16) return fail(MOE_ERR_INVALID_ARG, "mxfp4_dequantize: NULL pointer");
+  if (!aligned(out_bf16, 16) || !aligned(e2m1, 4))
+    return fail(MOE_ERR_INVALID_ARG, "mxfp4_dequantize: output must be 16-byte and codes 4-byte aligned");
+  const int64_t words = rows * (cols / 8);
+  int64_t grid = (words + 255) / 256;
+  const int64_t most = (int64_t)num_cus() * 16;
+  if (grid > most) grid = most;
+  hipLaunchKernelGGL(mx4::dequantize_kernel, dim3((unsigned)grid), dim3(256), 0, as_stream(stream),
+                     (const uint32_t*)e2m1, e8m0, words, (uint4*)out_bf16);
+  return check_launch("mxfp4_dequantize");
+}
+
+extern "C" moe_status moe_grouped_linear_mxfp4(int E, int64_t R, int K, int N, moe_dtype act, const void* x,
+                                               const uint8_t* x_scale, const uint8_t* const* w,
+                                               const uint8_t* const* w_scale, const int32_t* offsets, void* y,
+                                               void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_grouped_linear_mxfp4";
+  const std::string f(fn);
+  if (E < 1 || E > MOE_MAX_EXPERTS) return fail(MOE_ERR_INVALID_ARG, f + ": E out of [1, 256]");
+  if (R < 0 || R > 0x7FFFFFFF || K < 1 || N < 1) return fail(MOE_ERR_INVALID_ARG, f + ": bad R/K/N");
+  if (act != MOE_BF16 && act != MOE_MXFP4) return fail(MOE_ERR_INVALID_ARG, f + ": act must be BF16 or MXFP4");
+  moe_status st = mx4::check_shape(E, K, N, fn);
+  if (st != MOE_OK) return st;
+  if ((int64_t)N * K > 0x7FFFFFFFLL) return fail(MOE_ERR_UNSUPPORTED, f + ": weight exceeds 2^31 elements");
+  if (R == 0) return MOE_OK;
+  if (!x || !y || !offsets || !w || !w_scale) return fail(MOE_ERR_INVALID_ARG, f + ": NULL pointer");
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(offsets, 4)) return fail(MOE_ERR_INVALID_ARG, f + ": misaligned tensor");
+  if (act == MOE_MXFP4 && (!x_scale || !aligned(x_scale, 8)))
+    return fail(MOE_ERR_INVALID_ARG, f + ": MXFP4 rows need an 8-byte aligned x_scale");
+  for (int e = 0; e < E; ++e) {
+    if (!w[e] || !w_scale[e]) return fail(MOE_ERR_INVALID_ARG, f + ": NULL pointer for expert " + std::to_string(e));
+    if (!aligned(w[e], 16) || !aligned(w_scale[e], 8))
+      return fail(MOE_ERR_INVALID_ARG, f + ": weights must be 16-byte and their scales 8-byte aligned");
+  }
+  const size_t need = mx4::linear_workspace_bytes(E, R, K, N, act);
+  if (workspace_bytes < need) return fail(MOE_ERR_WORKSPACE, f + ": workspace too small");
+  if (need > 0 && (!workspace || !aligned(workspace, 256)))
+    return fail(MOE_ERR_INVALID_ARG, f + ": workspace NULL or not 256-byte aligned");
+  const hipStream_t s = as_stream(stream);
+  const uint8_t* xq = (const uint8_t*)x;
+  const uint8_t* xs = x_scale;
+  if (act == MOE_BF16) {
+    uint8_t* a = (uint8_t*)workspace;
+    uint8_t* b = a + align_up((size_t)R * K / 2, 256);
+    if ((st = mx4::quantize(x, R, K, a, b, s)) != MOE_OK) return st;
+    xq = a, xs = b;
+  }
+  mx4::Params p;
+  mx4::fill(p, E, R, K, N, xq, xs, w, w_scale, offsets, y);
+  return mx4::linear(p, s);
+}

@@ -396,9 +396,9 @@ extern "C" moe_status moe_permute(const void* x, const uint8_t* x_scale, moe_dty
   if (E < 1 || E > MOE_MAX_EXPERTS) return fail(MOE_ERR_INVALID_ARG, "moe_permute: E out of [1, 256]");
   if (k < 1 || k > E) return fail(MOE_ERR_INVALID_ARG, "moe_permute: k out of [1, E]");
   if (k > kMaxK) return fail(MOE_ERR_UNSUPPORTED, "moe_permute: k > 16");
-  if (dt != MOE_F32 && dt != MOE_BF16 && dt != MOE_MXFP8)
-    return fail(MOE_ERR_INVALID_ARG, "moe_permute: bad dtype");
-  if (dt == MOE_MXFP8 && H % 32 != 0) return fail(MOE_ERR_INVALID_ARG, "moe_permute: MXFP8 needs H % 32 == 0");
+  const bool mx = dt == MOE_MXFP8 || dt == MOE_MXFP4;  // codes with a scale per 32 values
+  if (dt != MOE_F32 && dt != MOE_BF16 && !mx) return fail(MOE_ERR_INVALID_ARG, "moe_permute: bad dtype");
+  if (mx && H % 32 != 0) return fail(MOE_ERR_INVALID_ARG, "moe_permute: MXFP8 and MXFP4 need H % 32 == 0");
   if (T * (int64_t)k > 0x7FFFFFFF) return fail(MOE_ERR_UNSUPPORTED, "moe_permute: T*k exceeds int32 rows");
   const hipStream_t s = as_stream(stream);
   if (reuse_map) {
@@ -410,11 +410,11 @@ extern "C" moe_status moe_permute(const void* x, const uint8_t* x_scale, moe_dty
       return fail(MOE_ERR_INVALID_ARG, "moe_permute: NULL pointer");
     if (prob_perm && !topk_prob) return fail(MOE_ERR_INVALID_ARG, "moe_permute: prob_perm needs topk_prob");
   }
-  if (dt == MOE_MXFP8 && T > 0 && (!x_scale || !x_perm_scale))
-    return fail(MOE_ERR_INVALID_ARG, "moe_permute: MXFP8 needs x_scale and x_perm_scale");
+  if (mx && T > 0 && (!x_scale || !x_perm_scale))
+    return fail(MOE_ERR_INVALID_ARG, "moe_permute: MXFP8 and MXFP4 need x_scale and x_perm_scale");
   const size_t esz = dt == MOE_F32 ? 4 : dt == MOE_BF16 ? 2 : 1;
-  const int64_t row_bytes = (int64_t)H * esz;
-  const int64_t srow_bytes = dt == MOE_MXFP8 ? H / 32 : 0;
+  const int64_t row_bytes = dt == MOE_MXFP4 ? H / 2 : (int64_t)H * esz;
+  const int64_t srow_bytes = mx ? H / 32 : 0;
   const int64_t nb = (T + kPermBlock - 1) / kPermBlock;
   auto pick_unit = [](int64_t bytes, const void* a, const void* b) {
     if (bytes % 16 == 0 && aligned(a, 16) && aligned(b, 16)) return 16;
@@ -422,14 +422,14 @@ extern "C" moe_status moe_permute(const void* x, const uint8_t* x_scale, moe_dty
     return 1;
   };
   const int unit = pick_unit(row_bytes, x, x_perm);
-  const int sunit = dt == MOE_MXFP8 ? pick_unit(srow_bytes, x_scale, x_perm_scale) : 1;
+  const int sunit = mx ? pick_unit(srow_bytes, x_scale, x_perm_scale) : 1;
 
   if (reuse_map) {
     int64_t blocks = (T + 3) / 4;
     hipLaunchKernelGGL(permute_scatter_kernel, dim3((unsigned)blocks), dim3(256), 0, s,
-                       (const uint8_t*)x, row_bytes, dt == MOE_MXFP8 ? x_scale : nullptr, srow_bytes,
+                       (const uint8_t*)x, row_bytes, mx ? x_scale : nullptr, srow_bytes,
                        nullptr, nullptr, nullptr, nullptr, T, E, k, 1, unit, sunit, (uint8_t*)x_perm,
-                       dt == MOE_MXFP8 ? x_perm_scale : nullptr, nullptr, (int32_t*)row_id_map, nullptr);
+                       mx ? x_perm_scale : nullptr, nullptr, (int32_t*)row_id_map, nullptr);
     return check_launch("moe_permute(reuse)");
   }
 
@@ -452,8 +452,8 @@ extern "C" moe_status moe_permute(const void* x, const uint8_t* x_scale, moe_dty
   if (T > 0) {
     int64_t blocks = (T + 3) / 4;
     hipLaunchKernelGGL(permute_scatter_kernel, dim3((unsigned)blocks), dim3(256), 0, s, (const uint8_t*)x,
-                       row_bytes, dt == MOE_MXFP8 ? x_scale : nullptr, srow_bytes, topk_idx, topk_prob, base,
-                       rank_local, T, E, k, 0, unit, sunit, (uint8_t*)x_perm, dt == MOE_MXFP8 ? x_perm_scale : nullptr,
+                       row_bytes, mx ? x_scale : nullptr, srow_bytes, topk_idx, topk_prob, base,
+                       rank_local, T, E, k, 0, unit, sunit, (uint8_t*)x_perm, mx ? x_perm_scale : nullptr,
                        prob_perm, row_id_map, src_token);
   }
   return check_launch("moe_permute");

@@ -50,7 +50,8 @@ typedef enum {
   MOE_F32 = 0,   /* float32 */
   MOE_BF16 = 1,  /* bfloat16 bit patterns */
   MOE_MXFP8 = 2, /* E4M3 codes (uint8) + one E8M0 scale byte per 32 consecutive values */
-  MOE_FP8 = 3    /* E4M3 codes (uint8) + one float32 scale for the whole tensor (value = code x scale) */
+  MOE_FP8 = 3,   /* E4M3 codes (uint8) + one float32 scale for the whole tensor (value = code x scale) */
+  MOE_MXFP4 = 4  /* E2M1 codes, two a byte (the even one in the low nibble) + one E8M0 scale byte per 32 values */
 } moe_dtype;
 
 /* Largest expert count the library accepts. */
@@ -171,9 +172,10 @@ moe_status moe_balance_loss_bwd(const float* logits, const int32_t* counts, cons
  * The R = T*k (token, slot) pairs are grouped by expert in ascending expert
  * order; inside a group rows are in ascending token order. Row r of the result
  * holds x[src_token[r]].
- *   x            [T, H] in dtype dt (F32 or BF16; MXFP8: codes, with x_scale [T, H/32])
+ *   x            [T, H] in dtype dt (F32 or BF16; MXFP8: codes, with x_scale [T, H/32]; MXFP4:
+ *                codes [T, H/2], with x_scale [T, H/32])
  *   topk_idx     [T, k] int32, topk_prob [T, k] float32 (may be NULL: prob_perm not written)
- *   x_perm       [R, H] (out), x_perm_scale [R, H/32] (out, MXFP8 only)
+ *   x_perm       [R, H] (out; MXFP4: [R, H/2]), x_perm_scale [R, H/32] (out, MXFP8 and MXFP4 only)
  *   prob_perm    [R] float32 (out, may be NULL) routing weight of each row
  *   split_sizes  [E] int32 (out) rows per expert; offsets [E+1] int32 (out) prefix sums
  *   row_id_map   [T*k] int32 (out) row of pair (t, j) at index t*k + j
@@ -440,17 +442,40 @@ moe_status mxfp8_quantize_weights(int n, const void* const* w_bf16, int64_t rows
 moe_status fp8_tensor_quantize_weights(int n, const void* const* w_bf16, int64_t rows, int64_t cols,
                                        uint8_t* const* e4m3, float* scale, void* const* packed, void* stream);
 
+/*
+ * MXFP4 block quantisation of a bf16 matrix along its rows: the weights and activations of
+ * the 4-bit grouped MLP (moe_grouped_mlp_fwd with MOE_MXFP4, moe_grouped_linear_mxfp4).
+ * For each block of 32 consecutive elements of a row: s = the smallest integer with
+ * max|block| <= 6 * 2^s, clamped to [-127, 127] (s = -127 for an all-zero block); the scale
+ * byte is s + 127 (E8M0); each element becomes the OCP E2M1 code of x / 2^s (magnitudes 0,
+ * 0.5, 1, 1.5, 2, 3, 4, 6 for codes 0..7, the sign in bit 3), rounded to nearest with ties to
+ * the even code, keeping x's sign bit. A block that holds an infinity or a NaN gets scale byte
+ * 255 (E8M0's NaN) and codes 0, and every value or product read from it is NaN.
+ *   in [rows, cols] bf16 (16-byte aligned, cols % 32 == 0), e2m1 [rows, cols/2] uint8 (out,
+ *   4-byte aligned; element 2i in the low nibble of byte i), e8m0 [rows, cols/32] uint8 (out)
+ */
+moe_status mxfp4_quantize(const void* in_bf16, int64_t rows, int64_t cols, uint8_t* e2m1, uint8_t* e8m0,
+                          void* stream);
+
+/*
+ * The values of MXFP4 codes, code * 2^s, in bf16 (exact but for magnitudes past bf16's
+ * range, which become infinities; NaN for scale byte 255).
+ *   out [rows, cols] bf16 (16-byte aligned, cols % 32 == 0)
+ */
+moe_status mxfp4_dequantize(const uint8_t* e2m1, const uint8_t* e8m0, int64_t rows, int64_t cols, void* out_bf16,
+                            void* stream);
+
 /* Description of one grouped MLP layer (the experts' shapes and precisions). */
 typedef struct {
   int E;             /* experts, 1..MOE_MAX_EXPERTS */
   int H;             /* hidden size (GEMM K of gate_up, N of down) */
   int I;             /* intermediate size (gate_up has 2I outputs) */
-  moe_dtype compute; /* GEMM input precision: MOE_F32, MOE_BF16, MOE_MXFP8 or MOE_FP8 */
+  moe_dtype compute; /* GEMM input precision: MOE_F32, MOE_BF16, MOE_MXFP8, MOE_FP8 or MOE_MXFP4 */
   moe_dtype act;     /* storage of x_perm: F32 (compute F32), BF16, or the compute dtype's
-                        codes (MXFP8 / FP8: codes + x_perm_scale) */
-  moe_dtype wt;      /* storage of weights: F32 (compute F32), BF16 (for MXFP8 / FP8 compute:
-                        master weights quantised inside the call), or the compute dtype's
-                        codes (codes + scale tables) */
+                        codes (MXFP8 / FP8 / MXFP4: codes + x_perm_scale) */
+  moe_dtype wt;      /* storage of weights: F32 (compute F32), BF16 (for MXFP8 / FP8 / MXFP4
+                        compute: master weights quantised inside the call), or the compute
+                        dtype's codes (codes + scale tables) */
   int save_for_bwd;  /* nonzero: write z_save and h_save for moe_grouped_mlp_bwd */
 } moe_mlp_desc;
 
@@ -483,8 +508,12 @@ typedef struct {
  *   w_gate_up_scale / w_down_scale [host] E pointers to [2I, H/32] / [H, I/32]
  *       E8M0 scales, only when wt = MXFP8 (else NULL)
  *   offsets [E+1] int32 (device), prob_perm [R] float32
+ * With compute = MXFP4 (serving: forward only, save_for_bwd must be 0), x_perm, W1_e, h and
+ * W2_e enter their GEMMs as MXFP4 (rule of mxfp4_quantize), h from its float32 value in the
+ * gate_up epilogue; scales are the E8M0 bytes of mxfp4_quantize ([R, H/32], [2I, H/32],
+ * [H, I/32]), 8-byte aligned. Rows past offsets[E] of y_perm are not written.
  * Shapes the GEMM kernels implement: BF16 needs H % 256 == 0 and I % 128 == 0;
- * MXFP8 and FP8 need H % 256 == 0, I % 256 == 0 and E <= 128; F32 needs H % 4 == 0.
+ * MXFP8, FP8 and MXFP4 need H % 256 == 0, I % 256 == 0 and E <= 128; F32 needs H % 4 == 0.
  */
 moe_status moe_grouped_mlp_fwd(const moe_mlp_desc* desc, int64_t R, const void* x_perm,
                                const uint8_t* x_perm_scale, const void* const* w_gate_up,
@@ -557,6 +586,22 @@ moe_status moe_grouped_linear(int E, int64_t R, int K, int N, moe_dtype dt, cons
                               size_t workspace_bytes, void* stream);
 
 /*
+ * GroupedLinear with MXFP4 weights: y[r] = x[r] W_e^T for the rows r of expert e, both
+ * operands MXFP4 along K, float32 accumulation.
+ *   act = BF16: x [R, K] bf16, quantised in the call by the rule of mxfp4_quantize (x_scale
+ *   ignored); act = MXFP4: x [R, K/2] codes with x_scale [R, K/32]
+ *   w [host] E pointers to [N, K/2] codes, w_scale [host] E pointers to [N, K/32] scales
+ *   y [R, N] bf16 (rounded to nearest even); rows past offsets[E] are not written
+ * x, y, w 16-byte, scales 8-byte aligned. Shapes: K % 256 == 0, N % 256 == 0, E <= 128.
+ * workspace: moe_workspace_size(MOE_OP_LINEAR_MXFP4, desc with E, H = K, I = N and act, R,
+ * ...) bytes, 256-byte aligned, caller-owned. Calls sharing a workspace must not overlap.
+ */
+moe_status moe_grouped_linear_mxfp4(int E, int64_t R, int K, int N, moe_dtype act, const void* x,
+                                    const uint8_t* x_scale, const uint8_t* const* w, const uint8_t* const* w_scale,
+                                    const int32_t* offsets, void* y, void* workspace, size_t workspace_bytes,
+                                    void* stream);
+
+/*
  * GroupedLinear(gate_up) fused with ScaledSwiGLU (the first kernel of the fused grouped
  * MLP, Challenge 3 and Figure 4). For the rows r of expert e:
  *   z = x[r] W_e^T (2I values),  h[r] = silu(z[0:I]) * z[I:2I] * prob[r]
@@ -582,8 +627,9 @@ typedef enum {
   MOE_OP_GROUPED_GEMM = 3, /* moe_grouped_linear / moe_grouped_gate_up_swiglu; no argument used */
   MOE_OP_ROUTER_BWD = 4,   /* moe_router_bwd: desc (E, H) and T used */
   MOE_OP_BALANCE_LOSS = 5, /* T and E used, R = seq_len; desc may be NULL */
-  MOE_OP_NORM_BWD = 6      /* moe_pre_norm_bwd / moe_post_norm_bwd: desc (H) and T used, E = gate kind,
+  MOE_OP_NORM_BWD = 6,     /* moe_pre_norm_bwd / moe_post_norm_bwd: desc (H) and T used, E = gate kind,
                               k = gate_group (at most T; only with MOE_GATE_CHANNEL) */
+  MOE_OP_LINEAR_MXFP4 = 7  /* moe_grouped_linear_mxfp4: desc (E, H = K, I = N, act) and R used */
 } moe_op;
 
 /* Workspace bytes an operation needs (0 is possible). bytes is a [host] pointer. */

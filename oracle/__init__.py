@@ -14,3 +14,4 @@ from .mxfp8 import *  # noqa: F401,F403
 from .router import *  # noqa: F401,F403
 from .fp8_tensor import *  # noqa: F401,F403
 from .block import *  # noqa: F401,F403
+from .mxfp4 import *  # noqa: F401,F403

@@ -92,3 +92,42 @@ def test_post_norm(L):
     assert _size(L, _lib.MOE_OP_NORM_BWD, None, 0, 4, 0, 0)[0] == INV
     assert _size(L, _lib.MOE_OP_NORM_BWD, d, 0, 4, 3, 0)[0] == INV
     assert _size(L, _lib.MOE_OP_NORM_BWD, d, 0, 4, 2, 0)[0] == INV
+
+
+def test_mxfp4(L):
+    assert L.mxfp4_quantize(D, 4, 48, D, D, None) == INV and L.mxfp4_quantize(D, -1, 64, D, D, None) == INV
+    assert L.mxfp4_quantize(None, 4, 64, D, D, None) == INV and L.mxfp4_quantize(D, 4, 64, ODD, D, None) == INV
+    assert L.mxfp4_quantize(ctypes.c_void_p(4104), 4, 64, D, D, None) == INV and L.mxfp4_quantize(None, 0, 64, None, None, None) == 0
+    assert L.mxfp4_dequantize(D, D, 4, 40, D, None) == INV and L.mxfp4_dequantize(D, None, 4, 64, D, None) == INV
+    assert L.mxfp4_dequantize(D, D, 4, 64, ctypes.c_void_p(4104), None) == INV
+    assert L.mxfp4_dequantize(None, None, 4, 0, None, None) == 0
+    tab = _lib.strided_table(4096, 4, 256)[0]
+    nul = _lib.ptr_table([4096, 4096, None, 4096])[0]
+    odd = _lib.ptr_table([4096, 4096, 4100, 4096])[0]
+    A, M = _lib.MOE_BF16, _lib.MOE_MXFP4
+
+    def lin(E=4, R=64, K=256, N=256, act=A, x=D, xs=None, w=tab, ws=tab, off=D, y=D, buf=D, n=1 << 20):
+        return L.moe_grouped_linear_mxfp4(E, R, K, N, act, x, xs, w, ws, off, y, buf, n, None)
+
+    assert lin(E=0) == INV and lin(E=257) == INV and lin(E=129) == UNS and lin(R=-1) == INV and lin(R=1 << 31) == INV
+    assert lin(K=128) == UNS and lin(N=320) == UNS and lin(act=_lib.MOE_MXFP8) == INV and lin(K=1 << 16, N=1 << 16) == UNS
+    assert lin(x=None) == INV and lin(y=ODD) == INV and lin(off=None) == INV and lin(w=None) == INV and lin(ws=None) == INV
+    assert lin(w=nul) == INV and b"expert 2" in L.moe_last_error()
+    assert lin(w=odd) == INV and lin(ws=odd) == INV and lin(act=M) == INV and lin(act=M, xs=ctypes.c_void_p(4100)) == INV
+    assert lin(n=16) == WS and lin(buf=None) == INV and lin(buf=ctypes.c_void_p(4112)) == INV and lin(R=0, x=None) == 0
+    Desc = _lib.MlpDesc
+    assert _size(L, _lib.MOE_OP_LINEAR_MXFP4, Desc(4, 256, 256, M, A, M, 0), 64, 0, 0, 0)[1] >= 64 * (128 + 8)
+    assert _size(L, _lib.MOE_OP_LINEAR_MXFP4, Desc(4, 256, 256, M, 0, M, 0), 64, 0, 0, 0)[0] == INV
+    assert _size(L, _lib.MOE_OP_LINEAR_MXFP4, None, 64, 0, 0, 0)[0] == INV
+    st, n = _size(L, _lib.MOE_OP_MLP_FWD, Desc(8, 512, 256, M, A, A, 0), 64, 0, 0, 0)
+    assert st == 0 and n >= 8 * 3 * 512 * 256 // 2 + 64 * (512 + 256) // 2
+    assert _size(L, _lib.MOE_OP_MLP_FWD, Desc(8, 512, 256, M, A, A, 1), 64, 0, 0, 0)[0] == UNS     # forward only
+    assert _size(L, _lib.MOE_OP_MLP_BWD, Desc(8, 512, 256, M, A, A, 0), 64, 0, 0, 0)[0] == UNS
+    assert _size(L, _lib.MOE_OP_MLP_FWD, Desc(129, 512, 256, M, A, A, 0), 64, 0, 0, 0)[0] == UNS
+    assert _size(L, _lib.MOE_OP_MLP_FWD, Desc(8, 512, 384, M, A, A, 0), 64, 0, 0, 0)[0] == UNS
+    assert _size(L, _lib.MOE_OP_MLP_FWD, Desc(8, 512, 256, M, _lib.MOE_MXFP8, M, 0), 64, 0, 0, 0)[0] == INV
+    d = Desc(4, 256, 256, M, M, M, 0)
+    fwd = lambda xs=D, s=tab: L.moe_grouped_mlp_fwd(ctypes.byref(d), 64, D, xs, tab, tab, s, tab, D, D, D, None, None, D, 0,
+                                                    None)
+    assert fwd() == WS and fwd(xs=None) == INV and fwd(xs=ctypes.c_void_p(4100)) == INV and fwd(s=None) == INV and fwd(s=odd) == INV
+    assert L.moe_grouped_gate_up_swiglu(4, 64, 256, 256, M, D, D, tab, tab, D, D, D, D, None, None, 0, None) == INV
