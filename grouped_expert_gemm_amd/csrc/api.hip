@@ -100,6 +100,8 @@ extern "C" moe_status moe_workspace_size(moe_op op, const moe_mlp_desc* desc, in
       if (!desc || R < 0 || desc->E < 1 || desc->E > MOE_MAX_EXPERTS || desc->H < 1 || desc->I < 1 ||
           (desc->act != MOE_BF16 && desc->act != MOE_MXFP4))
         return fail(MOE_ERR_INVALID_ARG, "moe_workspace_size(LINEAR_MXFP4): desc NULL or bad R/E/K/N/act");
+      if (const moe_status s = mx4::check_shape(desc->E, desc->H, desc->I, "moe_workspace_size(LINEAR_MXFP4)"); s != MOE_OK)
+        return s;
       *bytes = mx4::linear_workspace_bytes(desc->E, R, desc->H, desc->I, desc->act);
       return MOE_OK;
   }

@@ -7,6 +7,25 @@
 namespace moe {
 namespace mx4 {
 
+constexpr int kMaxE = 128;  // experts per call (two pointer tables in the kernel arguments)
+
+enum { EP_STORE = 0, EP_SWIGLU = 1 };
+
+// Operands of a grouped product. Scales are in the public row-major layout for the row
+// kernel, in the MFMA's lane order (lane_scales) for the tile kernel.
+struct Params {
+  const uint8_t* tab[kMaxE];    // per-expert weight codes [N][K / 2]
+  const uint8_t* tab_s[kMaxE];  // per-expert weight scales
+  const uint8_t* q;             // row codes [R][K / 2]
+  const uint8_t* q_s;           // row scales
+  void* c;                      // STORE: bf16 [R][N]; SWIGLU: h codes [R][I / 2]
+  uint8_t* c_s;                 // SWIGLU: h's scales, as the down product reads them
+  const int32_t* offsets;
+  const float* prob;
+  int64_t R;
+  int K, N, E, I, n_tiles;
+};
+
 constexpr uint32_t kNotFinite = 0x7F800000u;  // magnitude bits of infinity; above: NaN
 
 // E8M0 byte of a block whose largest magnitude has the float32 bits u: s + 127 with s the
@@ -40,7 +59,14 @@ __device__ __forceinline__ uint32_t pack8(const float* f, int byte) {
   return byte == 255 ? 0u : w;
 }
 
-moe_status quantize(const void* in_bf16, int64_t rows, int64_t cols, uint8_t* e2m1, uint8_t* e8m0, hipStream_t s);
+// lanes: scales in lane order, word ((k / 256 * rows + r) * 2 + g) with byte s the scale of
+// block 2s + g of the row's 256 values (cols % 256 == 0, scales 4-byte aligned)
+moe_status quantize(const void* in_bf16, int64_t rows, int64_t cols, uint8_t* e2m1, uint8_t* e8m0, hipStream_t s,
+                    bool lanes = false);
+// public-layout scales [rows][cols / 32] of n tensors of one shape -> lane order
+moe_status lane_scales(const uint8_t* const* src, uint8_t* const* dst, int n, int64_t rows, int64_t cols, hipStream_t s);
+
+moe_status launch_tile(int ep, const Params& p, hipStream_t s);
 
 moe_status check_shape(int E, int K, int N, const char* what);
 size_t mlp_workspace_bytes(const moe_mlp_desc& d, int64_t R);

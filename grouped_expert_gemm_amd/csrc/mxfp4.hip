@@ -25,7 +25,6 @@ namespace mx4 {
 
 using gemm::silu_f;
 
-constexpr int kMaxE = 128;  // experts per call (two pointer tables in the kernel arguments)
 constexpr int kUnit = 256;  // K values of one unit
 
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
@@ -38,8 +37,15 @@ __device__ __forceinline__ i32x8_t wide(uint4 v) { return i32x8_t{(int)v.x, (int
 // of bf16 each), whose largest magnitude two xor-shuffles find.
 // ---------------------------------------------------------------------------
 
+// byte of block b of row r in lane order (mxfp4.h)
+__device__ __forceinline__ int64_t lane_at(int64_t r, int64_t b, int64_t rows) {
+  return (((b >> 3) * rows + r) * 2 + (b & 1)) * 4 + ((b >> 1) & 3);
+}
+
+// lane_rows: 0 for row-major scales, else the row count, for lane order
 __global__ __launch_bounds__(256) void quantize_kernel(const uint4* __restrict__ in, int64_t nblocks,
-                                                       uint32_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+                                                       uint32_t* __restrict__ codes, uint8_t* __restrict__ scales,
+                                                       int64_t cols32, int64_t lane_rows) {
   const int64_t total = nblocks * 4, stride = (int64_t)gridDim.x * blockDim.x;
   const int64_t padded = (total + 63) / 64 * 64;  // whole wavefronts: every lane reaches the shuffles
   for (int64_t q = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; q < padded; q += stride) {
@@ -59,20 +65,65 @@ __global__ __launch_bounds__(256) void quantize_kernel(const uint4* __restrict__
     const int b = scale_byte(top);
     if (live) {
       codes[q] = pack8(f, b);
-      if ((q & 3) == 0) scales[q >> 2] = (uint8_t)b;
+      if ((q & 3) == 0) {
+        const int64_t n = q >> 2, r = lane_rows ? n / cols32 : 0;
+        scales[lane_rows ? lane_at(r, n - r * cols32, lane_rows) : n] = (uint8_t)b;
+      }
     }
   }
 }
 
-moe_status quantize(const void* in_bf16, int64_t rows, int64_t cols, uint8_t* e2m1, uint8_t* e8m0, hipStream_t s) {
+moe_status quantize(const void* in_bf16, int64_t rows, int64_t cols, uint8_t* e2m1, uint8_t* e8m0, hipStream_t s,
+                    bool lanes) {
   const int64_t nblocks = rows * (cols / 32);
   if (nblocks == 0) return MOE_OK;
   int64_t grid = (nblocks * 4 + 255) / 256;
   const int64_t most = (int64_t)num_cus() * 16;
   if (grid > most) grid = most;
   hipLaunchKernelGGL(quantize_kernel, dim3((unsigned)grid), dim3(256), 0, s, (const uint4*)in_bf16, nblocks,
-                     (uint32_t*)e2m1, e8m0);
+                     (uint32_t*)e2m1, e8m0, cols / 32, lanes ? rows : 0);
   return check_launch("mxfp4_quantize");
+}
+
+// Row-major scales to lane order: 64 rows x 8 steps a workgroup through LDS, 64 bytes of a
+// row read together, 512 bytes of a step written together.
+struct ScaleTables {
+  const uint2* src[kMaxE];
+  uint2* dst[kMaxE];
+};
+
+__global__ __launch_bounds__(256) void lane_scales_kernel(const ScaleTables tabs, int64_t rows, int steps) {
+  __shared__ uint2 tile[8][65];
+  const uint2* src = tabs.src[blockIdx.z];
+  uint2* dst = tabs.dst[blockIdx.z];
+  const int64_t r0 = (int64_t)blockIdx.x * 64;
+  const int s0 = blockIdx.y * 8, tid = threadIdx.x;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = (i * 256 + tid) >> 3, st = tid & 7;
+    if (r0 + r < rows && s0 + st < steps) {
+      const uint2 v = src[(r0 + r) * steps + s0 + st];
+      tile[st][r] = make_uint2(__builtin_amdgcn_perm(v.y, v.x, 0x06040200u), __builtin_amdgcn_perm(v.y, v.x, 0x07050301u));
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int st = (i * 256 + tid) >> 6, r = tid & 63;
+    if (r0 + r < rows && s0 + st < steps) dst[(int64_t)(s0 + st) * rows + r0 + r] = tile[st][r];
+  }
+}
+
+moe_status lane_scales(const uint8_t* const* src, uint8_t* const* dst, int n, int64_t rows, int64_t cols, hipStream_t s) {
+  ScaleTables t;
+  for (int i = 0; i < n; ++i) {
+    t.src[i] = reinterpret_cast<const uint2*>(src[i]);
+    t.dst[i] = reinterpret_cast<uint2*>(dst[i]);
+  }
+  const int steps = (int)(cols / 256);
+  const dim3 grid((unsigned)((rows + 63) / 64), (unsigned)((steps + 7) / 8), (unsigned)n);
+  hipLaunchKernelGGL(lane_scales_kernel, grid, dim3(256), 0, s, t, rows, steps);
+  return check_launch("MXFP4 scale conversion");
 }
 
 __global__ __launch_bounds__(256) void dequantize_kernel(const uint32_t* __restrict__ codes,
@@ -95,21 +146,6 @@ __global__ __launch_bounds__(256) void dequantize_kernel(const uint32_t* __restr
 // ---------------------------------------------------------------------------
 // grouped GEMM, few rows an expert
 // ---------------------------------------------------------------------------
-
-enum { EP_STORE = 0, EP_SWIGLU = 1 };
-
-struct Params {
-  const uint8_t* tab[kMaxE];    // per-expert weight codes [N][K / 2]
-  const uint8_t* tab_s[kMaxE];  // per-expert weight scales [N][K / 32]
-  const uint8_t* q;             // row codes [R][K / 2]
-  const uint8_t* q_s;           // row scales [R][K / 32]
-  void* c;                      // STORE: bf16 [R][N]; SWIGLU: h codes [R][I / 2]
-  uint8_t* c_s;                 // SWIGLU: h scales [R][I / 32]
-  const int32_t* offsets;
-  const float* prob;
-  int64_t R;
-  int K, N, E, I;
-};
 
 // the rank-th expert that has rows, or -1: its rows are [beg, end). Offsets are kept inside
 // [0, R]; a wavefront looks at 64 experts at a time.
@@ -255,6 +291,9 @@ moe_status check_shape(int E, int K, int N, const char* what) {
   return MOE_OK;
 }
 
+// Few rows an expert: bound by the weights' bytes, on the row kernel; else on 256-row tiles.
+static bool few_rows(int64_t R, int E) { return R <= (int64_t)64 * E; }
+
 static void fill(Params& p, int E, int64_t R, int K, int N, const uint8_t* x, const uint8_t* xs, const uint8_t* const* w,
                  const uint8_t* const* ws, const int32_t* offsets, void* c) {
   std::memset(&p, 0, sizeof(p));
@@ -265,76 +304,131 @@ static void fill(Params& p, int E, int64_t R, int K, int N, const uint8_t* x, co
   p.q = x, p.q_s = xs, p.c = c, p.offsets = offsets, p.R = R, p.K = K, p.N = N, p.E = E;
 }
 
-static moe_status gate_up(Params& p, int I, const float* prob, uint8_t* hs, hipStream_t s) {
-  p.I = I, p.prob = prob, p.c_s = hs;
+static moe_status gate_up(Params& p, int I, const float* prob, uint8_t* hs, bool few, hipStream_t s) {
+  p.I = I, p.prob = prob, p.c_s = hs, p.n_tiles = I / 128;
+  if (!few) return launch_tile(EP_SWIGLU, p, s);
   const int64_t experts = p.R < p.E ? p.R : p.E;
   hipLaunchKernelGGL(grouped_gemm_rows_kernel<EP_SWIGLU>, dim3((unsigned)(I / 32), (unsigned)experts), dim3(256), 0, s, p);
   return check_launch("MXFP4 gate_up + ScaledSwiGLU");
 }
 
-static moe_status linear(Params& p, hipStream_t s) {
+static moe_status linear(Params& p, bool few, hipStream_t s) {
+  p.n_tiles = p.N / 256;
+  if (!few) return launch_tile(EP_STORE, p, s);
   const int64_t experts = p.R < p.E ? p.R : p.E;
   hipLaunchKernelGGL(grouped_gemm_rows_kernel<EP_STORE>, dim3((unsigned)(p.N / 32), (unsigned)experts), dim3(256), 0, s, p);
   return check_launch("MXFP4 grouped linear");
 }
 
+// The operands of one call: codes and scales as the chosen kernel reads them, from codes as
+// they are (scales converted for the tile kernel) or quantised from bf16. `take` hands out
+// workspace; the same walk with ws = nullptr counts it.
+struct Carver {
+  uint8_t* base;
+  size_t used = 0;
+  uint8_t* take(size_t n) {
+    uint8_t* p = base ? base + used : nullptr;
+    used += a256(n);
+    return p;
+  }
+};
+
+static moe_status rows_in(Carver& ws, moe_dtype act, const void* x, const uint8_t* x_scale, int64_t R, int K, bool few,
+                          const uint8_t*& q, const uint8_t*& qs, hipStream_t s) {
+  q = (const uint8_t*)x, qs = x_scale;
+  if (act == MOE_BF16) {
+    uint8_t* c = ws.take((size_t)R * K / 2);
+    uint8_t* b = ws.take((size_t)R * K / 32);
+    q = c, qs = b;
+    return ws.base ? quantize(x, R, K, c, b, s, !few) : MOE_OK;
+  }
+  if (few) return MOE_OK;
+  uint8_t* b = ws.take((size_t)R * K / 32);
+  const uint8_t* src[1] = {x_scale};
+  uint8_t* dst[1] = {b};
+  qs = b;
+  return ws.base ? lane_scales(src, dst, 1, R, K, s) : MOE_OK;
+}
+
+static moe_status weights_in(Carver& ws, moe_dtype wt, const void* const* w, const uint8_t* const* scale, int E, int N,
+                             int K, bool few, const uint8_t** c, const uint8_t** cs, hipStream_t s) {
+  const size_t n = (size_t)N * K;
+  uint8_t* dst[kMaxE];
+  for (int e = 0; e < E; ++e) {
+    if (wt == MOE_BF16) {
+      uint8_t* a = ws.take(n / 2);
+      uint8_t* b = ws.take(n / 32);
+      c[e] = a, cs[e] = b;
+      if (ws.base) {
+        const moe_status st = quantize(w[e], N, K, a, b, s, !few);
+        if (st != MOE_OK) return st;
+      }
+    } else if (few) {
+      c[e] = w ? (const uint8_t*)w[e] : nullptr, cs[e] = scale ? scale[e] : nullptr;
+    } else {
+      c[e] = w ? (const uint8_t*)w[e] : nullptr, cs[e] = dst[e] = ws.take(n / 32);
+    }
+  }
+  return ws.base && wt != MOE_BF16 && !few ? lane_scales(scale, dst, E, N, K, s) : MOE_OK;
+}
+
+// the whole MLP, or with ws.base NULL only its workspace
+static moe_status mlp(Carver& ws, const moe_mlp_desc& d, int64_t R, const void* x_perm, const uint8_t* x_perm_scale,
+                      const void* const* w_gate_up, const void* const* w_down, const uint8_t* const* w_gate_up_scale,
+                      const uint8_t* const* w_down_scale, const int32_t* offsets, const float* prob_perm, void* y_perm,
+                      hipStream_t s) {
+  const int E = d.E, H = d.H, I = d.I;
+  const bool few = few_rows(R, E);
+  uint8_t* hq = ws.take((size_t)R * I / 2);
+  uint8_t* hs = ws.take((size_t)R * I / 32);
+  const uint8_t *xq, *xs;
+  const uint8_t *w1[kMaxE], *s1[kMaxE], *w2[kMaxE], *s2[kMaxE];
+  moe_status st;
+  if ((st = rows_in(ws, d.act, x_perm, x_perm_scale, R, H, few, xq, xs, s)) != MOE_OK) return st;
+  if ((st = weights_in(ws, d.wt, w_gate_up, w_gate_up_scale, E, 2 * I, H, few, w1, s1, s)) != MOE_OK) return st;
+  if ((st = weights_in(ws, d.wt, w_down, w_down_scale, E, H, I, few, w2, s2, s)) != MOE_OK) return st;
+  if (!ws.base) return MOE_OK;
+  Params p;
+  fill(p, E, R, H, 2 * I, xq, xs, w1, s1, offsets, hq);
+  if ((st = gate_up(p, I, prob_perm, hs, few, s)) != MOE_OK) return st;
+  fill(p, E, R, I, H, hq, hs, w2, s2, offsets, y_perm);
+  return linear(p, few, s);
+}
+
 size_t mlp_workspace_bytes(const moe_mlp_desc& d, int64_t R) {
-  const size_t I = d.I, H = d.H, E = d.E;
-  size_t b = a256(R * I / 2) + a256(R * I / 32);
-  if (d.act == MOE_BF16) b += a256(R * H / 2) + a256(R * H / 32);
-  if (d.wt == MOE_BF16) b += E * (a256(I * H) + a256(2 * I * H / 32) + a256(H * I / 2) + a256(H * I / 32));
-  return b;
+  Carver ws{nullptr};
+  mlp(ws, d, R, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr);
+  return ws.used;
 }
 
-size_t linear_workspace_bytes(int E, int64_t R, int K, int N, moe_dtype act) {
-  return act == MOE_BF16 ? a256((size_t)R * K / 2) + a256((size_t)R * K / 32) : 0;
-}
-
-// workspace: h's codes and scales, x's if given in bf16, the weights' if given in bf16
 moe_status forward(const moe_mlp_desc& d, int64_t R, const void* x_perm, const uint8_t* x_perm_scale,
                    const void* const* w_gate_up, const void* const* w_down, const uint8_t* const* w_gate_up_scale,
                    const uint8_t* const* w_down_scale, const int32_t* offsets, const float* prob_perm, void* y_perm,
-                   uint8_t* ws, hipStream_t s) {
-  const int E = d.E, H = d.H, I = d.I;
-  moe_status st;
-  auto take = [&](size_t n) {
-    uint8_t* p = ws;
-    ws += a256(n);
-    return p;
-  };
-  uint8_t* hq = take((size_t)R * I / 2);
-  uint8_t* hs = take((size_t)R * I / 32);
-  const uint8_t* xq = (const uint8_t*)x_perm;
-  const uint8_t* xs = x_perm_scale;
-  if (d.act == MOE_BF16) {
-    uint8_t* a = take((size_t)R * H / 2);
-    uint8_t* b = take((size_t)R * H / 32);
-    if ((st = quantize(x_perm, R, H, a, b, s)) != MOE_OK) return st;
-    xq = a, xs = b;
-  }
-  const uint8_t* w1[kMaxE];
-  const uint8_t* w2[kMaxE];
-  const uint8_t* s1[kMaxE];
-  const uint8_t* s2[kMaxE];
-  for (int e = 0; e < E; ++e) {
-    if (d.wt == MOE_BF16) {
-      uint8_t* a = take((size_t)I * H);
-      uint8_t* b = take((size_t)2 * I * H / 32);
-      uint8_t* a2 = take((size_t)H * I / 2);
-      uint8_t* b2 = take((size_t)H * I / 32);
-      if ((st = quantize(w_gate_up[e], 2 * (int64_t)I, H, a, b, s)) != MOE_OK) return st;
-      if ((st = quantize(w_down[e], H, I, a2, b2, s)) != MOE_OK) return st;
-      w1[e] = a, s1[e] = b, w2[e] = a2, s2[e] = b2;
-    } else {
-      w1[e] = (const uint8_t*)w_gate_up[e], s1[e] = w_gate_up_scale[e];
-      w2[e] = (const uint8_t*)w_down[e], s2[e] = w_down_scale[e];
-    }
-  }
+                   uint8_t* workspace, hipStream_t s) {
+  Carver ws{workspace};
+  return mlp(ws, d, R, x_perm, x_perm_scale, w_gate_up, w_down, w_gate_up_scale, w_down_scale, offsets, prob_perm,
+             y_perm, s);
+}
+
+static moe_status grouped_linear(Carver& ws, int E, int64_t R, int K, int N, moe_dtype act, const void* x,
+                                 const uint8_t* x_scale, const uint8_t* const* w, const uint8_t* const* w_scale,
+                                 const int32_t* offsets, void* y, hipStream_t s) {
+  const bool few = few_rows(R, E);
+  const uint8_t *xq, *xs;
+  const uint8_t *wq[kMaxE], *wqs[kMaxE];
+  moe_status st = rows_in(ws, act, x, x_scale, R, K, few, xq, xs, s);
+  if (st != MOE_OK) return st;
+  st = weights_in(ws, MOE_MXFP4, (const void* const*)w, w_scale, E, N, K, few, wq, wqs, s);
+  if (st != MOE_OK || !ws.base) return st;
   Params p;
-  fill(p, E, R, H, 2 * I, xq, xs, w1, s1, offsets, hq);
-  if ((st = gate_up(p, I, prob_perm, hs, s)) != MOE_OK) return st;
-  fill(p, E, R, I, H, hq, hs, w2, s2, offsets, y_perm);
-  return linear(p, s);
+  fill(p, E, R, K, N, xq, xs, wq, wqs, offsets, y);
+  return linear(p, few, s);
+}
+
+size_t linear_workspace_bytes(int E, int64_t R, int K, int N, moe_dtype act) {
+  Carver ws{nullptr};
+  grouped_linear(ws, E, R, K, N, act, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr);
+  return ws.used;
 }
 
 }  // namespace mx4
@@ -396,16 +490,7 @@ extern "C" moe_status moe_grouped_linear_mxfp4(int E, int64_t R, int K, int N, m
   if (workspace_bytes < need) return fail(MOE_ERR_WORKSPACE, f + ": workspace too small");
   if (need > 0 && (!workspace || !aligned(workspace, 256)))
     return fail(MOE_ERR_INVALID_ARG, f + ": workspace NULL or not 256-byte aligned");
-  const hipStream_t s = as_stream(stream);
-  const uint8_t* xq = (const uint8_t*)x;
-  const uint8_t* xs = x_scale;
-  if (act == MOE_BF16) {
-    uint8_t* a = (uint8_t*)workspace;
-    uint8_t* b = a + align_up((size_t)R * K / 2, 256);
-    if ((st = mx4::quantize(x, R, K, a, b, s)) != MOE_OK) return st;
-    xq = a, xs = b;
-  }
-  mx4::Params p;
-  mx4::fill(p, E, R, K, N, xq, xs, w, w_scale, offsets, y);
-  return mx4::linear(p, s);
+  // a call that needs no workspace still walks the same way: any non-NULL base serves
+  mx4::Carver ws{need > 0 ? (uint8_t*)workspace : (uint8_t*)y};
+  return mx4::grouped_linear(ws, E, R, K, N, act, x, x_scale, w, w_scale, offsets, y, as_stream(stream));
 }

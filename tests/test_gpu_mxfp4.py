@@ -143,6 +143,12 @@ LINEAR = [
     (256, 256, [1] * 128),
     (1024, 512, [0] * 63 + [7] + [0] * 36 + [1]),
     (512, 256, [0, 1500, 0, 513]),
+    # every number of K steps modulo the tile kernel's ring of five, one step alone among them
+    (256, 256, [300]),
+    (768, 512, [70, 400]),
+    (1024, 256, [513, 64]),
+    (1536, 256, [0, 255, 256, 1]),
+    (2304, 256, [200]),
 ]
 
 
@@ -226,6 +232,8 @@ MLP = [
     (768, 512, [130, 0, 257, 70]),
     (256, 256, [1] * 100 + [0] * 28),
     (512, 512, [900, 3]),
+    (1024, 1280, [300, 129]),
+    (1280, 256, [520]),
 ]
 
 
