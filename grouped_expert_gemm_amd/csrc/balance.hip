@@ -20,6 +20,7 @@
 
 #include "common.h"
 #include "internal.h"
+#include "lanes.h"
 
 namespace moe {
 namespace {
@@ -51,13 +52,14 @@ BalancePlan make_plan(int64_t T, int64_t seq_len, int E) {
 }
 
 // workspace: [S * nch][E] sums of p, [S * nch] sums of lse^2, [S * nch][E] counts,
-// [S * nch] token counts, [S] balance, [S] z
+// [S * nch] token counts, then per sequence [S] balance and [S] z (one workgroup a sequence),
+// or [S][E] sums of p and [S] of lse^2
 struct BalanceWs {
   float* p;
   float* z;
   int32_t* c;
   int32_t* n;
-  float* seq;  // [2][S]
+  float* seq;
 };
 
 BalanceWs carve(void* ws, const BalancePlan& p, int E) {
@@ -69,19 +71,6 @@ BalanceWs carve(void* ws, const BalancePlan& p, int E) {
   w.n = w.c + parts * E;
   w.seq = (float*)(w.n + parts);
   return w;
-}
-
-template <int L>
-__device__ __forceinline__ float group_max(float v) {
-#pragma unroll
-  for (int m = L / 2; m >= 1; m >>= 1) v = fmaxf(v, __shfl_xor(v, m, L));
-  return v;
-}
-template <int L>
-__device__ __forceinline__ float group_sum(float v) {
-#pragma unroll
-  for (int m = L / 2; m >= 1; m >>= 1) v += __shfl_xor(v, m, L);
-  return v;
 }
 
 // expert of this lane's value q
@@ -113,14 +102,14 @@ __device__ __forceinline__ bool softmax_row(float* v, float& lse) {
   float mx = -INFINITY;
 #pragma unroll
   for (int q = 0; q < 4; ++q) mx = fmaxf(mx, isnan(v[q]) ? INFINITY : v[q]);
-  mx = group_max<L>(mx);
+  mx = lanes_max<L>(mx);
   float den = 0.f;
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     v[q] = expf(v[q] - mx);
     den += v[q];
   }
-  den = group_sum<L>(den);
+  den = lanes_sum<L>(den);
   const float inv = 1.f / den;
 #pragma unroll
   for (int q = 0; q < 4; ++q) v[q] *= inv;
@@ -160,8 +149,7 @@ __device__ __forceinline__ void finish_sequence(const SeqOut& o, int64_t s, cons
   }
   // 256 values, pairwise in a fixed order; mass (1 but for rounding) keeps a NaN row visible
   float v = term + mass;
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
+  v = lanes_sum<64>(v);
   if ((tid & 63) == 0) red[tid >> 6] = v;
   __syncthreads();
   if (tid == 0) {
@@ -275,50 +263,103 @@ __global__ __launch_bounds__(kThreads) void balance_fwd_kernel(const float* __re
   }
 }
 
-// one workgroup a sequence: its nch partial sums, rows r0, r0 + per, ... by thread, the
-// per (<= 256 / E) sub-sums then added in order
+// A sequence's nch partial sums: 8 experts a workgroup, 32 threads an expert each adding
+// every 32nd, eight loads in flight, then the 32 in order. The first workgroup of a sequence
+// also adds its nch sums of lse^2 and token counts.
 __global__ __launch_bounds__(kThreads) void balance_join_kernel(int64_t nch, BalanceWs ws, SeqOut o) {
-  __shared__ float fp[256], sp[256];
-  __shared__ int32_t fc[256], sc[256];
-  __shared__ float fz[256], red[4];
-  __shared__ int32_t fn[256];
+  __shared__ float fp[32][9];
+  __shared__ int32_t fc[32][9];
+  __shared__ float fz[4];
+  __shared__ int32_t fn[4];
   const int tid = threadIdx.x, E = o.E;
-  const int64_t s = blockIdx.x, first = s * nch;
-  const int per = 256 / E, e = tid % E, r0 = tid / E;
-  float p = 0.f, z = 0.f;
-  int32_t c = 0, n = 0;
-  if (r0 < per)
-    for (int64_t r = r0; r < nch; r += per) {
+  const int64_t s = blockIdx.y, first = s * nch;
+  const int e = blockIdx.x * 8 + (tid & 7), r0 = tid >> 3;
+  float p = 0.f;
+  int32_t c = 0;
+  if (e < E) {
+#pragma unroll 8
+    for (int64_t r = r0; r < nch; r += 32) {
       p += ws.p[(first + r) * E + e];
       c += ws.c[(first + r) * E + e];
     }
-  for (int64_t r = tid; r < nch; r += 256) {
-    z += ws.z[first + r];
-    n += ws.n[first + r];
   }
-  fp[tid] = p, fc[tid] = c, fz[tid] = z, fn[tid] = n;
+  fp[r0][tid & 7] = p;
+  fc[r0][tid & 7] = c;
+  if (blockIdx.x == 0) {
+    float z = 0.f;
+    int32_t n = 0;
+    for (int64_t r = tid; r < nch; r += kThreads) {
+      z += ws.z[first + r];
+      n += ws.n[first + r];
+    }
+    z = lanes_sum<64>(z);
+    n = (int32_t)lanes_reduce<64>((uint32_t)n, [](uint32_t a, uint32_t b) { return a + b; });
+    if ((tid & 63) == 0) {
+      fz[tid >> 6] = z;
+      fn[tid >> 6] = n;
+    }
+  }
   __syncthreads();
-  if (tid < E) {
-    float a = 0.f;
-    int32_t b = 0;
-    for (int r = 0; r < per; ++r) {
-      a += fp[r * E + tid];
-      b += fc[r * E + tid];
+  if (tid < 8 && e < E) {
+    p = 0.f;
+    c = 0;
+#pragma unroll
+    for (int r = 0; r < 32; ++r) {
+      p += fp[r][tid];
+      c += fc[r][tid];
     }
-    sp[tid] = a;
-    sc[tid] = b;
+    ws.seq[s * E + e] = p;
+    o.counts[s * E + e] = c;
   }
-  for (int m = 128; m >= 1; m >>= 1) {
-    if (tid < m) {
-      fz[tid] += fz[tid + m];
-      fn[tid] += fn[tid + m];
-    }
-    __syncthreads();
+  if (blockIdx.x == 0 && tid == 0) {
+    ws.seq[o.S * E + s] = (fz[0] + fz[1]) + (fz[2] + fz[3]);
+    o.tokens[s] = fn[0] + fn[1] + fn[2] + fn[3];
   }
-  finish_sequence(o, s, sp, sc, fz[0], fn[0], red);
 }
 
-// the mean over the sequences with tokens
+// The loss from the joined sums: a wavefront a sequence at a time, then the 16 wavefronts in order.
+__global__ __launch_bounds__(1024) void balance_loss_kernel(BalanceWs ws, SeqOut o) {
+  __shared__ float fb[16], fz[16];
+  __shared__ int32_t fn[16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, E = o.E;
+  float bal = 0.f, z = 0.f;
+  int32_t seqs = 0;
+  for (int64_t s = wave; s < o.S; s += 16) {
+    const int32_t n = o.tokens[s];
+    if (n == 0) continue;
+    const int64_t kn = (int64_t)o.k * n;
+    float v = 0.f;
+    for (int e = lane; e < E; e += 64) {
+      const float mass = ws.seq[s * E + e] / (float)n;
+      v += (float)((int64_t)E * o.counts[s * E + e] - kn) / (float)kn * mass + mass;
+    }
+    bal += lanes_sum<64>(v);
+    z += ws.seq[o.S * E + s] / (float)n;
+    ++seqs;
+  }
+  if (lane == 0) {
+    fb[wave] = bal;
+    fz[wave] = z;
+    fn[wave] = seqs;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 16; ++w) {
+      bal += fb[w];
+      z += fz[w];
+      seqs += fn[w];
+    }
+    const float d = seqs > 0 ? (float)seqs : 1.f;
+    bal /= d;
+    z /= d;
+    o.loss[0] = total_loss(o.a, bal, o.b, z);
+    o.loss[1] = bal;
+    o.loss[2] = z;
+    o.tokens[o.S] = seqs;
+  }
+}
+
+// the mean over the sequences with tokens, where each was finished by its one workgroup
 __global__ __launch_bounds__(kThreads) void balance_mean_kernel(SeqOut o) {
   __shared__ float fb[256], fz[256];
   __shared__ int32_t fn[256];
@@ -394,7 +435,7 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(const float* __re
       const bool ok = softmax_row<L>(v[u], lse) && live[u];
 #pragma unroll
       for (int q = 0; q < 4; ++q) share += v[u][q] * over[q];
-      share = group_sum<L>(share);
+      share = lanes_sum<L>(share);
       const float base = b2 * lse - share;
       float r[4];
 #pragma unroll
@@ -450,7 +491,7 @@ moe_status check_sizes(const char* fn, int64_t T, int E, int k, int64_t seq_len)
 
 size_t balance_workspace_bytes(int64_t T, int64_t seq_len, int E) {
   const BalancePlan p = make_plan(T, seq_len, E);
-  return align_up((size_t)(p.S * p.nch) * (8 * (size_t)E + 8) + (size_t)p.S * 8, 256);
+  return align_up((size_t)(p.S * p.nch) * (8 * (size_t)E + 8) + (size_t)p.S * (4 * (size_t)E + 8), 256);
 }
 
 }  // namespace moe
@@ -491,8 +532,12 @@ extern "C" moe_status moe_balance_loss(const float* logits, const int32_t* topk_
       hipLaunchKernelGGL((balance_fwd_kernel<L, V, false>), grid, block, 0, s, logits, topk_idx, mask, seq_len, p.nch,
                          p.chunk, ws, o);
   });
-  if (p.nch > 1) hipLaunchKernelGGL(balance_join_kernel, dim3((unsigned)p.S), dim3(kThreads), 0, s, p.nch, ws, o);
-  if (p.S > 1) hipLaunchKernelGGL(balance_mean_kernel, dim3(1), dim3(kThreads), 0, s, o);
+  if (p.nch > 1) {  // fewer than kTargetWgs sequences
+    hipLaunchKernelGGL(balance_join_kernel, dim3((E + 7) / 8, (unsigned)p.S), dim3(kThreads), 0, s, p.nch, ws, o);
+    hipLaunchKernelGGL(balance_loss_kernel, dim3(1), dim3(1024), 0, s, ws, o);
+  } else if (p.S > 1) {
+    hipLaunchKernelGGL(balance_mean_kernel, dim3(1), dim3(kThreads), 0, s, o);
+  }
   return check_launch("moe_balance_loss");
 }
 

@@ -18,6 +18,7 @@
 #include "common.h"
 #include "gemm_common.h"
 #include "internal.h"
+#include "lanes.h"
 #include "mxfp4.h"
 
 namespace moe {
@@ -34,7 +35,7 @@ __device__ __forceinline__ i32x8_t wide(uint4 v) { return i32x8_t{(int)v.x, (int
 
 // ---------------------------------------------------------------------------
 // quantisation: HBM-bound, 2 bytes in, 17/32 out a value. Four lanes own a block (16 bytes
-// of bf16 each), whose largest magnitude two xor-shuffles find.
+// of bf16 each), whose largest magnitude two lane moves find.
 // ---------------------------------------------------------------------------
 
 // byte of block b of row r in lane order (mxfp4.h)
@@ -47,7 +48,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(const uint4* __restrict__
                                                        uint32_t* __restrict__ codes, uint8_t* __restrict__ scales,
                                                        int64_t cols32, int64_t lane_rows) {
   const int64_t total = nblocks * 4, stride = (int64_t)gridDim.x * blockDim.x;
-  const int64_t padded = (total + 63) / 64 * 64;  // whole wavefronts: every lane reaches the shuffles
+  const int64_t padded = (total + 63) / 64 * 64;  // whole wavefronts: every lane reaches the lane moves
   for (int64_t q = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; q < padded; q += stride) {
     const bool live = q < total;
     const uint4 v = live ? in[q] : make_uint4(0, 0, 0, 0);
@@ -60,8 +61,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(const uint4* __restrict__
       f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
       top = max(top, max((w[i] << 16) & 0x7FFFFFFFu, w[i] & 0x7FFF0000u));
     }
-    top = max(top, (uint32_t)__shfl_xor((int)top, 1));
-    top = max(top, (uint32_t)__shfl_xor((int)top, 2));
+    top = lanes_umax<4>(top);
     const int b = scale_byte(top);
     if (live) {
       codes[q] = pack8(f, b);
@@ -264,8 +264,7 @@ __global__ __launch_bounds__(256) void grouped_gemm_rows_kernel(const Params prm
         const float p = prm.prob[mg < end ? mg : end - 1];
         const float h0 = silu_f(v0) * sum(32 + cp) * p, h1 = silu_f(v1) * sum(32 + cp + 1) * p;
         uint32_t top = max(__float_as_uint(h0) & 0x7FFFFFFFu, __float_as_uint(h1) & 0x7FFFFFFFu);
-#pragma unroll
-        for (int m = 8; m >= 1; m >>= 1) top = max(top, (uint32_t)__shfl_xor((int)top, m));
+        top = lanes_umax<16>(top);
         const int b = scale_byte(top);
         if (mg < end) {
           const uint32_t code = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, ldexpf(h0, 127 - b), ldexpf(h1, 127 - b), 1.f, 0);

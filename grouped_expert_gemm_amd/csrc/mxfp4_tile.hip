@@ -262,6 +262,12 @@ void grouped_gemm_tile_kernel(const Params prm) {
     static_for<RES>([&](auto V) { kstep(kt + decltype(V)::value, V); });
     wait_vm<0>();  // the empty copies past the last step land before LDS is reused
     lds_barrier();
+    // the sums are complete here: without this the compiler moves the last steps' MFMAs, with
+    // their operands held or spilled, into the epilogue's branches
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int b = 0; b < 4; ++b) asm volatile("" : "+a"(acc[a][b]));
 
     // ---------------- epilogue ----------------
     int ln = lane;
@@ -335,6 +341,7 @@ void grouped_gemm_tile_kernel(const Params prm) {
             // block 4 (nt & 1) + 2 wn + sn of the down product's step nt / 2
             if (ehi == 0) prm.c_s[(((int64_t)(nt >> 1) * R + mg) * 2 + sn) * 4 + (nt & 1) * 2 + wn] = (uint8_t)b;
           }
+          __builtin_amdgcn_sched_barrier(0);  // one block's values in registers at a time
         }
       }
     }

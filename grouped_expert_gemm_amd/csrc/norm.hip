@@ -18,6 +18,7 @@
 
 #include "common.h"
 #include "internal.h"
+#include "lanes.h"
 
 namespace moe {
 namespace {
@@ -71,8 +72,7 @@ __device__ __forceinline__ typename Raw<BF16, V>::type pack(const float* v) {
 // (a thread may be one reduction ahead of another, never two)
 template <int TPR>
 __device__ __forceinline__ float team_sum(float v, float* buf) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
+  v = lanes_sum<64>(v);
   if constexpr (TPR > 64) {
     if ((threadIdx.x & 63) == 0) buf[threadIdx.x >> 6] = v;
     __syncthreads();
@@ -135,20 +135,21 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(const F
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int v = 0; v < V; ++v) acc[i][v] = 0.f;
-      for (int j0 = 0; j0 < p.k; j0 += 2) {  // two rows' loads in flight; a dropped slot adds nothing
-        raw_t q[2][NV];
-        bool ok[2];
+      constexpr int kSlots = NV * V <= 32 ? 4 : 2;  // rows whose loads are in flight together
+      for (int j0 = 0; j0 < p.k; j0 += kSlots) {
+        raw_t q[kSlots][NV];
+        bool ok[kSlots];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < kSlots; ++u) {
           const int32_t r = j0 + u < p.k ? p.rows[t * p.k + j0 + u] : -1;
-          ok[u] = r >= 0 && r < R;
+          ok[u] = r >= 0 && r < R;  // a dropped slot adds nothing
           const elem_t* src = (const elem_t*)p.y + (int64_t)(ok[u] ? r : 0) * H;
 #pragma unroll
           for (int i = 0; i < NV; ++i)
             q[u][i] = in[i] && ok[u] ? *reinterpret_cast<const raw_t*>(src + (i * TPR + tr) * V) : raw_t{};
         }
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
+        for (int u = 0; u < kSlots; ++u)
           if (ok[u]) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -402,26 +403,34 @@ __global__ __launch_bounds__(TPR) void norm_bwd_kernel(const BwdParams p) {
         p.part[ch * H + (i * TPR + tr) * V + v] = GATE == GATE_CHANNEL && p.plan.pieces > 1 ? own[i][v] : sum[i][v];
 }
 
-// dw (and, for pieces, d_gate): 16 columns a workgroup, 16 threads a column each adding
-// every 16th partial row, then the 16 sums in order
+// dw (and, for pieces, d_gate): 16 columns a workgroup and 16 threads a column, `par` of them
+// on different groups at a time and 16 / par on the pieces of each; sums in a fixed order
 template <bool BF16>
 __global__ __launch_bounds__(256) void norm_join_kernel(const float* __restrict__ part, int64_t groups, int64_t pieces,
-                                                        int H, const void* __restrict__ w, const void* __restrict__ gate,
-                                                        float* __restrict__ dw, float* __restrict__ dgate) {
+                                                        int par, int H, const void* __restrict__ w,
+                                                        const void* __restrict__ gate, float* __restrict__ dw,
+                                                        float* __restrict__ dgate) {
   __shared__ float sums[16][17];
   const int cl = threadIdx.x & 15, q = threadIdx.x >> 4;
   const int col = blockIdx.x * 16 + cl;
+  const int each = 16 / par, gq = q / each, sub = q % each;
   float total = 0.f;
-  for (int64_t g = 0; g < groups; ++g) {
+  for (int64_t g0 = 0; g0 < groups; g0 += par) {
+    const int64_t g = g0 + gq;
     float s = 0.f;
-    if (col < H)
-      for (int64_t i = q; i < pieces; i += 16) s += part[(g * pieces + i) * H + col];
-    sums[q][cl] = s;
-    __syncthreads();
-    if (q == 0 && col < H) {
-      s = sums[0][cl];
-#pragma unroll
-      for (int i = 1; i < 16; ++i) s += sums[i][cl];
+    if (col < H && g < groups) {
+      const float* src = part + g * pieces * H + col;
+#pragma unroll 8
+      for (int64_t i = sub; i < pieces; i += each) s += src[i * H];
+    }
+    if (each > 1) {
+      sums[q][cl] = s;
+      __syncthreads();
+      if (sub == 0)
+        for (int i = 1; i < each; ++i) s += sums[q + i][cl];
+      __syncthreads();
+    }
+    if (sub == 0 && col < H && g < groups) {
       if (gate) {
         const float gv = BF16 ? bf16_to_f32(((const uint16_t*)gate)[g * H + col]) : ((const float*)gate)[g * H + col];
         const float wv = BF16 ? bf16_to_f32(((const uint16_t*)w)[col]) : ((const float*)w)[col];
@@ -431,9 +440,13 @@ __global__ __launch_bounds__(256) void norm_join_kernel(const float* __restrict_
         total = s;
       }
     }
-    __syncthreads();
   }
-  if (q == 0 && col < H) dw[col] = total;
+  sums[q][cl] = total;
+  __syncthreads();
+  if (q == 0 && col < H) {
+    for (int i = 1; i < par; ++i) total += sums[i * each][cl];
+    dw[col] = total;
+  }
 }
 
 template <int N>
@@ -521,8 +534,10 @@ void launch_bwd(const BwdParams& p, int gate_kind, bool bf16, bool vec, float* d
   const bool pieces = p.plan.pieces > 1;
   const dim3 grid((unsigned)((p.H + 15) / 16));
   const int64_t groups = pieces ? p.plan.chunks / p.plan.pieces : 1, each = pieces ? p.plan.pieces : p.plan.chunks;
+  int par = 1;
+  while (par < 16 && par < groups) par *= 2;
   auto kernel = bf16 ? norm_join_kernel<true> : norm_join_kernel<false>;
-  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, p.part, groups, each, p.H, p.w, pieces ? p.gate : nullptr, dw,
+  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, p.part, groups, each, par, p.H, p.w, pieces ? p.gate : nullptr, dw,
                      pieces ? p.dgate : nullptr);
 }
 
