@@ -122,10 +122,9 @@ def check(fn_name: str, status: int):
         raise MoeError(fn_name, status, f"{L.moe_status_str(status).decode()}: {L.moe_last_error().decode()}")
 
 
-def strided_table(base, n, stride):
-    """ptr_table of n pointers, stride bytes apart."""
-    arr = (ctypes.c_void_p * n)(*range(base, base + n * stride, stride)) if stride else (ctypes.c_void_p * n)(*[base] * n)
-    return ctypes.cast(arr, PP), arr
+def strided_table(ptrs):
+    """ptr_table of a contiguous int64 CPU tensor of addresses (which has to outlive the call)."""
+    return ctypes.cast(ptrs.data_ptr(), PP)
 
 
 def ptr_table(ptrs):

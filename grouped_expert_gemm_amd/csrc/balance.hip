@@ -26,7 +26,8 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 2;          // tokens of a group whose loads are in flight together
+constexpr int kUnroll = 4;          // tokens of a group whose loads are in flight together
+constexpr int kMinTokens = 2;       // tokens of a group that are worth a workgroup and a partial sum of their own
 constexpr int64_t kTargetWgs = 1024;
 
 struct BalancePlan {
@@ -41,7 +42,7 @@ inline int group_lanes(int E) {
 
 BalancePlan make_plan(int64_t T, int64_t seq_len, int E) {
   BalancePlan p{T / seq_len, seq_len, 1, 0};
-  const int64_t step = (int64_t)(kThreads / group_lanes(E)) * kUnroll;
+  const int64_t step = (int64_t)(kThreads / group_lanes(E)) * kMinTokens;
   const int64_t most = (seq_len + step - 1) / step;
   int64_t want = p.S > 0 ? (kTargetWgs + p.S - 1) / p.S : 1;
   if (want > most) want = most;
@@ -192,6 +193,7 @@ __global__ __launch_bounds__(kThreads) void balance_fwd_kernel(const float* __re
   int n = 0;
   for (int64_t i0 = 0; i0 < len; i0 += (int64_t)G * kUnroll) {  // the same trip count in every lane
     float v[kUnroll][4];
+    int32_t id[kUnroll][4];  // this lane's slots j, j + L, ... (k <= E <= 4 L); -1: none
     bool live[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -199,6 +201,8 @@ __global__ __launch_bounds__(kThreads) void balance_fwd_kernel(const float* __re
       live[u] = i < len && (!mask || mask[beg + i] != 0);
       if (live[u]) load_row<L, VEC>(logits + (beg + i) * E, j, E, v[u]);
       else v[u][0] = v[u][1] = v[u][2] = v[u][3] = -INFINITY;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) id[u][q] = live[u] && j + q * L < k ? idx[(beg + i) * k + j + q * L] : -1;
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
@@ -211,15 +215,9 @@ __global__ __launch_bounds__(kThreads) void balance_fwd_kernel(const float* __re
           zs += lse * lse;
           ++n;
         }
-        const int64_t t = beg + i0 + u * G + g;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {  // k <= E <= 4 L
-          const int slot = j + q * L;
-          if (slot < k) {
-            const int e = idx[t * k + slot];
-            if ((unsigned)e < (unsigned)E) atomicAdd(&sc[e], 1);
-          }
-        }
+        for (int q = 0; q < 4; ++q)
+          if ((unsigned)id[u][q] < (unsigned)E) atomicAdd(&sc[id[u][q]], 1);
       }
     }
   }

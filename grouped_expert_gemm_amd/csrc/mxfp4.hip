@@ -13,6 +13,7 @@
 // columns (32 gate and 32 up rows with SwiGLU) of one expert, its four wavefronts every
 // fourth 256-value unit of K, and their partial products are added through LDS in wavefront
 // order. The next unit's weights are in flight while one is multiplied.
+// (Many rows: mxfp4_tile.hip.)
 #include <cstring>
 
 #include "common.h"
@@ -31,7 +32,7 @@ constexpr int kUnit = 256;  // K values of one unit
 typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
-__device__ __forceinline__ i32x8_t wide(uint4 v) { return i32x8_t{(int)v.x, (int)v.y, (int)v.z, (int)v.w, 0, 0, 0, 0}; }
+__device__ __forceinline__ i32x8_t wide(i32x4_t v) { return i32x8_t{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
 
 // ---------------------------------------------------------------------------
 // quantisation: HBM-bound, 2 bytes in, 17/32 out a value. Four lanes own a block (16 bytes
@@ -173,37 +174,70 @@ __device__ __forceinline__ int find_expert(const int32_t* offsets, int E, int R,
   return -1;
 }
 
-template <int EP>
-__global__ __launch_bounds__(256) void grouped_gemm_rows_kernel(const Params prm) {
+// 32 bf16 values of one block -> its codes and scale byte
+__device__ __forceinline__ i32x4_t quantize_block(const uint4* x, int& byte) {
+  uint4 v[4];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = x[i];
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+    for (int h = 0; h < 4; ++h) top = max(top, max((w[h] << 16) & 0x7FFFFFFFu, w[h] & 0x7FFF0000u));
+  }
+  byte = scale_byte(top);
+  i32x4_t c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    float f[8];
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      f[2 * h] = __uint_as_float(w[h] << 16);
+      f[2 * h + 1] = __uint_as_float(w[h] & 0xFFFF0000u);
+    }
+    c[i] = (int)pack8(f, byte);
+  }
+  return c;
+}
+
+// kBF16: the rows are bf16 and each lane quantises the blocks that it multiplies, for calls of
+// so few rows that doing it in every workgroup costs less than a launch of its own
+template <int EP, bool kBF16>
+__global__ __launch_bounds__(256, 2) void grouped_gemm_rows_kernel(const Params prm) {
   constexpr int NA = EP == EP_SWIGLU ? 4 : 2;   // 16-row weight tiles
-  constexpr int RT = 4;                         // 16-row tiles of x at a time
+  constexpr int RT = kBF16 ? 1 : 4;             // 16-row tiles of x at a time
   constexpr int LD = NA * 16 + 4;
   __shared__ __attribute__((aligned(16))) float part[4][16][LD];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l16 = lane & 15, g = lane >> 4;
   int beg, end;
   const int e = find_expert(prm.offsets, prm.E, (int)prm.R, blockIdx.y, beg, end);
   if (e < 0) return;
   const int K = prm.K, units = K / kUnit;
   const int64_t ldc = K / 2, lds = K / 32;
-  const uint8_t* wc[NA];
-  const uint8_t* ws[NA];
+  // a wavefront-uniform base and 32-bit lane offsets (a weight is under 2^30 bytes)
+  const uint8_t* wbase = prm.tab[e];
+  const uint8_t* sbase = prm.tab_s[e];
+  uint32_t wc[NA], ws[NA];
 #pragma unroll
   for (int a = 0; a < NA; ++a) {
     const int n = EP == EP_SWIGLU ? (a >= 2 ? prm.I : 0) + blockIdx.x * 32 + (a & 1) * 16 + l16
                                   : blockIdx.x * 32 + a * 16 + l16;
-    wc[a] = prm.tab[e] + (int64_t)n * ldc + g * 16;
-    ws[a] = prm.tab_s[e] + (int64_t)n * lds;
+    wc[a] = (uint32_t)(n * ldc + g * 16);
+    ws[a] = (uint32_t)(n * lds);
   }
   for (int r0 = beg; r0 < end; r0 += RT * 16) {
     const int nrt = min(RT, (end - r0 + 15) / 16);
-    const uint8_t* xc[RT];
-    const uint8_t* xs[RT];
+    const uint8_t* xbase = prm.q + (int64_t)r0 * (kBF16 ? (int64_t)K * 2 : ldc);
+    const uint8_t* xsbase = kBF16 ? nullptr : prm.q_s + (int64_t)r0 * lds;
+    uint32_t xc[RT], xs[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      const int row = min(r0 + r * 16 + l16, end - 1);  // past the expert: any valid row, discarded
-      xc[r] = prm.q + row * ldc + g * 16;
-      xs[r] = prm.q_s + row * lds;
+      const int row = min(r * 16 + l16, end - 1 - r0);  // past the expert: any valid row, discarded
+      xc[r] = kBF16 ? (uint32_t)((row * K + g * 32) * 2) : (uint32_t)(row * ldc + g * 16);
+      xs[r] = (uint32_t)(row * lds);
     }
     typedef float f4 __attribute__((ext_vector_type(4)));
     f4 acc[NA][RT];
@@ -211,29 +245,38 @@ __global__ __launch_bounds__(256) void grouped_gemm_rows_kernel(const Params prm
     for (int a = 0; a < NA; ++a)
 #pragma unroll
       for (int r = 0; r < RT; ++r) acc[a][r] = f4{0.f, 0.f, 0.f, 0.f};
-    uint4 w[2][NA][2];
+    i32x4_t w[2][NA][2];
     uint2 sw[2][NA];
-    auto load = [&](int u, uint4 (&c)[NA][2], uint2 (&s)[NA]) {
+    auto load = [&](int u, i32x4_t (&c)[NA][2], uint2 (&s)[NA]) {
 #pragma unroll
       for (int a = 0; a < NA; ++a) {
-        c[a][0] = *reinterpret_cast<const uint4*>(wc[a] + u * 128);
-        c[a][1] = *reinterpret_cast<const uint4*>(wc[a] + u * 128 + 64);
-        s[a] = *reinterpret_cast<const uint2*>(ws[a] + u * 8);
+        c[a][0] = *reinterpret_cast<const i32x4_t*>(wbase + u * 128 + wc[a]);
+        c[a][1] = *reinterpret_cast<const i32x4_t*>(wbase + u * 128 + 64 + wc[a]);
+        s[a] = *reinterpret_cast<const uint2*>(sbase + u * 8 + ws[a]);
       }
     };
-    auto step = [&](int u, const uint4 (&c)[NA][2], const uint2 (&s)[NA]) {
+    auto step = [&](int u, const i32x4_t (&c)[NA][2], const uint2 (&s)[NA]) {
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         if (r >= nrt) break;
-        const uint4 x0 = *reinterpret_cast<const uint4*>(xc[r] + u * 128);
-        const uint4 x1 = *reinterpret_cast<const uint4*>(xc[r] + u * 128 + 64);
-        const uint2 sx = *reinterpret_cast<const uint2*>(xs[r] + u * 8);
+        i32x4_t x0, x1;
+        int sx0, sx1;
+        if constexpr (kBF16) {
+          x0 = quantize_block(reinterpret_cast<const uint4*>(xbase + u * 512 + xc[r]), sx0);
+          x1 = quantize_block(reinterpret_cast<const uint4*>(xbase + u * 512 + 256 + xc[r]), sx1);
+        } else {
+          x0 = *reinterpret_cast<const i32x4_t*>(xbase + u * 128 + xc[r]);
+          x1 = *reinterpret_cast<const i32x4_t*>(xbase + u * 128 + 64 + xc[r]);
+          const uint2 sx = *reinterpret_cast<const uint2*>(xsbase + u * 8 + xs[r]);
+          sx0 = (int)(sx.x >> (8 * g));
+          sx1 = (int)(sx.y >> (8 * g));
+        }
 #pragma unroll
         for (int a = 0; a < NA; ++a) {
           acc[a][r] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(c[a][0]), wide(x0), acc[a][r], 4, 4, 0,
-                                                                        (int)(s[a].x >> (8 * g)), 0, (int)(sx.x >> (8 * g)));
+                                                                        (int)(s[a].x >> (8 * g)), 0, sx0);
           acc[a][r] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(wide(c[a][1]), wide(x1), acc[a][r], 4, 4, 0,
-                                                                        (int)(s[a].y >> (8 * g)), 0, (int)(sx.y >> (8 * g)));
+                                                                        (int)(s[a].y >> (8 * g)), 0, sx1);
         }
       }
     };
@@ -290,8 +333,14 @@ moe_status check_shape(int E, int K, int N, const char* what) {
   return MOE_OK;
 }
 
-// Few rows an expert: bound by the weights' bytes, on the row kernel; else on 256-row tiles.
-static bool few_rows(int64_t R, int E) { return R <= (int64_t)64 * E; }
+// How a call reads its rows. Few rows an expert are bound by the weights' bytes: the row
+// kernel; otherwise 256-row tiles. At most 16 rows in all, given in bf16, are quantised by
+// the row kernel itself.
+enum class Path { kRowsBF16, kRows, kTiles };
+static Path choose(int64_t R, int E, moe_dtype act) {
+  if (act == MOE_BF16 && R <= 16) return Path::kRowsBF16;
+  return R <= (int64_t)64 * E ? Path::kRows : Path::kTiles;
+}
 
 static void fill(Params& p, int E, int64_t R, int K, int N, const uint8_t* x, const uint8_t* xs, const uint8_t* const* w,
                  const uint8_t* const* ws, const int32_t* offsets, void* c) {
@@ -300,23 +349,17 @@ static void fill(Params& p, int E, int64_t R, int K, int N, const uint8_t* x, co
     p.tab[e] = w[e];
     p.tab_s[e] = ws[e];
   }
-  p.q = x, p.q_s = xs, p.c = c, p.offsets = offsets, p.R = R, p.K = K, p.N = N, p.E = E;
+  p.q = x, p.q_s = xs, p.c = c, p.offsets = offsets, p.R = R, p.K = K, p.N = N, p.E = E, p.n_tiles = N / 256;
 }
 
-static moe_status gate_up(Params& p, int I, const float* prob, uint8_t* hs, bool few, hipStream_t s) {
-  p.I = I, p.prob = prob, p.c_s = hs, p.n_tiles = I / 128;
-  if (!few) return launch_tile(EP_SWIGLU, p, s);
+template <int EP>
+static moe_status launch(const Params& p, Path path, hipStream_t s) {
+  if (path == Path::kTiles) return launch_tile(EP, p, s);
   const int64_t experts = p.R < p.E ? p.R : p.E;
-  hipLaunchKernelGGL(grouped_gemm_rows_kernel<EP_SWIGLU>, dim3((unsigned)(I / 32), (unsigned)experts), dim3(256), 0, s, p);
-  return check_launch("MXFP4 gate_up + ScaledSwiGLU");
-}
-
-static moe_status linear(Params& p, bool few, hipStream_t s) {
-  p.n_tiles = p.N / 256;
-  if (!few) return launch_tile(EP_STORE, p, s);
-  const int64_t experts = p.R < p.E ? p.R : p.E;
-  hipLaunchKernelGGL(grouped_gemm_rows_kernel<EP_STORE>, dim3((unsigned)(p.N / 32), (unsigned)experts), dim3(256), 0, s, p);
-  return check_launch("MXFP4 grouped linear");
+  const dim3 grid((unsigned)((EP == EP_SWIGLU ? p.I : p.N) / 32), (unsigned)experts);
+  if (path == Path::kRowsBF16) hipLaunchKernelGGL((grouped_gemm_rows_kernel<EP, true>), grid, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((grouped_gemm_rows_kernel<EP, false>), grid, dim3(256), 0, s, p);
+  return check_launch(EP == EP_SWIGLU ? "MXFP4 gate_up + ScaledSwiGLU" : "MXFP4 grouped linear");
 }
 
 // The operands of one call: codes and scales as the chosen kernel reads them, from codes as
@@ -332,16 +375,17 @@ struct Carver {
   }
 };
 
-static moe_status rows_in(Carver& ws, moe_dtype act, const void* x, const uint8_t* x_scale, int64_t R, int K, bool few,
+static moe_status rows_in(Carver& ws, moe_dtype act, const void* x, const uint8_t* x_scale, int64_t R, int K, Path path,
                           const uint8_t*& q, const uint8_t*& qs, hipStream_t s) {
   q = (const uint8_t*)x, qs = x_scale;
+  if (path == Path::kRowsBF16) return MOE_OK;
   if (act == MOE_BF16) {
     uint8_t* c = ws.take((size_t)R * K / 2);
     uint8_t* b = ws.take((size_t)R * K / 32);
     q = c, qs = b;
-    return ws.base ? quantize(x, R, K, c, b, s, !few) : MOE_OK;
+    return ws.base ? quantize(x, R, K, c, b, s, path == Path::kTiles) : MOE_OK;
   }
-  if (few) return MOE_OK;
+  if (path == Path::kRows) return MOE_OK;
   uint8_t* b = ws.take((size_t)R * K / 32);
   const uint8_t* src[1] = {x_scale};
   uint8_t* dst[1] = {b};
@@ -350,7 +394,7 @@ static moe_status rows_in(Carver& ws, moe_dtype act, const void* x, const uint8_
 }
 
 static moe_status weights_in(Carver& ws, moe_dtype wt, const void* const* w, const uint8_t* const* scale, int E, int N,
-                             int K, bool few, const uint8_t** c, const uint8_t** cs, hipStream_t s) {
+                             int K, Path path, const uint8_t** c, const uint8_t** cs, hipStream_t s) {
   const size_t n = (size_t)N * K;
   uint8_t* dst[kMaxE];
   for (int e = 0; e < E; ++e) {
@@ -359,16 +403,16 @@ static moe_status weights_in(Carver& ws, moe_dtype wt, const void* const* w, con
       uint8_t* b = ws.take(n / 32);
       c[e] = a, cs[e] = b;
       if (ws.base) {
-        const moe_status st = quantize(w[e], N, K, a, b, s, !few);
+        const moe_status st = quantize(w[e], N, K, a, b, s, path == Path::kTiles);
         if (st != MOE_OK) return st;
       }
-    } else if (few) {
+    } else if (path != Path::kTiles) {
       c[e] = w ? (const uint8_t*)w[e] : nullptr, cs[e] = scale ? scale[e] : nullptr;
     } else {
       c[e] = w ? (const uint8_t*)w[e] : nullptr, cs[e] = dst[e] = ws.take(n / 32);
     }
   }
-  return ws.base && wt != MOE_BF16 && !few ? lane_scales(scale, dst, E, N, K, s) : MOE_OK;
+  return ws.base && wt != MOE_BF16 && path == Path::kTiles ? lane_scales(scale, dst, E, N, K, s) : MOE_OK;
 }
 
 // the whole MLP, or with ws.base NULL only its workspace
@@ -377,21 +421,22 @@ static moe_status mlp(Carver& ws, const moe_mlp_desc& d, int64_t R, const void* 
                       const uint8_t* const* w_down_scale, const int32_t* offsets, const float* prob_perm, void* y_perm,
                       hipStream_t s) {
   const int E = d.E, H = d.H, I = d.I;
-  const bool few = few_rows(R, E);
+  const Path path = choose(R, E, d.act);
   uint8_t* hq = ws.take((size_t)R * I / 2);
   uint8_t* hs = ws.take((size_t)R * I / 32);
   const uint8_t *xq, *xs;
   const uint8_t *w1[kMaxE], *s1[kMaxE], *w2[kMaxE], *s2[kMaxE];
   moe_status st;
-  if ((st = rows_in(ws, d.act, x_perm, x_perm_scale, R, H, few, xq, xs, s)) != MOE_OK) return st;
-  if ((st = weights_in(ws, d.wt, w_gate_up, w_gate_up_scale, E, 2 * I, H, few, w1, s1, s)) != MOE_OK) return st;
-  if ((st = weights_in(ws, d.wt, w_down, w_down_scale, E, H, I, few, w2, s2, s)) != MOE_OK) return st;
+  if ((st = rows_in(ws, d.act, x_perm, x_perm_scale, R, H, path, xq, xs, s)) != MOE_OK) return st;
+  if ((st = weights_in(ws, d.wt, w_gate_up, w_gate_up_scale, E, 2 * I, H, path, w1, s1, s)) != MOE_OK) return st;
+  if ((st = weights_in(ws, d.wt, w_down, w_down_scale, E, H, I, path, w2, s2, s)) != MOE_OK) return st;
   if (!ws.base) return MOE_OK;
   Params p;
   fill(p, E, R, H, 2 * I, xq, xs, w1, s1, offsets, hq);
-  if ((st = gate_up(p, I, prob_perm, hs, few, s)) != MOE_OK) return st;
+  p.I = I, p.prob = prob_perm, p.c_s = hs, p.n_tiles = I / 128;
+  if ((st = launch<EP_SWIGLU>(p, path, s)) != MOE_OK) return st;
   fill(p, E, R, I, H, hq, hs, w2, s2, offsets, y_perm);
-  return linear(p, few, s);
+  return launch<EP_STORE>(p, path == Path::kTiles ? path : Path::kRows, s);  // h is MXFP4 already
 }
 
 size_t mlp_workspace_bytes(const moe_mlp_desc& d, int64_t R) {
@@ -412,16 +457,16 @@ moe_status forward(const moe_mlp_desc& d, int64_t R, const void* x_perm, const u
 static moe_status grouped_linear(Carver& ws, int E, int64_t R, int K, int N, moe_dtype act, const void* x,
                                  const uint8_t* x_scale, const uint8_t* const* w, const uint8_t* const* w_scale,
                                  const int32_t* offsets, void* y, hipStream_t s) {
-  const bool few = few_rows(R, E);
+  const Path path = choose(R, E, act);
   const uint8_t *xq, *xs;
   const uint8_t *wq[kMaxE], *wqs[kMaxE];
-  moe_status st = rows_in(ws, act, x, x_scale, R, K, few, xq, xs, s);
+  moe_status st = rows_in(ws, act, x, x_scale, R, K, path, xq, xs, s);
   if (st != MOE_OK) return st;
-  st = weights_in(ws, MOE_MXFP4, (const void* const*)w, w_scale, E, N, K, few, wq, wqs, s);
+  st = weights_in(ws, MOE_MXFP4, (const void* const*)w, w_scale, E, N, K, path, wq, wqs, s);
   if (st != MOE_OK || !ws.base) return st;
   Params p;
   fill(p, E, R, K, N, xq, xs, wq, wqs, offsets, y);
-  return linear(p, few, s);
+  return launch<EP_STORE>(p, path, s);
 }
 
 size_t linear_workspace_bytes(int E, int64_t R, int K, int N, moe_dtype act) {

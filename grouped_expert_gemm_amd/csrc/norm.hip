@@ -403,17 +403,22 @@ __global__ __launch_bounds__(TPR) void norm_bwd_kernel(const BwdParams p) {
         p.part[ch * H + (i * TPR + tr) * V + v] = GATE == GATE_CHANNEL && p.plan.pieces > 1 ? own[i][v] : sum[i][v];
 }
 
-// dw (and, for pieces, d_gate): 16 columns a workgroup and 16 threads a column, `par` of them
-// on different groups at a time and 16 / par on the pieces of each; sums in a fixed order
+// dw (and, for pieces, d_gate): 16 columns a workgroup and 64 threads a column (4 a
+// wavefront), `par` <= 16 groups of them on different gate groups at a time and 64 / par on
+// the pieces of each; sums in a fixed order. The partial rows come from other XCDs' caches,
+// so what counts is that all of a column's loads are in flight at once (512 rows x 4096
+// columns: 10.3 us with 16 threads a column).
 template <bool BF16>
-__global__ __launch_bounds__(256) void norm_join_kernel(const float* __restrict__ part, int64_t groups, int64_t pieces,
-                                                        int par, int H, const void* __restrict__ w,
-                                                        const void* __restrict__ gate, float* __restrict__ dw,
-                                                        float* __restrict__ dgate) {
+__global__ __launch_bounds__(1024) void norm_join_kernel(const float* __restrict__ part, int64_t groups, int64_t pieces,
+                                                         int par, int H, const void* __restrict__ w,
+                                                         const void* __restrict__ gate, float* __restrict__ dw,
+                                                         float* __restrict__ dgate) {
   __shared__ float sums[16][17];
-  const int cl = threadIdx.x & 15, q = threadIdx.x >> 4;
+  const int cl = threadIdx.x & 15, q = threadIdx.x >> 4, wave = threadIdx.x >> 6;
   const int col = blockIdx.x * 16 + cl;
-  const int each = 16 / par, gq = q / each, sub = q % each;
+  const int each = 64 / par, gq = q / each, sub = q % each;
+  const int waves = each / 4;                            // wavefronts on one group
+  const bool lead = wave % waves == 0 && (q & 3) == 0;   // the thread that finishes its group's column
   float total = 0.f;
   for (int64_t g0 = 0; g0 < groups; g0 += par) {
     const int64_t g = g0 + gq;
@@ -423,14 +428,19 @@ __global__ __launch_bounds__(256) void norm_join_kernel(const float* __restrict_
 #pragma unroll 8
       for (int64_t i = sub; i < pieces; i += each) s += src[i * H];
     }
-    if (each > 1) {
-      sums[q][cl] = s;
+    // the wavefront's 4 threads of a column, then the group's wavefronts in order
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(s), __float_as_uint(s), false, false);
+    s = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(s), __float_as_uint(s), false, false);
+    s = __uint_as_float(b[0]) + __uint_as_float(b[1]);
+    if (waves > 1) {
+      if ((q & 3) == 0) sums[wave][cl] = s;
       __syncthreads();
-      if (sub == 0)
-        for (int i = 1; i < each; ++i) s += sums[q + i][cl];
+      if (lead)
+        for (int i = 1; i < waves; ++i) s += sums[wave + i][cl];
       __syncthreads();
     }
-    if (sub == 0 && col < H && g < groups) {
+    if (lead && col < H && g < groups) {
       if (gate) {
         const float gv = BF16 ? bf16_to_f32(((const uint16_t*)gate)[g * H + col]) : ((const float*)gate)[g * H + col];
         const float wv = BF16 ? bf16_to_f32(((const uint16_t*)w)[col]) : ((const float*)w)[col];
@@ -441,10 +451,10 @@ __global__ __launch_bounds__(256) void norm_join_kernel(const float* __restrict_
       }
     }
   }
-  sums[q][cl] = total;
+  if (lead) sums[wave][cl] = total;
   __syncthreads();
   if (q == 0 && col < H) {
-    for (int i = 1; i < par; ++i) total += sums[i * each][cl];
+    for (int i = 1; i < par; ++i) total += sums[i * waves][cl];
     dw[col] = total;
   }
 }
@@ -537,7 +547,7 @@ void launch_bwd(const BwdParams& p, int gate_kind, bool bf16, bool vec, float* d
   int par = 1;
   while (par < 16 && par < groups) par *= 2;
   auto kernel = bf16 ? norm_join_kernel<true> : norm_join_kernel<false>;
-  hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, p.part, groups, each, par, p.H, p.w, pieces ? p.gate : nullptr, dw,
+  hipLaunchKernelGGL(kernel, grid, dim3(1024), 0, s, p.part, groups, each, par, p.H, p.w, pieces ? p.gate : nullptr, dw,
                      pieces ? p.dgate : nullptr);
 }
 

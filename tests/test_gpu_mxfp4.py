@@ -143,6 +143,9 @@ LINEAR = [
     (256, 256, [1] * 128),
     (1024, 512, [0] * 63 + [7] + [0] * 36 + [1]),
     (512, 256, [0, 1500, 0, 513]),
+    # 16 rows in all and one more: quantised by the product's own kernel, and before it
+    (768, 512, [0, 5, 1, 0, 7]),
+    (2816, 256, [6, 0, 8]),
     # every number of K steps modulo the tile kernel's ring of five, one step alone among them
     (256, 256, [300]),
     (768, 512, [70, 400]),
@@ -233,6 +236,8 @@ MLP = [
     (256, 256, [1] * 100 + [0] * 28),
     (512, 512, [900, 3]),
     (1024, 1280, [300, 129]),
+    (1280, 768, [3, 0, 12, 1]),
+    (512, 768, [17]),
     (1280, 256, [520]),
 ]
 
