@@ -11,15 +11,16 @@ constexpr int kMaxE = 128;  // experts per call (two pointer tables in the kerne
 
 enum { EP_STORE = 0, EP_SWIGLU = 1 };
 
-// Operands of a grouped product. Scales are in the public row-major layout for the row
-// kernel, in the MFMA's lane order (lane_scales) for the tile kernel.
+// Operands of a grouped product. The row kernel reads the public row-major layouts; the tile
+// kernel reads every scale in the MFMA's lane order (lane_scales) and the rows' codes in
+// fragment order (frag_rows).
 struct Params {
   const uint8_t* tab[kMaxE];    // per-expert weight codes [N][K / 2]
   const uint8_t* tab_s[kMaxE];  // per-expert weight scales
   const uint8_t* q;             // row codes [R][K / 2]
   const uint8_t* q_s;           // row scales
-  void* c;                      // STORE: bf16 [R][N]; SWIGLU: h codes [R][I / 2]
-  uint8_t* c_s;                 // SWIGLU: h's scales, as the down product reads them
+  void* c;                      // STORE: bf16 [R][N]; SWIGLU: h codes [R][I / 2] ...
+  uint8_t* c_s;                 // ... and h's scales, both as the down product reads them
   const int32_t* offsets;
   const float* prob;
   int64_t R;
@@ -65,6 +66,15 @@ moe_status quantize(const void* in_bf16, int64_t rows, int64_t cols, uint8_t* e2
                     bool lanes = false);
 // public-layout scales [rows][cols / 32] of n tensors of one shape -> lane order
 moe_status lane_scales(const uint8_t* const* src, uint8_t* const* dst, int n, int64_t rows, int64_t cols, hipStream_t s);
+
+// Rows for the tile kernel. Fragment order: the 16 bytes of block 2s + g of row r's K values
+// [64 s, 64 s + 64) stand at ((r / 32) * (cols / 64) + s) * 1024 + g * 512 + (r % 32) * 16, so
+// the operand of an MFMA is 1 KiB in a row; the buffer has frag_bytes. Scales in lane order.
+// From bf16 (quantised) or from public-layout codes and scales; cols % 256 == 0.
+inline size_t frag_bytes(int64_t rows, int64_t cols) { return (size_t)((rows + 31) / 32 * 32) * cols / 2; }
+moe_status quantize_frag(const void* in_bf16, int64_t rows, int64_t cols, uint8_t* codes, uint8_t* scales, hipStream_t s);
+moe_status frag_rows(const uint8_t* e2m1, const uint8_t* e8m0, int64_t rows, int64_t cols, uint8_t* codes, uint8_t* scales,
+                     hipStream_t s);
 
 moe_status launch_tile(int ep, const Params& p, hipStream_t s);
 

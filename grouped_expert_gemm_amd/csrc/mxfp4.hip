@@ -88,6 +88,10 @@ moe_status quantize(const void* in_bf16, int64_t rows, int64_t cols, uint8_t* e2
 
 // Row-major scales to lane order: 64 rows x 8 steps a workgroup through LDS, 64 bytes of a
 // row read together, 512 bytes of a step written together.
+__device__ __forceinline__ uint2 lane_order(uint2 v) {  // the 8 scales of a row's 256 values
+  return make_uint2(__builtin_amdgcn_perm(v.y, v.x, 0x06040200u), __builtin_amdgcn_perm(v.y, v.x, 0x07050301u));
+}
+
 struct ScaleTables {
   const uint2* src[kMaxE];
   uint2* dst[kMaxE];
@@ -103,8 +107,7 @@ __global__ __launch_bounds__(256) void lane_scales_kernel(const ScaleTables tabs
   for (int i = 0; i < 2; ++i) {
     const int r = (i * 256 + tid) >> 3, st = tid & 7;
     if (r0 + r < rows && s0 + st < steps) {
-      const uint2 v = src[(r0 + r) * steps + s0 + st];
-      tile[st][r] = make_uint2(__builtin_amdgcn_perm(v.y, v.x, 0x06040200u), __builtin_amdgcn_perm(v.y, v.x, 0x07050301u));
+      tile[st][r] = lane_order(src[(r0 + r) * steps + s0 + st]);
     }
   }
   __syncthreads();
@@ -125,6 +128,76 @@ moe_status lane_scales(const uint8_t* const* src, uint8_t* const* dst, int n, in
   const dim3 grid((unsigned)((rows + 63) / 64), (unsigned)((steps + 7) / 8), (unsigned)n);
   hipLaunchKernelGGL(lane_scales_kernel, grid, dim3(256), 0, s, t, rows, steps);
   return check_launch("MXFP4 scale conversion");
+}
+
+// Rows into fragment order (mxfp4.h): a wavefront takes 8 rows x 256 values, 8 lanes a row, and
+// writes whole 128-byte lines (8 rows of one 16-byte block).
+__global__ __launch_bounds__(256) void quantize_frag_kernel(const uint16_t* __restrict__ in, int64_t rows, int64_t cols,
+                                                            uint8_t* __restrict__ codes, uint2* __restrict__ scales) {
+  const int lane = threadIdx.x & 63, l8 = lane & 7;
+  const int64_t steps = cols / 256;
+  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t step = item % steps, r = item / steps * 8 + (lane >> 3);
+  const bool live = r < rows;
+  uint4 v[4];
+  const uint16_t* src = in + r * cols + step * 256 + l8 * 8;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = live ? *reinterpret_cast<const uint4*>(src + i * 64) : make_uint4(0, 0, 0, 0);
+  uint8_t* dst = codes + ((r >> 5) * (cols / 64) + step * 4) * 1024 + (l8 >> 2) * 512 + (r & 31) * 16 + (l8 & 3) * 4;
+  uint32_t word = 0;  // the scales of block l8 / 4 of the four slices
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    float f[8];
+    uint32_t top = 0;
+#pragma unroll
+    for (int h = 0; h < 4; ++h) {
+      f[2 * h] = __uint_as_float(w[h] << 16);
+      f[2 * h + 1] = __uint_as_float(w[h] & 0xFFFF0000u);
+      top = max(top, max((w[h] << 16) & 0x7FFFFFFFu, w[h] & 0x7FFF0000u));
+    }
+    const int b = scale_byte(lanes_umax<4>(top));
+    word |= (uint32_t)b << (8 * i);
+    if (live) *reinterpret_cast<uint32_t*>(dst + i * 1024) = pack8(f, b);
+  }
+  if (live && (l8 & 3) == 0) reinterpret_cast<uint32_t*>(scales + step * rows + r)[l8 >> 2] = word;
+}
+
+__global__ __launch_bounds__(256) void frag_rows_kernel(const uint8_t* __restrict__ in, const uint2* __restrict__ in_s,
+                                                        int64_t rows, int64_t cols, uint8_t* __restrict__ codes,
+                                                        uint2* __restrict__ scales) {
+  const int lane = threadIdx.x & 63, l8 = lane & 7;
+  const int64_t steps = cols / 256;
+  const int64_t item = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int64_t step = item % steps, r = item / steps * 8 + (lane >> 3);
+  if (r >= rows) return;
+  const uint4 v = *reinterpret_cast<const uint4*>(in + r * (cols / 2) + step * 128 + l8 * 16);
+  *reinterpret_cast<uint4*>(codes + ((r >> 5) * (cols / 64) + step * 4 + (l8 >> 1)) * 1024 + (l8 & 1) * 512 + (r & 31) * 16) = v;
+  if (l8 == 0) scales[step * rows + r] = lane_order(in_s[r * steps + step]);
+}
+
+static moe_status check_items(int64_t rows, int64_t cols, int64_t& blocks) {
+  blocks = ((rows + 7) / 8 * (cols / 256) + 3) / 4;
+  return blocks <= 0x7FFFFFFF ? MOE_OK : fail(MOE_ERR_UNSUPPORTED, "MXFP4 rows: too many values for one launch");
+}
+
+moe_status quantize_frag(const void* in_bf16, int64_t rows, int64_t cols, uint8_t* codes, uint8_t* scales, hipStream_t s) {
+  int64_t blocks;
+  const moe_status st = check_items(rows, cols, blocks);
+  if (st != MOE_OK) return st;
+  hipLaunchKernelGGL(quantize_frag_kernel, dim3((unsigned)blocks), dim3(256), 0, s, (const uint16_t*)in_bf16, rows, cols,
+                     codes, (uint2*)scales);
+  return check_launch("MXFP4 row quantisation");
+}
+
+moe_status frag_rows(const uint8_t* e2m1, const uint8_t* e8m0, int64_t rows, int64_t cols, uint8_t* codes, uint8_t* scales,
+                     hipStream_t s) {
+  int64_t blocks;
+  const moe_status st = check_items(rows, cols, blocks);
+  if (st != MOE_OK) return st;
+  hipLaunchKernelGGL(frag_rows_kernel, dim3((unsigned)blocks), dim3(256), 0, s, e2m1, (const uint2*)e8m0, rows, cols, codes,
+                     (uint2*)scales);
+  return check_launch("MXFP4 row conversion");
 }
 
 __global__ __launch_bounds__(256) void dequantize_kernel(const uint32_t* __restrict__ codes,
@@ -378,19 +451,13 @@ struct Carver {
 static moe_status rows_in(Carver& ws, moe_dtype act, const void* x, const uint8_t* x_scale, int64_t R, int K, Path path,
                           const uint8_t*& q, const uint8_t*& qs, hipStream_t s) {
   q = (const uint8_t*)x, qs = x_scale;
-  if (path == Path::kRowsBF16) return MOE_OK;
-  if (act == MOE_BF16) {
-    uint8_t* c = ws.take((size_t)R * K / 2);
-    uint8_t* b = ws.take((size_t)R * K / 32);
-    q = c, qs = b;
-    return ws.base ? quantize(x, R, K, c, b, s, path == Path::kTiles) : MOE_OK;
-  }
-  if (path == Path::kRows) return MOE_OK;
+  if (path == Path::kRowsBF16 || (path == Path::kRows && act != MOE_BF16)) return MOE_OK;
+  uint8_t* c = ws.take(path == Path::kTiles ? frag_bytes(R, K) : (size_t)R * K / 2);
   uint8_t* b = ws.take((size_t)R * K / 32);
-  const uint8_t* src[1] = {x_scale};
-  uint8_t* dst[1] = {b};
-  qs = b;
-  return ws.base ? lane_scales(src, dst, 1, R, K, s) : MOE_OK;
+  q = c, qs = b;
+  if (!ws.base) return MOE_OK;
+  if (path == Path::kRows) return quantize(x, R, K, c, b, s);
+  return act == MOE_BF16 ? quantize_frag(x, R, K, c, b, s) : frag_rows((const uint8_t*)x, x_scale, R, K, c, b, s);
 }
 
 static moe_status weights_in(Carver& ws, moe_dtype wt, const void* const* w, const uint8_t* const* scale, int E, int N,
@@ -422,7 +489,7 @@ static moe_status mlp(Carver& ws, const moe_mlp_desc& d, int64_t R, const void* 
                       hipStream_t s) {
   const int E = d.E, H = d.H, I = d.I;
   const Path path = choose(R, E, d.act);
-  uint8_t* hq = ws.take((size_t)R * I / 2);
+  uint8_t* hq = ws.take(path == Path::kTiles ? frag_bytes(R, I) : (size_t)R * I / 2);
   uint8_t* hs = ws.take((size_t)R * I / 32);
   const uint8_t *xq, *xs;
   const uint8_t *w1[kMaxE], *s1[kMaxE], *w2[kMaxE], *s2[kMaxE];
