@@ -48,15 +48,15 @@ __device__ __forceinline__ int scale_byte(uint32_t u) {
 }
 
 // Eight E2M1 codes (value 0 in the low nibble) of f / 2^(byte - 127), |f| <= 6 * 2^(byte - 127):
-// ldexp is exact (or far below the smallest code's half), the conversion rounds to nearest,
-// ties to the even code, and keeps the sign of zero.
+// the conversion divides by its scale operand, a power of two, rounds to nearest, ties to the
+// even code, and keeps the sign of zero.
 __device__ __forceinline__ uint32_t pack8(const float* f, int byte) {
-  const int s = 127 - byte;
+  const float s = __uint_as_float(byte ? (uint32_t)byte << 23 : 0x00400000u);
   uint32_t w = 0;
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, ldexpf(f[0], s), ldexpf(f[1], s), 1.f, 0);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, ldexpf(f[2], s), ldexpf(f[3], s), 1.f, 1);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, ldexpf(f[4], s), ldexpf(f[5], s), 1.f, 2);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, ldexpf(f[6], s), ldexpf(f[7], s), 1.f, 3);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[0], f[1], s, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[2], f[3], s, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[4], f[5], s, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[6], f[7], s, 3);
   return byte == 255 ? 0u : w;
 }
 

@@ -13,8 +13,7 @@
 // What the copies have to cover is the latency past L2, about 2 us when every CU streams:
 // a version with both operands in LDS had 0.75 and 1.6 steps (of ~1 us) of lead and ran at
 // 1.74 us a step; MFMA alone is 1.07 us at 1.9 GHz.
-// The next tile's first loads are issued before a tile's epilogue, whose stores are then
-// never waited for ahead of the next tile's second step.
+// The next tile's first loads are issued between the blocks of a tile's epilogue.
 //
 // The K loop runs all but the last three steps in groups of four and RES more, so every ring
 // slot is a constant; the last three issue no copies (an expert's product of fewer than three
@@ -74,35 +73,48 @@ void grouped_gemm_tile_kernel(const Params prm) {
   };
 
   // ---------------- tiles ----------------
-  // expert-major, row tiles in groups of at most 16 (tile_in_expert); the offsets are made a
-  // nondecreasing sequence inside [0, R] on the way
-  auto clamp_off = [&](int v, int prev) -> int {
-    v = v < prev ? prev : v;
-    return v > R ? R : v;
-  };
-  auto tiles_of = [&](int rows) -> int { return ((rows + kBM - 1) / kBM) * n_tiles; };
-  int e_w = 0, ob = 0, oe = clamp_off(load_const(prm.offsets, 1), 0), ts_w = 0;
-  int nt_w = tiles_of(oe);
+  // expert-major, row tiles in groups of at most 16 (tile_in_expert). Lane l holds experts l and
+  // l + 64: their rows (offsets made a nondecreasing sequence inside [0, R]) and first tile, so
+  // a tile is found without a memory access.
+  struct Span {
+    int beg, end, first;
+  } span[2];
+  int total = 0;
+  for (int h = 0, rows_before = 0; h < 2; ++h) {
+    const int e = h * 64 + lane;
+    int end = min(max(e < E ? prm.offsets[e + 1] : 0, rows_before), R);
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int o = __shfl_up(end, d, 64);
+      if (lane >= d) end = max(end, o);
+    }
+    int beg = __shfl_up(end, 1, 64);
+    if (lane == 0) beg = rows_before;
+    const int tiles = e < E ? (end - beg + kBM - 1) / kBM * n_tiles : 0;
+    int upto = tiles;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int o = __shfl_up(upto, d, 64);
+      if (lane >= d) upto += o;
+    }
+    span[h] = Span{beg, end, total + upto - tiles};
+    rows_before = __builtin_amdgcn_readlane(end, 63);
+    total += __builtin_amdgcn_readlane(upto, 63);
+  }
   struct Tile {
     int e, nt, row, row_end;
   };
-  auto find_tile = [&](int t, Tile& tile) -> bool {  // t never decreases from call to call
-    while (e_w < E && t >= ts_w + nt_w) {
-      ts_w += nt_w;
-      ++e_w;
-      ob = oe;
-      if (e_w < E) {
-        oe = clamp_off(load_const(prm.offsets, e_w + 1), ob);
-        nt_w = tiles_of(oe - ob);
-      }
-    }
-    if (e_w >= E) return false;
+  auto find_tile = [&](int t, Tile& tile) -> bool {
+    if (t >= total) return false;
+    // of experts that start at one tile only the last has any
+    const int e = __popcll(__ballot(lane < E && span[0].first <= t)) + __popcll(__ballot(lane + 64 < E && span[1].first <= t)) - 1;
+    const bool up = e >= 64;
+    const int beg = __builtin_amdgcn_readlane(up ? span[1].beg : span[0].beg, e & 63);
+    const int end = __builtin_amdgcn_readlane(up ? span[1].end : span[0].end, e & 63);
+    const int first = __builtin_amdgcn_readlane(up ? span[1].first : span[0].first, e & 63);
     int mt, nt;
-    tile_in_expert(t - ts_w, (oe - ob + kBM - 1) / kBM, n_tiles, mt, nt);
-    tile.e = __builtin_amdgcn_readfirstlane(e_w);
-    tile.nt = __builtin_amdgcn_readfirstlane(nt);
-    tile.row = __builtin_amdgcn_readfirstlane(ob + mt * kBM);
-    tile.row_end = __builtin_amdgcn_readfirstlane(oe);
+    tile_in_expert(t - first, (end - beg + kBM - 1) / kBM, n_tiles, mt, nt);
+    tile = Tile{e, __builtin_amdgcn_readfirstlane(nt), __builtin_amdgcn_readfirstlane(beg + mt * kBM), end};
     return true;
   };
 
@@ -198,6 +210,8 @@ void grouped_gemm_tile_kernel(const Params prm) {
   using C3 = std::integral_constant<int, 3>;
   using C4 = std::integral_constant<int, 4>;
   using C6 = std::integral_constant<int, 6>;
+  using C5 = std::integral_constant<int, 5>;
+  using C7 = std::integral_constant<int, 7>;
   using C8 = std::integral_constant<int, 8>;
   using C12 = std::integral_constant<int, 12>;
   Scales r0, r1, r2;  // of steps kt, kt + 1, kt + 2
@@ -234,19 +248,23 @@ void grouped_gemm_tile_kernel(const Params prm) {
     r0 = r1;
     r1 = r2;
   };
-  auto prologue = [&]() {
-    load_scales(0, r0);
-    load_Q(0, C0{}, C0{});
-    copy_P(0, C0{}, C0{}, C8{});
-    load_Q(0, C0{}, C1{});
-    load_Q(0, C0{}, C2{});
-    load_Q(0, C0{}, C3{});
-    copy_P(1, C1{}, C0{}, C8{});
-    load_scales(1, r1);
-    load_Q(1, C1{}, C0{});
-    load_Q(1, C1{}, C1{});
-    load_Q(1, C1{}, C2{});
-    copy_P(2, C2{}, C0{}, C8{});
+  // a tile's first loads, in seven parts
+  auto first_loads = [&](auto I) {
+    constexpr int i = decltype(I)::value;
+    if constexpr (i == 0) load_scales(0, r0);
+    if constexpr (i == 1) copy_P(0, C0{}, C0{}, C8{});
+    if constexpr (i == 2) static_for<4>([&](auto S) { load_Q(0, C0{}, S); });
+    if constexpr (i == 3) copy_P(1, C1{}, C0{}, C8{});
+    if constexpr (i == 4) load_scales(1, r1);
+    if constexpr (i == 5) static_for<3>([&](auto S) { load_Q(1, C1{}, S); });
+    if constexpr (i == 6) copy_P(2, C2{}, C0{}, C8{});
+  };
+  // parts [A, B), in that order among the operations around them
+  auto parts = [&](auto A, auto B) {
+    static_for<decltype(B)::value - decltype(A)::value>([&](auto I) {
+      first_loads(std::integral_constant<int, decltype(A)::value + decltype(I)::value>{});
+    });
+    __builtin_amdgcn_sched_barrier(0);
   };
 
   Tile cur;
@@ -254,7 +272,7 @@ void grouped_gemm_tile_kernel(const Params prm) {
   int t = first;
   if (!find_tile(t, cur)) return;
   set_tile(cur);
-  prologue();
+  parts(C0{}, C7{});
   wait_vm<0>();
   bool more = true;
   while (more) {
@@ -292,8 +310,6 @@ void grouped_gemm_tile_kernel(const Params prm) {
     more = find_tile(t, next);
     set_tile(next);  // past the last tile: this one's first loads again, unused
     __builtin_amdgcn_sched_barrier(0);
-    prologue();
-    __builtin_amdgcn_sched_barrier(0);
 
     // ---------------- epilogue ----------------
     int ln = lane;
@@ -315,6 +331,9 @@ void grouped_gemm_tile_kernel(const Params prm) {
       for (int sm = 0; sm < 2; ++sm)
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
+          if (sm == 0 && b == 0) parts(C0{}, C3{});
+          if (sm == 0 && b == 1) parts(C3{}, C5{});
+          if (sm == 1 && b == 0) parts(C5{}, C7{});
 #pragma unroll
           for (int sq = 0; sq < 4; ++sq)
 #pragma unroll
@@ -348,6 +367,11 @@ void grouped_gemm_tile_kernel(const Params prm) {
         uint32_t bytes[4];
 #pragma unroll
         for (int sn = 0; sn < 4; ++sn) {
+          if (sm == 0 && sn == 0) parts(C0{}, C2{});
+          if (sm == 0 && sn == 1) parts(C2{}, C3{});
+          if (sm == 0 && sn == 2) parts(C3{}, C4{});
+          if (sm == 0 && sn == 3) parts(C4{}, C6{});
+          if (sm == 1 && sn == 0) parts(C6{}, C7{});
           // a 32-value block of h: columns 8j + 4 ehi + (0..3) here, the others in lane ^ 32
           float h[16];
           uint32_t top = 0;
@@ -376,8 +400,9 @@ void grouped_gemm_tile_kernel(const Params prm) {
       }
     }
     cur = next;
-    // the next tile's first loads, but not the stores above, which are younger
-    wait_vm<EP == EP_STORE ? 32 : 10>();
+    // the next tile's first loads have landed; the stores of the last two blocks (four and the
+    // scales' with SwiGLU) are younger
+    wait_vm<EP == EP_STORE ? 16 : 5>();
   }
   wait_vm<0>();
 }
