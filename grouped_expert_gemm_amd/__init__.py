@@ -53,24 +53,32 @@ def _need_cuda(*ts):
 
 def _need(fn, ref, *ts):
     """Every given tensor on ref's GPU and contiguous."""
-    dev = ref.device
+    dev = ref.get_device()   # -1 on the CPU
     for t in (ref, *ts):
         if t is not None:
-            if t.device != dev or not t.is_cuda:
+            if t.get_device() != dev or dev < 0:
                 raise ValueError(f"{fn}: tensors must live on one GPU")
             if not t.is_contiguous():
                 raise ValueError(f"{fn}: tensors must be contiguous")
 
 
-def _launch(fn, dev, *args):
-    """Call entry point fn (its last argument, the stream, added) with dev as the current device."""
-    stream = torch._C._cuda_getCurrentRawStream(dev.index)  # torch.cuda.current_stream(dev).cuda_stream, 2 us faster
-    if torch.cuda.current_device() == dev.index:
-        status = getattr(lib(), fn)(*args, stream)
+def _a(t):
+    """A tensor's address for a pointer argument (None: NULL)."""
+    return t.data_ptr() if t is not None else None
+
+
+def _launch(fn, t, *args):
+    """Call entry point fn (its last argument, the stream, added) with t's GPU as the current device."""
+    L = lib()
+    dev = t.get_device()
+    stream = torch._C._cuda_getCurrentRawStream(dev)  # torch.cuda.current_stream(dev).cuda_stream, 2 us faster
+    if torch.cuda.current_device() == dev:
+        status = getattr(L, fn)(*args, stream)
     else:
         with torch.cuda.device(dev):
-            status = getattr(lib(), fn)(*args, stream)
-    check(fn, status)
+            status = getattr(L, fn)(*args, stream)
+    if status:
+        check(fn.removesuffix("_tables"), status)
 
 
 def _workspace(nbytes, device):
@@ -167,9 +175,10 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, balance_coef:
     counts = torch.empty((T // L, E), dtype=torch.int32, device=dev)
     tokens = torch.empty(T // L + 1, dtype=torch.int32, device=dev)
     loss = torch.empty(3, dtype=torch.float32, device=dev)
-    ws = _workspace(workspace_size(_lib.MOE_OP_BALANCE_LOSS, None, L, T, E), dev)
-    _launch("moe_balance_loss", dev, _p(logits), _p(topk_idx), _p(mask), T, E, topk_idx.shape[1], L, balance_coef,
-            z_coef, _p(counts), _p(tokens), _p(loss), _p(ws), ws.numel())
+    need = workspace_size(_lib.MOE_OP_BALANCE_LOSS, None, L, T, E)
+    ws = _workspace(need, dev) if need else None
+    _launch("moe_balance_loss", logits, _a(logits), _a(topk_idx), _a(mask), T, E, topk_idx.shape[1], L, balance_coef,
+            z_coef, _a(counts), _a(tokens), _a(loss), _a(ws), need)
     return loss, counts, tokens
 
 
@@ -192,8 +201,8 @@ def moe_balance_loss_bwd(logits: torch.Tensor, counts: torch.Tensor, tokens: tor
         raise ValueError("moe_balance_loss_bwd: logits and d_loss must be float32, counts and tokens the forward's")
     if d_logits is None:
         d_logits = torch.empty_like(logits)
-    _launch("moe_balance_loss_bwd", logits.device, _p(logits), _p(counts), _p(tokens), _p(mask), T, E, k, L,
-            balance_coef, z_coef, _p(d_loss), _p(d_logits_in), _p(d_logits))
+    _launch("moe_balance_loss_bwd", logits, _a(logits), _a(counts), _a(tokens), _a(mask), T, E, k, L,
+            balance_coef, z_coef, _a(d_loss), _a(d_logits_in), _a(d_logits))
     return d_logits
 
 
@@ -237,7 +246,7 @@ def moe_pre_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, save_
         raise ValueError("moe_pre_norm: weight must be [H]")
     y = torch.empty_like(x)
     rstd = torch.empty(T, dtype=torch.float32, device=x.device) if save_rstd else None
-    _launch("moe_pre_norm", x.device, _p(x), _p(weight), dt, T, H, eps, _p(y), _p(rstd))
+    _launch("moe_pre_norm", x, _a(x), _a(weight), dt, T, H, eps, _a(y), _a(rstd))
     return (y, rstd) if save_rstd else y
 
 
@@ -261,8 +270,8 @@ def moe_pre_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, rs
         dx = torch.empty_like(x)
     dw = torch.empty(H, dtype=torch.float32, device=x.device)
     ws = _norm_workspace(T, H, _lib.MOE_GATE_NONE, 1, x.device)
-    _launch("moe_pre_norm_bwd", x.device, _p(dy), _p(x), _p(weight), _p(rstd), _p(dx_in), dx_in_scale, dt, T, H,
-            _p(dx), _p(dw), _p(ws), ws.numel())
+    _launch("moe_pre_norm_bwd", x, _a(dy), _a(x), _a(weight), _a(rstd), _a(dx_in), dx_in_scale, dt, T, H,
+            _a(dx), _a(dw), _a(ws), ws.numel())
     return dx, dw
 
 
@@ -294,9 +303,9 @@ def moe_post_norm(y: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, row_id
         r["y_next"] = torch.empty_like(x)
         if save_for_bwd:
             r["rstd_next"] = torch.empty(T, dtype=torch.float32, device=dev)
-    _launch("moe_post_norm", dev, _p(y), _p(row_id_map), k, _p(x), _p(weight), kind, _p(gate), group, residual_scale,
-            _p(next_weight), dt, T, H, eps, _p(r["out"]), _p(r.get("c")), _p(r.get("rstd")), _p(r.get("y_next")),
-            _p(r.get("rstd_next")))
+    _launch("moe_post_norm", x, _a(y), _a(row_id_map), k, _a(x), _a(weight), kind, _a(gate), group, residual_scale,
+            _a(next_weight), dt, T, H, eps, _a(r["out"]), _a(r.get("c")), _a(r.get("rstd")), _a(r.get("y_next")),
+            _a(r.get("rstd_next")))
     return r
 
 
@@ -322,8 +331,8 @@ def moe_post_norm_bwd(dout: torch.Tensor, c: torch.Tensor, rstd: torch.Tensor, w
     if gate is not None:
         dgate = (torch.empty if T > 0 else torch.zeros)(gate.shape, dtype=torch.float32, device=dev)
     ws = _norm_workspace(T, H, kind, group, dev)
-    _launch("moe_post_norm_bwd", dev, _p(dout), _p(c), _p(rstd), _p(weight), kind, _p(gate), group, _p(row_id_map), k,
-            dt, T, H, _p(dy), _p(dw), _p(dgate), _p(ws), ws.numel())
+    _launch("moe_post_norm_bwd", dout, _a(dout), _a(c), _a(rstd), _a(weight), kind, _a(gate), group, _a(row_id_map), k,
+            dt, T, H, _a(dy), _a(dw), _a(dgate), _a(ws), ws.numel())
     r = dict(dy=dy, dweight=dw)
     if gate is not None:
         r["dgate"] = dgate
@@ -403,7 +412,7 @@ def mxfp4_quantize(x: torch.Tensor):
     rows = x.numel() // cols if cols else 0
     codes = torch.empty((*x.shape[:-1], cols // 2), dtype=torch.uint8, device=x.device)
     scales = torch.empty((*x.shape[:-1], cols // 32), dtype=torch.uint8, device=x.device)
-    _launch("mxfp4_quantize", x.device, _p(x), rows, cols, _p(codes), _p(scales))
+    _launch("mxfp4_quantize", x, _a(x), rows, cols, _a(codes), _a(scales))
     return codes, scales
 
 
@@ -416,7 +425,7 @@ def mxfp4_dequantize(codes: torch.Tensor, scales: torch.Tensor) -> torch.Tensor:
     cols = 2 * codes.shape[-1]
     rows = codes.numel() // codes.shape[-1] if cols else 0
     out = torch.empty((*codes.shape[:-1], cols), dtype=torch.bfloat16, device=codes.device)
-    _launch("mxfp4_dequantize", codes.device, _p(codes), _p(scales), rows, cols, _p(out))
+    _launch("mxfp4_dequantize", codes, _a(codes), _a(scales), rows, cols, _a(out))
     return out
 
 
@@ -549,25 +558,22 @@ def _experts(w):
 
 
 def _weight_table(fn, w, dev):
-    """Per-expert weights, one tensor [E, ...] or a list -> (pointer table, what keeps it alive, E, shape, dtype).
-    One tensor's pointers are a stride apart, so a call does not touch E slices."""
+    """Per-expert weights, one tensor [E, ...] or a list -> (pointer table, E, shape, dtype). One
+    tensor's pointers are a stride apart, so a call does not touch E slices."""
     if isinstance(w, torch.Tensor):
-        if w.device != dev or not w.is_contiguous():
-            raise ValueError(f"{fn}: weights must be contiguous and live on the rows' GPU")
+        if w.get_device() != dev or not w.is_contiguous() or w.numel() == 0:
+            raise ValueError(f"{fn}: weights must be contiguous, not empty, and live on the rows' GPU")
         E, *shape = w.shape
-        base, stride = w.data_ptr(), w.stride(0) * w.element_size()
-        if E == 0 or stride == 0:
-            raise ValueError(f"{fn}: empty weights")
-        keep = torch.arange(base, base + E * stride, stride, dtype=torch.int64, device="cpu")
-        return _lib.strided_table(keep), keep, E, tuple(shape), w.dtype
+        table = (ctypes.c_void_p * E)()
+        lib().moe_pointer_table(w.data_ptr(), w.stride(0) * w.element_size(), E, table)
+        return table, E, tuple(shape), w.dtype
     w = list(w)
     if not w:
         raise ValueError(f"{fn}: no weights")
     for t in w:
-        if t.device != dev or not t.is_contiguous() or t.shape != w[0].shape or t.dtype != w[0].dtype:
+        if t.get_device() != dev or not t.is_contiguous() or t.shape != w[0].shape or t.dtype != w[0].dtype:
             raise ValueError(f"{fn}: the experts' weights must be contiguous, alike, and live on the rows' GPU")
-    table, keep = ptr_table([t.data_ptr() for t in w])
-    return table, keep, len(w), tuple(w[0].shape), w[0].dtype
+    return (ctypes.c_void_p * len(w))(*[t.data_ptr() for t in w]), len(w), tuple(w[0].shape), w[0].dtype
 
 
 def _mxfp4_rows(fn, x, x_scale):
@@ -584,19 +590,19 @@ def _mxfp4_rows(fn, x, x_scale):
 
 def _mxfp4_weight(fn, w, scale, N, K, dev, masters=False):
     """Tables of E weights [N, K] given as MXFP4 codes [E, N, K/2] with scales [E, N, K/32] (or, where
-    masters are taken, bf16 [E, N, K]) -> (codes table, scale table, storage dtype, E, N, what to keep)."""
-    t, keep, E, shape, dtype = _weight_table(fn, w, dev)
+    masters are taken, bf16 [E, N, K]) -> (codes table, scale table, storage dtype, E, N)."""
+    t, E, shape, dtype = _weight_table(fn, w, dev)
     if masters and dtype == torch.bfloat16:
         if len(shape) != 2 or shape[1] != K or (N is not None and shape[0] != N):
             raise ValueError(f"{fn}: weight shapes do not fit the rows")
-        return t, None, MOE_BF16, E, shape[0], keep
+        return t, None, MOE_BF16, E, shape[0]
     if scale is None:
         raise ValueError(f"{fn}: MXFP4 weights need their scales")
-    ts, keep_s, Es, sshape, sdtype = _weight_table(fn, scale, dev)
+    ts, Es, sshape, sdtype = _weight_table(fn, scale, dev)
     if dtype != torch.uint8 or sdtype != torch.uint8 or Es != E or len(shape) != 2 or shape[1] * 2 != K \
             or sshape != (shape[0], K // 32) or (N is not None and shape[0] != N):
         raise ValueError(f"{fn}: MXFP4 weights must be uint8 codes [N, K/2] with uint8 scales [N, K/32] per expert")
-    return t, ts, MOE_MXFP4, E, shape[0], (keep, keep_s)
+    return t, ts, MOE_MXFP4, E, shape[0]
 
 
 def _check_offsets(fn, offsets, E):
@@ -613,17 +619,17 @@ def moe_grouped_linear_mxfp4(x: torch.Tensor, w, w_scale, offsets: torch.Tensor,
     fn = "moe_grouped_linear_mxfp4"
     _need(fn, x, offsets, x_scale, out, workspace)
     act, K = _mxfp4_rows(fn, x, x_scale)
-    dev, R = x.device, x.shape[0]
-    t, ts, _, E, N, keep = _mxfp4_weight(fn, w, w_scale, None, K, dev)
+    R = x.shape[0]
+    t, ts, _, E, N = _mxfp4_weight(fn, w, w_scale, None, K, x.get_device())
     _check_offsets(fn, offsets, E)
     if out is None:
-        out = torch.empty((R, N), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((R, N), dtype=torch.bfloat16, device=x.device)
     elif out.dtype != torch.bfloat16 or out.shape != (R, N):
         raise ValueError(f"{fn}: out must be bfloat16 [R, N]")
     need = workspace_size(_lib.MOE_OP_LINEAR_MXFP4, MlpDesc(E, K, N, MOE_MXFP4, act, MOE_MXFP4, 0), R)
-    ws = workspace if workspace is not None and workspace.numel() >= need else _workspace(need, dev)
-    _launch(fn, dev, E, R, K, N, act, _p(x), _p(x_scale), t, ts, _p(offsets), _p(out), _p(ws), ws.numel())
-    del keep
+    if workspace is None or workspace.numel() < need:
+        workspace = _workspace(need, x.device) if need else None
+    _launch(fn, x, E, R, K, N, act, _a(x), _a(x_scale), t, ts, _a(offsets), _a(out), _a(workspace), need)
     return out
 
 
@@ -631,23 +637,23 @@ def _mlp_fwd_mxfp4(x, w_gate_up, w_down, offsets, prob, save_for_bwd, x_scale, w
     fn = "moe_grouped_mlp_fwd"
     _need(fn, x, offsets, prob, x_scale, out, workspace)
     act, H = _mxfp4_rows(fn, x, x_scale)
-    dev, R = x.device, x.shape[0]
-    t1, s1, wt, E, twoI, keep1 = _mxfp4_weight(fn, w_gate_up, w1_scale, None, H, dev, masters=True)
+    dev, R = x.get_device(), x.shape[0]
+    t1, s1, wt, E, twoI = _mxfp4_weight(fn, w_gate_up, w1_scale, None, H, dev, masters=True)
     I = twoI // 2
-    t2, s2, wt2, E2, _, keep2 = _mxfp4_weight(fn, w_down, w2_scale, H, I, dev, masters=True)
+    t2, s2, wt2, E2, _ = _mxfp4_weight(fn, w_down, w2_scale, H, I, dev, masters=True)
     _check_offsets(fn, offsets, E)
     if wt2 != wt or E2 != E or twoI % 2 or prob.dtype != torch.float32 or prob.numel() != R:
         raise ValueError(f"{fn}: weights must share E and storage, prob_perm must be float32 [R]")
     if out is None:
-        out = torch.empty((R, H), dtype=torch.bfloat16, device=dev)
+        out = torch.empty((R, H), dtype=torch.bfloat16, device=x.device)
     elif out.dtype != torch.bfloat16 or out.shape != (R, H):
         raise ValueError(f"{fn}: out must be bfloat16 [R, H]")
     desc = MlpDesc(E, H, I, MOE_MXFP4, act, wt, int(save_for_bwd))
     need = workspace_size(_lib.MOE_OP_MLP_FWD, desc, R)
-    ws = workspace if workspace is not None and workspace.numel() >= need else _workspace(need, dev)
-    _launch(fn, dev, ctypes.byref(desc), R, _p(x), _p(x_scale), t1, t2, s1, s2, _p(offsets), _p(prob), _p(out), None,
-            None, _p(ws), ws.numel())
-    del keep1, keep2
+    if workspace is None or workspace.numel() < need:
+        workspace = _workspace(need, x.device) if need else None
+    _launch("moe_grouped_mlp_fwd_tables", x, ctypes.byref(desc), R, _a(x), _a(x_scale), t1, t2, s1, s2, _a(offsets),
+            _a(prob), _a(out), None, None, _a(workspace), need)
     return out
 
 

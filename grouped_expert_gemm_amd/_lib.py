@@ -27,7 +27,7 @@ EXPORTS = (
     "moe_grouped_mlp_fwd", "moe_grouped_mlp_bwd", "moe_grouped_linear", "moe_grouped_gate_up_swiglu",
     "moe_balance_loss", "moe_balance_loss_bwd",
     "moe_pre_norm", "moe_pre_norm_bwd", "moe_post_norm", "moe_post_norm_bwd",
-    "mxfp4_quantize", "mxfp4_dequantize", "moe_grouped_linear_mxfp4",
+    "mxfp4_quantize", "mxfp4_dequantize", "moe_grouped_linear_mxfp4", "moe_pointer_table",
     "moe_workspace_size",
     "moe_status_str", "moe_last_error",
 )
@@ -92,13 +92,19 @@ def _declare(lib):
         "moe_post_norm_bwd": [vp, vp, vp, vp, c_int, vp, i64, vp, c_int, c_int, i64, c_int, vp, vp, vp, vp, sz, vp],
         "mxfp4_quantize": [vp, i64, i64, vp, vp, vp],
         "mxfp4_dequantize": [vp, vp, i64, i64, vp, vp],
-        "moe_grouped_linear_mxfp4": [c_int, i64, c_int, c_int, c_int, vp, vp, PP, PP, vp, vp, vp, sz, vp],
+        "moe_grouped_linear_mxfp4": [c_int, i64, c_int, c_int, c_int, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+        "moe_pointer_table": [vp, i64, c_int, vp],
         "moe_workspace_size": [c_int, ctypes.POINTER(MlpDesc), i64, i64, c_int, c_int, ctypes.POINTER(sz)],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = c_int
+    # the same entry point taking its tables' addresses as plain numbers, which skips four casts a call
+    fn = lib["moe_grouped_mlp_fwd"]
+    fn.argtypes = [vp if t is PP else t for t in sig["moe_grouped_mlp_fwd"]]
+    fn.restype = c_int
+    lib.moe_grouped_mlp_fwd_tables = fn
 
 
 def lib():
@@ -120,11 +126,6 @@ def check(fn_name: str, status: int):
     if status != MOE_OK:
         L = lib()
         raise MoeError(fn_name, status, f"{L.moe_status_str(status).decode()}: {L.moe_last_error().decode()}")
-
-
-def strided_table(ptrs):
-    """ptr_table of a contiguous int64 CPU tensor of addresses (which has to outlive the call)."""
-    return ctypes.cast(ptrs.data_ptr(), PP)
 
 
 def ptr_table(ptrs):

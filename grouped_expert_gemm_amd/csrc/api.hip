@@ -107,3 +107,9 @@ extern "C" moe_status moe_workspace_size(moe_op op, const moe_mlp_desc* desc, in
   }
   return fail(MOE_ERR_INVALID_ARG, "moe_workspace_size: unknown op");
 }
+
+extern "C" moe_status moe_pointer_table(const void* base, int64_t stride, int n, const void** table) {
+  if (n < 0 || (n > 0 && (!base || !table))) return fail(MOE_ERR_INVALID_ARG, "moe_pointer_table: n < 0 or NULL pointer");
+  for (int i = 0; i < n; ++i) table[i] = (const uint8_t*)base + (int64_t)i * stride;
+  return MOE_OK;
+}

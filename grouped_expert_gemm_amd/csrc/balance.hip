@@ -26,7 +26,6 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;          // tokens of a group whose loads are in flight together
 constexpr int kMinTokens = 2;       // tokens of a group that are worth a workgroup and a partial sum of their own
 constexpr int64_t kTargetWgs = 1024;
 
@@ -170,7 +169,7 @@ __device__ __forceinline__ void finish_sequence(const SeqOut& o, int64_t s, cons
 }
 
 // kDirect: one workgroup a sequence, which finishes it itself
-template <int L, bool VEC, bool kDirect>
+template <int L, bool VEC, bool kDirect, int U>
 __global__ __launch_bounds__(kThreads) void balance_fwd_kernel(const float* __restrict__ logits,
                                                                const int32_t* __restrict__ idx,
                                                                const uint8_t* __restrict__ mask, int64_t seq_len,
@@ -191,12 +190,12 @@ __global__ __launch_bounds__(kThreads) void balance_fwd_kernel(const float* __re
   float ps[4] = {0.f, 0.f, 0.f, 0.f};
   float zs = 0.f;
   int n = 0;
-  for (int64_t i0 = 0; i0 < len; i0 += (int64_t)G * kUnroll) {  // the same trip count in every lane
-    float v[kUnroll][4];
-    int32_t id[kUnroll][4];  // this lane's slots j, j + L, ... (k <= E <= 4 L); -1: none
-    bool live[kUnroll];
+  for (int64_t i0 = 0; i0 < len; i0 += (int64_t)G * U) {  // the same trip count in every lane
+    float v[U][4];
+    int32_t id[U][4];  // this lane's slots j, j + L, ... (k <= E <= 4 L); -1: none
+    bool live[U];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < U; ++u) {
       const int64_t i = i0 + u * G + g;
       live[u] = i < len && (!mask || mask[beg + i] != 0);
       if (live[u]) load_row<L, VEC>(logits + (beg + i) * E, j, E, v[u]);
@@ -205,7 +204,7 @@ __global__ __launch_bounds__(kThreads) void balance_fwd_kernel(const float* __re
       for (int q = 0; q < 4; ++q) id[u][q] = live[u] && j + q * L < k ? idx[(beg + i) * k + j + q * L] : -1;
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < U; ++u) {
       float lse;
       const bool ok = softmax_row<L>(v[u], lse) && live[u];
       if (ok) {
@@ -390,7 +389,7 @@ __global__ __launch_bounds__(kThreads) void balance_mean_kernel(SeqOut o) {
 }
 
 // d_in may be d_logits itself: each value is read and written by the same lane
-template <int L, bool VEC>
+template <int L, bool VEC, int U>
 __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(const float* __restrict__ logits,
                                                                const int32_t* __restrict__ counts,
                                                                const int32_t* __restrict__ tokens,
@@ -414,11 +413,11 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(const float* __re
   }
   const float scale = n > 0 ? (d_loss ? *d_loss : 1.f) / ((float)seqs * (float)n) : 0.f;
   const float b2 = 2.f * b;
-  for (int64_t i0 = 0; i0 < len; i0 += (int64_t)G * kUnroll) {
-    float v[kUnroll][4], w[kUnroll][4];
-    bool in[kUnroll], live[kUnroll];
+  for (int64_t i0 = 0; i0 < len; i0 += (int64_t)G * U) {
+    float v[U][4], w[U][4];
+    bool in[U], live[U];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < U; ++u) {
       const int64_t i = i0 + u * G + g;
       in[u] = i < len;
       live[u] = in[u] && n > 0 && (!mask || mask[beg + i] != 0);
@@ -428,7 +427,7 @@ __global__ __launch_bounds__(kThreads) void balance_bwd_kernel(const float* __re
       else w[u][0] = w[u][1] = w[u][2] = w[u][3] = 0.f;
     }
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
+    for (int u = 0; u < U; ++u) {
       float lse, share = 0.f;
       const bool ok = softmax_row<L>(v[u], lse) && live[u];
 #pragma unroll
@@ -457,12 +456,20 @@ __global__ void balance_empty_kernel(float* loss, int32_t* tokens) {
   if (threadIdx.x == 3) tokens[0] = 0;
 }
 
-// f(lanes of a group, 16-byte rows) as compile-time constants
+// f(lanes of a group, 16-byte rows, tokens of a group in flight) as compile-time constants. Four
+// tokens in flight pay off where a workgroup's run is long enough to repeat them (131072 x 256:
+// forward 50 -> 43 us), and only cost registers in runs of two to seven tokens a group (16384 x
+// 128: forward 6.0 us with two, 8.1 with four).
 template <typename F>
-void dispatch(int E, bool vec, F&& f) {
+void dispatch(int E, bool vec, int64_t chunk, F&& f) {
+  const bool long_run = chunk * group_lanes(E) >= 8 * kThreads;
   auto with = [&](auto Lc) {
-    if (vec) f(Lc, std::true_type{});
-    else f(Lc, std::false_type{});
+    auto then = [&](auto Vc) {
+      if (long_run) f(Lc, Vc, std::integral_constant<int, 4>{});
+      else f(Lc, Vc, std::integral_constant<int, 2>{});
+    };
+    if (vec) then(std::true_type{});
+    else then(std::false_type{});
   };
   switch (group_lanes(E)) {
     case 1: with(std::integral_constant<int, 1>{}); break;
@@ -489,6 +496,7 @@ moe_status check_sizes(const char* fn, int64_t T, int E, int k, int64_t seq_len)
 
 size_t balance_workspace_bytes(int64_t T, int64_t seq_len, int E) {
   const BalancePlan p = make_plan(T, seq_len, E);
+  if (p.S * p.nch <= 1) return 0;  // one workgroup does it all
   return align_up((size_t)(p.S * p.nch) * (8 * (size_t)E + 8) + (size_t)p.S * (4 * (size_t)E + 8), 256);
 }
 
@@ -512,22 +520,22 @@ extern "C" moe_status moe_balance_loss(const float* logits, const int32_t* topk_
   if (!logits || !topk_idx || !counts) return fail(MOE_ERR_INVALID_ARG, "moe_balance_loss: NULL pointer");
   if (!aligned(logits, 4) || !aligned(topk_idx, 4) || !aligned(counts, 4))
     return fail(MOE_ERR_INVALID_ARG, "moe_balance_loss: misaligned pointer");
-  if (workspace_bytes < balance_workspace_bytes(T, seq_len, E))
-    return fail(MOE_ERR_WORKSPACE, "moe_balance_loss: workspace too small");
-  if (!workspace || !aligned(workspace, 256))
+  const size_t need = balance_workspace_bytes(T, seq_len, E);
+  if (workspace_bytes < need) return fail(MOE_ERR_WORKSPACE, "moe_balance_loss: workspace too small");
+  if (need > 0 && (!workspace || !aligned(workspace, 256)))
     return fail(MOE_ERR_INVALID_ARG, "moe_balance_loss: workspace NULL or not 256-byte aligned");
   const BalancePlan p = make_plan(T, seq_len, E);
   const BalanceWs ws = carve(workspace, p, E);
   const SeqOut o{counts, tokens, loss, ws.seq, balance_coef, z_coef, p.S, E, k};
-  dispatch(E, E % 4 == 0 && aligned(logits, 16), [&](auto Lc, auto Vc) {
-    constexpr int L = decltype(Lc)::value;
+  dispatch(E, E % 4 == 0 && aligned(logits, 16), p.chunk, [&](auto Lc, auto Vc, auto Uc) {
+    constexpr int L = decltype(Lc)::value, U = decltype(Uc)::value;
     constexpr bool V = decltype(Vc)::value;
     const dim3 grid((unsigned)(p.S * p.nch)), block(kThreads);
     if (p.nch == 1)
-      hipLaunchKernelGGL((balance_fwd_kernel<L, V, true>), grid, block, 0, s, logits, topk_idx, mask, seq_len, p.nch,
+      hipLaunchKernelGGL((balance_fwd_kernel<L, V, true, U>), grid, block, 0, s, logits, topk_idx, mask, seq_len, p.nch,
                          p.chunk, ws, o);
     else
-      hipLaunchKernelGGL((balance_fwd_kernel<L, V, false>), grid, block, 0, s, logits, topk_idx, mask, seq_len, p.nch,
+      hipLaunchKernelGGL((balance_fwd_kernel<L, V, false, U>), grid, block, 0, s, logits, topk_idx, mask, seq_len, p.nch,
                          p.chunk, ws, o);
   });
   if (p.nch > 1) {  // fewer than kTargetWgs sequences
@@ -552,8 +560,8 @@ extern "C" moe_status moe_balance_loss_bwd(const float* logits, const int32_t* c
     return fail(MOE_ERR_INVALID_ARG, "moe_balance_loss_bwd: misaligned pointer");
   const BalancePlan p = make_plan(T, seq_len, E);
   const bool vec = E % 4 == 0 && aligned(logits, 16) && aligned(d_logits, 16) && aligned(d_logits_in, 16);
-  dispatch(E, vec, [&](auto Lc, auto Vc) {
-    hipLaunchKernelGGL((balance_bwd_kernel<decltype(Lc)::value, decltype(Vc)::value>), dim3((unsigned)(p.S * p.nch)),
+  dispatch(E, vec, p.chunk, [&](auto Lc, auto Vc, auto Uc) {
+    hipLaunchKernelGGL((balance_bwd_kernel<decltype(Lc)::value, decltype(Vc)::value, decltype(Uc)::value>), dim3((unsigned)(p.S * p.nch)),
                        dim3(kThreads), 0, as_stream(stream), logits, counts, tokens, mask, d_loss, d_logits_in,
                        d_logits, p.S, seq_len, p.nch, p.chunk, E, k, balance_coef, z_coef);
   });

@@ -47,11 +47,16 @@ __device__ __forceinline__ int scale_byte(uint32_t u) {
   return b < 0 ? 0 : (b > 254 ? 254 : b);
 }
 
+// 2^(byte - 127), the scale operand of the conversions (byte 0: the subnormal 2^-127)
+__device__ __forceinline__ float scale_value(int byte) {
+  return __uint_as_float(byte ? (uint32_t)byte << 23 : 0x00400000u);
+}
+
 // Eight E2M1 codes (value 0 in the low nibble) of f / 2^(byte - 127), |f| <= 6 * 2^(byte - 127):
 // the conversion divides by its scale operand, a power of two, rounds to nearest, ties to the
 // even code, and keeps the sign of zero.
 __device__ __forceinline__ uint32_t pack8(const float* f, int byte) {
-  const float s = __uint_as_float(byte ? (uint32_t)byte << 23 : 0x00400000u);
+  const float s = scale_value(byte);
   uint32_t w = 0;
   w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[0], f[1], s, 0);
   w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[2], f[3], s, 1);

@@ -462,11 +462,17 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(const float* __restrict
 template <int N>
 using Int = std::integral_constant<int, N>;
 
-// f(BF16, V, TPR, NV): the narrowest team and fewest vectors a thread that hold the row
+// f(BF16, V, TPR, NV): the narrowest team and fewest vectors a thread that hold the row.
+// many: rows enough to fill the card with one wavefront each; a row of up to 64 x 4 vectors then
+// goes to one wavefront, which reduces without barriers and keeps four times the rows of a
+// 256-thread team in flight (16384 x 2048, 8 rows combined: 185 -> 153 us; a single row takes
+// longer that way).
 template <typename F>
-void dispatch(bool bf16, bool vec, int H, F&& f) {
+void dispatch(bool bf16, bool vec, int H, bool many, F&& f) {
   const std::true_type B{};
   const std::false_type S{};
+  if (many && vec && bf16 && H > 1024 && H <= 2048) return f(B, Int<8>{}, Int<64>{}, Int<4>{});
+  if (many && vec && !bf16 && H > 512 && H <= 1024) return f(S, Int<4>{}, Int<64>{}, Int<4>{});
   if (bf16 && vec) {
     if (H <= 512) f(B, Int<8>{}, Int<64>{}, Int<1>{});
     else if (H <= 1024) f(B, Int<8>{}, Int<64>{}, Int<2>{});
@@ -520,7 +526,7 @@ moe_status check_gate(const std::string& fn, int gate_kind, const void* gate, in
 
 template <bool kPost>
 void launch_fwd(const FwdParams& p, bool bf16, bool vec, hipStream_t s) {
-  dispatch(bf16, vec, p.H, [&](auto B, auto Vc, auto Tc, auto Nc) {
+  dispatch(bf16, vec, p.H, p.T >= 4 * num_cus(), [&](auto B, auto Vc, auto Tc, auto Nc) {
     constexpr int TPR = decltype(Tc)::value;
     constexpr int teams = TPR < 256 ? 256 / TPR : 1;
     int64_t grid = (p.T + teams - 1) / teams;
@@ -532,7 +538,7 @@ void launch_fwd(const FwdParams& p, bool bf16, bool vec, hipStream_t s) {
 }
 
 void launch_bwd(const BwdParams& p, int gate_kind, bool bf16, bool vec, float* dw, hipStream_t s) {
-  dispatch(bf16, vec, p.H, [&](auto B, auto Vc, auto Tc, auto Nc) {
+  dispatch(bf16, vec, p.H, false, [&](auto B, auto Vc, auto Tc, auto Nc) {
     constexpr int TPR = decltype(Tc)::value;
     const dim3 grid((unsigned)p.plan.chunks), block(TPR);
     constexpr bool b = decltype(B)::value;

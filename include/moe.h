@@ -636,6 +636,13 @@ typedef enum {
 moe_status moe_workspace_size(moe_op op, const moe_mlp_desc* desc, int64_t R, int64_t T, int E,
                               int k, size_t* bytes);
 
+/*
+ * A [host] pointer table of n tensors stored one after the other, stride bytes apart:
+ * table[i] = base + i * stride. For callers to whom building the table of the weights of
+ * many experts entry by entry costs more than the call.
+ */
+moe_status moe_pointer_table(const void* base, int64_t stride, int n, const void** table);
+
 const char* moe_status_str(moe_status s);
 /* Description of the last failure on the calling thread ("" if none). */
 const char* moe_last_error(void);

@@ -27,7 +27,7 @@ def _size(L, op, desc, R, T, E, k):
 
 
 def test_balance_loss(L):
-    def fwd(logits=D, idx=D, T=64, E=8, k=2, seq=64, counts=D, tokens=D, loss=D, ws=D, nbytes=1 << 20):
+    def fwd(logits=D, idx=D, T=64, E=8, k=2, seq=32, counts=D, tokens=D, loss=D, ws=D, nbytes=1 << 20):
         return L.moe_balance_loss(logits, idx, None, T, E, k, seq, 1.0, 0.0, counts, tokens, loss, ws, nbytes, None)
 
     assert fwd(T=-1) == INV and fwd(E=0) == INV and fwd(E=257) == INV and fwd(k=0) == INV and fwd(k=9) == INV
@@ -48,7 +48,8 @@ def test_balance_loss(L):
     assert st == 0 and n > 0
     assert _size(L, _lib.MOE_OP_BALANCE_LOSS, None, 5, 16384, 128, 0)[0] == INV
     assert _size(L, _lib.MOE_OP_BALANCE_LOSS, None, 0, 16384, 128, 0)[0] == INV
-    assert _size(L, _lib.MOE_OP_BALANCE_LOSS, None, 1, 0, 128, 0)[0] == 0
+    assert _size(L, _lib.MOE_OP_BALANCE_LOSS, None, 1, 0, 128, 0) == (0, 0)
+    assert _size(L, _lib.MOE_OP_BALANCE_LOSS, None, 1, 1, 256, 0) == (0, 0)   # one workgroup
 
 
 def test_pre_norm(L):
@@ -102,6 +103,10 @@ def test_mxfp4(L):
     assert L.mxfp4_dequantize(D, D, 4, 64, ctypes.c_void_p(4104), None) == INV
     assert L.mxfp4_dequantize(None, None, 4, 0, None, None) == 0
     tab = _lib.ptr_table([4096, 4352, 4608, 4864])[0]
+    f = L.moe_pointer_table
+    arr = (ctypes.c_void_p * 4)()
+    assert f(4096, 256, 4, arr) == 0 and list(arr) == [4096, 4352, 4608, 4864]
+    assert f(None, 256, 4, arr) == INV and f(4096, 256, 4, None) == INV and f(4096, 256, -1, arr) == INV and f(4096, 0, 0, None) == 0
     nul = _lib.ptr_table([4096, 4096, None, 4096])[0]
     odd = _lib.ptr_table([4096, 4096, 4100, 4096])[0]
     A, M = _lib.MOE_BF16, _lib.MOE_MXFP4
