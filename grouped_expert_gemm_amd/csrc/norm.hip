@@ -25,47 +25,128 @@ namespace {
 
 constexpr int kMaxH = 16384;
 constexpr int kMaxSlots = 16;
-constexpr int64_t kTargetChunks = 512;
 
 enum { GATE_NONE = 0, GATE_TOKEN = 1, GATE_CHANNEL = 2 };
 
-// ---- vectors of V elements: 16 bytes, or one element where rows are not aligned ----
-template <bool BF16, int V>
-struct Raw;
-template <>
-struct Raw<true, 8> { typedef uint4 type; };
-template <>
-struct Raw<true, 1> { typedef uint16_t type; };
-template <>
-struct Raw<false, 4> { typedef float4 type; };
-template <>
-struct Raw<false, 1> { typedef float type; };
+// ---- vectors of 16 bytes: V = 8 bf16 or 4 float32 ----
+template <bool BF16>
+constexpr int kVec = BF16 ? 8 : 4;
+typedef unsigned int raw_t __attribute__((ext_vector_type(4)));
+typedef raw_t raw_any_t __attribute__((aligned(2)));  // at any element's address: the card reads those too
 
-template <bool BF16, int V>
-__device__ __forceinline__ void unpack(const typename Raw<BF16, V>::type& r, float* v) {
-  if constexpr (BF16 && V == 8) {
-    const uint32_t u[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(u[i] << 16);
-      v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-    }
-  } else if constexpr (BF16) {
-    v[0] = bf16_to_f32(r);
-  } else if constexpr (V == 4) {
-    v[0] = r.x, v[1] = r.y, v[2] = r.z, v[3] = r.w;
+// One of a thread's vectors of a row of H elements: its first column, how many of the row's
+// elements it holds, and where it is read. ALIGNED rows are whole 16-byte vectors. In other
+// rows the last vector may be part-filled: it is read as the row's last 16 bytes, `skip`
+// elements early, and shifted when it is used, so that no load waits for a branch; rows of
+// less than one vector are read element by element.
+struct Span {
+  int col, cnt, at, skip;
+};
+
+template <int V>
+__device__ __forceinline__ Span span(int H, int i) {
+  Span c;
+  c.col = i * V;
+  c.cnt = min(max(H - c.col, 0), V);
+  c.at = max(min(c.col, H - V), 0);
+  c.skip = H < V ? 0 : min(c.col - c.at, V);
+  return c;
+}
+
+// SHORT: the row may be shorter than a vector
+template <bool BF16, bool ALIGNED, bool SHORT>
+__device__ __forceinline__ raw_t load_vec(const void* base, int64_t row, const Span& c, int H) {
+  typedef typename std::conditional<BF16, uint16_t, float>::type elem_t;
+  const elem_t* p = (const elem_t*)base + row;
+  raw_t r = {0, 0, 0, 0};
+  if constexpr (ALIGNED) {
+    if (c.cnt > 0) r = *reinterpret_cast<const raw_t*>(p + c.col);
+  } else if (!SHORT || H >= kVec<BF16>) {
+    r = *reinterpret_cast<const raw_any_t*>(p + c.at);
   } else {
-    v[0] = r;
+#pragma unroll
+    for (int i = 0; i < kVec<BF16> - 1; ++i)
+      if (i < c.cnt) {
+        if constexpr (BF16) r[i / 2] |= (uint32_t)p[i] << (16 * (i & 1));
+        else r[i] = __float_as_uint(p[i]);
+      }
+  }
+  return r;
+}
+
+// a loaded vector without the elements before its first column, zeros behind the row's end
+template <bool BF16, bool ALIGNED>
+__device__ __forceinline__ raw_t settle(raw_t r, const Span& c) {
+  if constexpr (!ALIGNED)
+    if (c.skip > 0) {
+      int s = c.skip;
+      if constexpr (BF16) {
+        if (s & 1) r = raw_t{r[0] >> 16 | r[1] << 16, r[1] >> 16 | r[2] << 16, r[2] >> 16 | r[3] << 16, r[3] >> 16};
+        s >>= 1;
+      }
+      if (s & 1) r = raw_t{r[1], r[2], r[3], 0};
+      if (s & 2) r = raw_t{r[2], r[3], 0, 0};
+      if (s & 4) r = raw_t{0, 0, 0, 0};
+    }
+  return r;
+}
+
+template <bool BF16, bool ALIGNED>
+__device__ __forceinline__ void store_vec(void* base, int64_t at, int n, raw_t r) {
+  typedef typename std::conditional<BF16, uint16_t, float>::type elem_t;
+  elem_t* p = (elem_t*)base + at;
+  if constexpr (ALIGNED) {
+    if (n > 0) *reinterpret_cast<raw_t*>(p) = r;
+  } else if (n == kVec<BF16>) {
+    *reinterpret_cast<raw_any_t*>(p) = r;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kVec<BF16> - 1; ++i)
+      if (i < n) {
+        if constexpr (BF16) p[i] = (uint16_t)(r[i / 2] >> (16 * (i & 1)));
+        else p[i] = __uint_as_float(r[i]);
+      }
   }
 }
 
-template <bool BF16, int V>
-__device__ __forceinline__ typename Raw<BF16, V>::type pack(const float* v) {
-  if constexpr (BF16 && V == 8)
-    return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
-  else if constexpr (BF16) return (uint16_t)f32_to_bf16(v[0]);
-  else if constexpr (V == 4) return make_float4(v[0], v[1], v[2], v[3]);
-  else return v[0];
+// the first n of V sums
+template <bool BF16, bool ALIGNED>
+__device__ __forceinline__ void store_sums(float* p, int n, const float* v) {
+  constexpr int V = kVec<BF16>;
+  if constexpr (ALIGNED) {
+    if (n > 0)
+#pragma unroll
+      for (int i = 0; i < V; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) p[i] = v[i];
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void unpack(raw_t r, float* v) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (BF16) {
+      v[2 * i] = __uint_as_float(r[i] << 16);
+      v[2 * i + 1] = __uint_as_float(r[i] & 0xFFFF0000u);
+    } else {
+      v[i] = __uint_as_float(r[i]);
+    }
+  }
+}
+
+template <bool BF16, bool ALIGNED>
+__device__ __forceinline__ void unpack(raw_t r, const Span& c, float* v) {
+  unpack<BF16>(settle<BF16, ALIGNED>(r, c), v);
+}
+
+template <bool BF16>
+__device__ __forceinline__ raw_t pack(const float* v) {
+  if constexpr (BF16)
+    return raw_t{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7])};
+  else return raw_t{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
 }
 
 // the team's sum of v, in every thread; buf: TPR / 64 floats, one of two alternating buffers
@@ -101,23 +182,22 @@ struct FwdParams {
 };
 
 // kPost: combine, gate, residual, next norm; else the plain norm of y's rows
-template <bool BF16, int V, int TPR, int NV, bool kPost>
+template <bool BF16, bool AL, int TPR, int NV, bool kPost>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(const FwdParams p) {
-  typedef typename Raw<BF16, V>::type raw_t;
-  typedef typename std::conditional<BF16, uint16_t, float>::type elem_t;
+  constexpr int V = kVec<BF16>;
+  constexpr bool kShort = TPR * NV == 64;
   constexpr int kTeams = TPR < 256 ? 256 / TPR : 1;
   __shared__ float red[2][TPR > 64 ? TPR / 64 : 1];
   const int tr = threadIdx.x % TPR;
   const int H = p.H;
   const float inv_h = 1.f / (float)H;  // applied to each term: a sum of squares would overflow H times earlier
   raw_t w[NV], w2[NV];
-  bool in[NV];
+  Span c[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int col = (i * TPR + tr) * V;
-    in[i] = col < H;
-    w[i] = in[i] ? *reinterpret_cast<const raw_t*>((const elem_t*)p.w + col) : raw_t{};
-    w2[i] = kPost && p.w_next && in[i] ? *reinterpret_cast<const raw_t*>((const elem_t*)p.w_next + col) : raw_t{};
+    c[i] = span<V>(H, i * TPR + tr);
+    w[i] = settle<BF16, AL>(load_vec<BF16, AL, kShort>(p.w, 0, c[i], H), c[i]);
+    w2[i] = kPost && p.w_next ? settle<BF16, AL>(load_vec<BF16, AL, kShort>(p.w_next, 0, c[i], H), c[i]) : raw_t{};
   }
   // every thread of a workgroup runs the same rows' loop (team_sum has barriers only where
   // the workgroup is one team)
@@ -127,7 +207,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(const F
     if constexpr (kPost) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        xr[i] = in[i] ? *reinterpret_cast<const raw_t*>((const elem_t*)p.x + t * H + (i * TPR + tr) * V) : raw_t{};
+        xr[i] = load_vec<BF16, AL, kShort>(p.x, t * H, c[i], H);
     }
     if (kPost && p.rows) {
       const int64_t R = p.T * p.k;
@@ -143,10 +223,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(const F
         for (int u = 0; u < kSlots; ++u) {
           const int32_t r = j0 + u < p.k ? p.rows[t * p.k + j0 + u] : -1;
           ok[u] = r >= 0 && r < R;  // a dropped slot adds nothing
-          const elem_t* src = (const elem_t*)p.y + (int64_t)(ok[u] ? r : 0) * H;
 #pragma unroll
           for (int i = 0; i < NV; ++i)
-            q[u][i] = in[i] && ok[u] ? *reinterpret_cast<const raw_t*>(src + (i * TPR + tr) * V) : raw_t{};
+            q[u][i] = j0 + u < p.k ? load_vec<BF16, AL, kShort>(p.y, ok[u] ? (int64_t)r * H : 0, c[i], H) : raw_t{};
         }
 #pragma unroll
         for (int u = 0; u < kSlots; ++u)
@@ -154,7 +233,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(const F
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
               float f[V];
-              unpack<BF16, V>(q[u][i], f);
+              unpack<BF16, AL>(q[u][i], c[i], f);
 #pragma unroll
               for (int v = 0; v < V; ++v) acc[i][v] += f[v];
             }
@@ -163,8 +242,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(const F
     } else {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const raw_t q = in[i] ? *reinterpret_cast<const raw_t*>((const elem_t*)p.y + t * H + (i * TPR + tr) * V) : raw_t{};
-        unpack<BF16, V>(q, acc[i]);
+        unpack<BF16, AL>(load_vec<BF16, AL, kShort>(p.y, t * H, c[i], H), c[i], acc[i]);
       }
     }
     float ss = 0.f;
@@ -176,20 +254,20 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(const F
     if (p.rstd && tr == 0) p.rstd[t] = r;
     float gt = 1.f;
     if (kPost && p.gate_kind == GATE_TOKEN) gt = BF16 ? bf16_to_f32(((const uint16_t*)p.gate)[t]) : ((const float*)p.gate)[t];
-    const elem_t* grow = (const elem_t*)p.gate + (kPost && p.gate_kind == GATE_CHANNEL ? t / p.group * H : 0);
+    const int64_t grow = kPost && p.gate_kind == GATE_CHANNEL ? t / p.group * H : 0;
     float ss2 = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t at = t * H + (i * TPR + tr) * V;
+      const int64_t at = t * H + c[i].col;
       if constexpr (kPost)
-        if (p.c && in[i]) *reinterpret_cast<raw_t*>((elem_t*)p.c + at) = pack<BF16, V>(acc[i]);
+        if (p.c) store_vec<BF16, AL>(p.c, at, c[i].cnt, pack<BF16>(acc[i]));
       float f[V];
-      unpack<BF16, V>(w[i], f);
+      unpack<BF16>(w[i], f);
       if constexpr (kPost) {
         float x[V], g[V];
-        unpack<BF16, V>(xr[i], x);
-        if (p.gate_kind == GATE_CHANNEL && in[i]) {
-          unpack<BF16, V>(*reinterpret_cast<const raw_t*>(grow + (i * TPR + tr) * V), g);
+        unpack<BF16, AL>(xr[i], c[i], x);
+        if (p.gate_kind == GATE_CHANNEL) {
+          unpack<BF16, AL>(load_vec<BF16, AL, kShort>(p.gate, grow, c[i], H), c[i], g);
         } else {
 #pragma unroll
           for (int v = 0; v < V; ++v) g[v] = gt;
@@ -200,13 +278,12 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(const F
 #pragma unroll
         for (int v = 0; v < V; ++v) acc[i][v] = acc[i][v] * r * f[v];
       }
-      const raw_t o = pack<BF16, V>(acc[i]);
-      if (in[i]) *reinterpret_cast<raw_t*>((elem_t*)p.out + at) = o;
-      if constexpr (kPost) {  // the next norm reads the sum as it was stored
-        unpack<BF16, V>(o, acc[i]);
-        if (in[i])
+      const raw_t o = pack<BF16>(acc[i]);
+      store_vec<BF16, AL>(p.out, at, c[i].cnt, o);
+      if constexpr (kPost) {  // the next norm reads the sum as it was stored (0 past the row's end)
+        unpack<BF16>(o, acc[i]);
 #pragma unroll
-          for (int v = 0; v < V; ++v) ss2 += acc[i][v] * inv_h * acc[i][v];
+        for (int v = 0; v < V; ++v) ss2 += acc[i][v] * inv_h * acc[i][v];
       }
     }
     if constexpr (kPost) {
@@ -216,10 +293,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(const F
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           float f[V];
-          unpack<BF16, V>(w2[i], f);
+          unpack<BF16>(w2[i], f);
 #pragma unroll
           for (int v = 0; v < V; ++v) acc[i][v] = acc[i][v] * r2 * f[v];
-          if (in[i]) *reinterpret_cast<raw_t*>((elem_t*)p.y_next + t * H + (i * TPR + tr) * V) = pack<BF16, V>(acc[i]);
+          store_vec<BF16, AL>(p.y_next, t * H + c[i].col, c[i].cnt, pack<BF16>(acc[i]));
         }
       } else if (TPR > 64) {
         __syncthreads();  // red[0] is written again by the next row
@@ -232,15 +309,24 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void norm_fwd_kernel(const F
 
 // Runs of tokens of the backward: run c covers [c * chunk, + chunk), or, where a gate row is
 // shared by more tokens than that (pieces > 1), piece c % pieces of group c / pieces.
+// The partial rows of all runs come to about 2^21 floats, which the caches hold: 512 runs of
+// wide rows, up to 2048 of narrow ones, whose teams of one wavefront need that many to fill
+// the card (131072 x 128 in bf16: 151 us with 512 runs, 49 with 2048; 16384 x 2048 to 8 rows
+// a token: 169 with 512, 147 with 1024; 32768 x 4096: 165 with 512, 173 with 1024). A run has
+// at least 4 rows, down to one for few tokens, where the rows that follow one another take
+// longer than more partial rows to join (64 x 4096: 10.6 us with 4 rows a run, 8.1 with one;
+// 512 x 8192: 20.6 and 23.4).
 struct ChunkPlan {
   int64_t chunks, chunk, pieces;
 };
 
-ChunkPlan plan_chunks(int64_t T, int gate_kind, int64_t group) {
+ChunkPlan plan_chunks(int64_t T, int H, int gate_kind, int64_t group) {
   ChunkPlan p{0, 1, 1};
   if (T == 0) return p;
-  int64_t c = (T + kTargetChunks - 1) / kTargetChunks;
-  if (c < 4) c = T < 4 ? T : 4;
+  const int64_t fit = (1 << 21) / H, target = fit < 512 ? 512 : fit > 2048 ? 2048 : fit;
+  const int64_t least = T <= 128 ? 1 : T <= 384 ? (T + 127) / 128 : 4;
+  int64_t c = (T + target - 1) / target;
+  if (c < least) c = least;
   if (gate_kind == GATE_CHANNEL && group < T) {
     if (group > c) {
       p.pieces = (group + c - 1) / c;
@@ -280,10 +366,10 @@ struct BwdParams {
 // A partial row holds the sum of gate a (no gate, gate per token, or whole groups in the
 // run, whose d_gate rows are then written here), or of a alone where the run is a piece of
 // one group (the join then makes both dw and d_gate from it).
-template <bool BF16, int V, int TPR, int NV, int GATE>
+template <bool BF16, bool AL, int TPR, int NV, int GATE>
 __global__ __launch_bounds__(TPR) void norm_bwd_kernel(const BwdParams p) {
-  typedef typename Raw<BF16, V>::type raw_t;
-  typedef typename std::conditional<BF16, uint16_t, float>::type elem_t;
+  constexpr int V = kVec<BF16>;
+  constexpr bool kShort = TPR * NV == 64;
   __shared__ float red[2][TPR > 64 ? TPR / 64 : 1];
   const int tr = threadIdx.x;
   const int H = p.H;
@@ -302,13 +388,12 @@ __global__ __launch_bounds__(TPR) void norm_bwd_kernel(const BwdParams p) {
   }
   t1 = t1 < p.T ? t1 : p.T;
   raw_t w[NV], graw[NV];
-  bool in[NV];
+  Span c[NV];
   float sum[NV][V], own[NV][V];  // own: sum of a over the current group (channel gates)
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int col = (i * TPR + tr) * V;
-    in[i] = col < H;
-    w[i] = in[i] ? *reinterpret_cast<const raw_t*>((const elem_t*)p.w + col) : raw_t{};
+    c[i] = span<V>(H, i * TPR + tr);
+    w[i] = settle<BF16, AL>(load_vec<BF16, AL, kShort>(p.w, 0, c[i], H), c[i]);
     graw[i] = raw_t{};
 #pragma unroll
     for (int v = 0; v < V; ++v) sum[i][v] = own[i][v] = 0.f;
@@ -319,29 +404,26 @@ __global__ __launch_bounds__(TPR) void norm_bwd_kernel(const BwdParams p) {
     raw_t dr[NV], cr[NV], xr[NV];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int64_t at = t * H + (i * TPR + tr) * V;
-      dr[i] = in[i] ? *reinterpret_cast<const raw_t*>((const elem_t*)p.dout + at) : raw_t{};
-      cr[i] = in[i] ? *reinterpret_cast<const raw_t*>((const elem_t*)p.c + at) : raw_t{};
-      xr[i] = GATE == GATE_NONE && p.dx_in && in[i] ? *reinterpret_cast<const raw_t*>((const elem_t*)p.dx_in + at) : raw_t{};
+      dr[i] = load_vec<BF16, AL, kShort>(p.dout, t * H, c[i], H);
+      cr[i] = load_vec<BF16, AL, kShort>(p.c, t * H, c[i], H);
+      xr[i] = GATE == GATE_NONE && p.dx_in ? load_vec<BF16, AL, kShort>(p.dx_in, t * H, c[i], H) : raw_t{};
     }
     const float r = p.rstd[t];
     float gt = 1.f;
     if (GATE == GATE_TOKEN) gt = BF16 ? bf16_to_f32(((const uint16_t*)p.gate)[t]) : ((const float*)p.gate)[t];
     if (GATE == GATE_CHANNEL && (t == t0 || t % p.group == 0)) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (in[i])
-          graw[i] = *reinterpret_cast<const raw_t*>((const elem_t*)p.gate + t / p.group * H + (i * TPR + tr) * V);
+      for (int i = 0; i < NV; ++i) graw[i] = settle<BF16, AL>(load_vec<BF16, AL, kShort>(p.gate, t / p.group * H, c[i], H), c[i]);
     }
     float n[NV][V], d[NV][V];
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float f[V], g[V];
-      unpack<BF16, V>(cr[i], n[i]);
-      unpack<BF16, V>(dr[i], d[i]);
-      unpack<BF16, V>(w[i], f);
-      if (GATE == GATE_CHANNEL) unpack<BF16, V>(graw[i], g);
+      unpack<BF16, AL>(cr[i], c[i], n[i]);
+      unpack<BF16, AL>(dr[i], c[i], d[i]);
+      unpack<BF16>(w[i], f);
+      if (GATE == GATE_CHANNEL) unpack<BF16>(graw[i], g);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         n[i][v] *= r;
@@ -359,7 +441,7 @@ __global__ __launch_bounds__(TPR) void norm_bwd_kernel(const BwdParams p) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float x[V];
-      unpack<BF16, V>(xr[i], x);
+      unpack<BF16, AL>(xr[i], c[i], x);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         d[i][v] = m * (d[i][v] - n[i][v] * q);
@@ -371,36 +453,32 @@ __global__ __launch_bounds__(TPR) void norm_bwd_kernel(const BwdParams p) {
         const int32_t row = p.rows[t * p.k + j];
         if (row < 0 || row >= R) continue;
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
-          if (in[i])
-            *reinterpret_cast<raw_t*>((elem_t*)p.dy + (int64_t)row * H + (i * TPR + tr) * V) = pack<BF16, V>(d[i]);
+        for (int i = 0; i < NV; ++i) store_vec<BF16, AL>(p.dy, (int64_t)row * H + c[i].col, c[i].cnt, pack<BF16>(d[i]));
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (in[i]) *reinterpret_cast<raw_t*>((elem_t*)p.dy + t * H + (i * TPR + tr) * V) = pack<BF16, V>(d[i]);
+      for (int i = 0; i < NV; ++i) store_vec<BF16, AL>(p.dy, t * H + c[i].col, c[i].cnt, pack<BF16>(d[i]));
     }
     if (GATE == GATE_CHANNEL && p.plan.pieces == 1 && (t + 1 == t1 || (t + 1) % p.group == 0)) {  // the group ends here
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         float f[V], g[V];
-        unpack<BF16, V>(w[i], f);
-        unpack<BF16, V>(graw[i], g);
+        unpack<BF16>(w[i], f);
+        unpack<BF16>(graw[i], g);
+        float dg[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-          if (in[i] && p.dgate) p.dgate[t / p.group * H + (i * TPR + tr) * V + v] = f[v] * own[i][v];
+          dg[v] = f[v] * own[i][v];
           sum[i][v] += g[v] * own[i][v];
           own[i][v] = 0.f;
         }
+        if (p.dgate) store_sums<BF16, AL>(p.dgate + t / p.group * H + c[i].col, c[i].cnt, dg);
       }
     }
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i)
-    if (in[i])
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        p.part[ch * H + (i * TPR + tr) * V + v] = GATE == GATE_CHANNEL && p.plan.pieces > 1 ? own[i][v] : sum[i][v];
+    store_sums<BF16, AL>(p.part + ch * H + c[i].col, c[i].cnt, GATE == GATE_CHANNEL && p.plan.pieces > 1 ? own[i] : sum[i]);
 }
 
 // dw (and, for pieces, d_gate): 16 columns a workgroup and 64 threads a column (4 a
@@ -462,41 +540,29 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(const float* __restrict
 template <int N>
 using Int = std::integral_constant<int, N>;
 
-// f(BF16, V, TPR, NV): the narrowest team and fewest vectors a thread that hold the row.
-// many: rows enough to fill the card with one wavefront each; a row of up to 64 x 4 vectors then
+// f(BF16, ALIGNED, TPR, NV): the narrowest team and fewest vectors a thread that hold the row.
+// MANY: rows enough to fill the card with one wavefront each; a row of up to 64 x 4 vectors then
 // goes to one wavefront, which reduces without barriers and keeps four times the rows of a
 // 256-thread team in flight (16384 x 2048, 8 rows combined: 185 -> 153 us; a single row takes
 // longer that way).
-template <typename F>
-void dispatch(bool bf16, bool vec, int H, bool many, F&& f) {
-  const std::true_type B{};
-  const std::false_type S{};
-  if (many && vec && bf16 && H > 1024 && H <= 2048) return f(B, Int<8>{}, Int<64>{}, Int<4>{});
-  if (many && vec && !bf16 && H > 512 && H <= 1024) return f(S, Int<4>{}, Int<64>{}, Int<4>{});
-  if (bf16 && vec) {
-    if (H <= 512) f(B, Int<8>{}, Int<64>{}, Int<1>{});
-    else if (H <= 1024) f(B, Int<8>{}, Int<64>{}, Int<2>{});
-    else if (H <= 2048) f(B, Int<8>{}, Int<256>{}, Int<1>{});
-    else if (H <= 4096) f(B, Int<8>{}, Int<256>{}, Int<2>{});
-    else if (H <= 8192) f(B, Int<8>{}, Int<256>{}, Int<4>{});
-    else f(B, Int<8>{}, Int<1024>{}, Int<2>{});
-  } else if (vec) {
-    if (H <= 512) f(S, Int<4>{}, Int<64>{}, Int<2>{});
-    else if (H <= 1024) f(S, Int<4>{}, Int<256>{}, Int<1>{});
-    else if (H <= 2048) f(S, Int<4>{}, Int<256>{}, Int<2>{});
-    else if (H <= 4096) f(S, Int<4>{}, Int<256>{}, Int<4>{});
-    else if (H <= 8192) f(S, Int<4>{}, Int<1024>{}, Int<2>{});
-    else f(S, Int<4>{}, Int<1024>{}, Int<4>{});
-  } else {
-    auto scalar = [&](auto b) {
-      if (H <= 512) f(b, Int<1>{}, Int<64>{}, Int<8>{});
-      else if (H <= 1024) f(b, Int<1>{}, Int<256>{}, Int<4>{});
-      else if (H <= 4096) f(b, Int<1>{}, Int<256>{}, Int<16>{});
-      else f(b, Int<1>{}, Int<1024>{}, Int<16>{});
-    };
-    if (bf16) scalar(B);
-    else scalar(S);
-  }
+template <bool MANY, typename F>
+void dispatch(bool bf16, bool al, int H, F&& f) {
+  auto by_width = [&](auto B, auto A) {
+    const int u = (H + kVec<decltype(B)::value> - 1) / kVec<decltype(B)::value>;  // vectors of a row
+    if (u <= 64) f(B, A, Int<64>{}, Int<1>{});
+    else if (u <= 128) f(B, A, Int<64>{}, Int<2>{});
+    else if (u <= 256) f(B, A, Int<MANY ? 64 : 256>{}, Int<MANY ? 4 : 1>{});
+    else if (u <= 512) f(B, A, Int<256>{}, Int<2>{});
+    else if (u <= 1024) f(B, A, Int<256>{}, Int<4>{});
+    else if (u <= 2048) f(B, A, Int<1024>{}, Int<2>{});
+    else if constexpr (!decltype(B)::value) f(B, A, Int<1024>{}, Int<4>{});  // float32 up to 16384
+  };
+  auto by_rows = [&](auto B) {
+    if (al) by_width(B, std::true_type{});
+    else by_width(B, std::false_type{});
+  };
+  if (bf16) by_rows(std::true_type{});
+  else by_rows(std::false_type{});
 }
 
 bool all_aligned(std::initializer_list<const void*> ps, size_t a) {
@@ -526,7 +592,7 @@ moe_status check_gate(const std::string& fn, int gate_kind, const void* gate, in
 
 template <bool kPost>
 void launch_fwd(const FwdParams& p, bool bf16, bool vec, hipStream_t s) {
-  dispatch(bf16, vec, p.H, p.T >= 4 * num_cus(), [&](auto B, auto Vc, auto Tc, auto Nc) {
+  auto go = [&](auto B, auto Vc, auto Tc, auto Nc) {
     constexpr int TPR = decltype(Tc)::value;
     constexpr int teams = TPR < 256 ? 256 / TPR : 1;
     int64_t grid = (p.T + teams - 1) / teams;
@@ -534,15 +600,18 @@ void launch_fwd(const FwdParams& p, bool bf16, bool vec, hipStream_t s) {
     if (grid > most) grid = most;
     hipLaunchKernelGGL((norm_fwd_kernel<decltype(B)::value, decltype(Vc)::value, TPR, decltype(Nc)::value, kPost>),
                        dim3((unsigned)grid), dim3(TPR < 256 ? 256 : TPR), 0, s, p);
-  });
+  };
+  if (p.T >= 4 * num_cus()) dispatch<true>(bf16, vec, p.H, go);
+  else dispatch<false>(bf16, vec, p.H, go);
 }
 
 void launch_bwd(const BwdParams& p, int gate_kind, bool bf16, bool vec, float* dw, hipStream_t s) {
-  dispatch(bf16, vec, p.H, false, [&](auto B, auto Vc, auto Tc, auto Nc) {
+  dispatch<false>(bf16, vec, p.H, [&](auto B, auto Vc, auto Tc, auto Nc) {
     constexpr int TPR = decltype(Tc)::value;
     const dim3 grid((unsigned)p.plan.chunks), block(TPR);
     constexpr bool b = decltype(B)::value;
-    constexpr int V = decltype(Vc)::value, NV = decltype(Nc)::value;
+    constexpr bool V = decltype(Vc)::value;
+    constexpr int NV = decltype(Nc)::value;
     if (gate_kind == GATE_TOKEN) hipLaunchKernelGGL((norm_bwd_kernel<b, V, TPR, NV, GATE_TOKEN>), grid, block, 0, s, p);
     else if (gate_kind == GATE_CHANNEL) hipLaunchKernelGGL((norm_bwd_kernel<b, V, TPR, NV, GATE_CHANNEL>), grid, block, 0, s, p);
     else hipLaunchKernelGGL((norm_bwd_kernel<b, V, TPR, NV, GATE_NONE>), grid, block, 0, s, p);
@@ -570,7 +639,7 @@ moe_status zero_dw(float* dw, int H, hipStream_t s, const char* what) {
 }  // namespace
 
 size_t norm_bwd_workspace_bytes(int64_t T, int H, int gate_kind, int64_t gate_group) {
-  return align_up((size_t)plan_chunks(T, gate_kind, gate_group).chunks * H * 4, 256);
+  return align_up((size_t)plan_chunks(T, H, gate_kind, gate_group).chunks * H * 4, 256);
 }
 
 }  // namespace moe
@@ -611,7 +680,7 @@ extern "C" moe_status moe_pre_norm_bwd(const void* dy, const void* x, const void
     return fail(MOE_ERR_INVALID_ARG, "moe_pre_norm_bwd: workspace NULL or not 256-byte aligned");
   BwdParams p{};
   p.dout = dy, p.c = x, p.rstd = rstd, p.w = weight, p.dx_in = dx_in, p.dx_scale = dx_in_scale, p.dy = dx;
-  p.part = (float*)workspace, p.T = T, p.H = H, p.k = 1, p.plan = plan_chunks(T, GATE_NONE, 0);
+  p.part = (float*)workspace, p.T = T, p.H = H, p.k = 1, p.plan = plan_chunks(T, H, GATE_NONE, 0);
   launch_bwd(p, GATE_NONE, dt == MOE_BF16, H * esz % 16 == 0 && all_aligned({dy, x, weight, dx_in, dx}, 16), dweight, s);
   return check_launch("moe_pre_norm_bwd");
 }
@@ -663,8 +732,8 @@ extern "C" moe_status moe_post_norm_bwd(const void* dout, const void* c, const f
   BwdParams p{};
   p.dout = dout, p.c = c, p.rstd = rstd, p.w = weight, p.gate = gate, p.rows = row_id_map, p.dy = dy;
   p.dgate = dgate, p.part = (float*)workspace, p.T = T, p.group = channel ? gate_group : 1, p.H = H, p.k = k;
-  p.plan = plan_chunks(T, gate_kind, gate_group);
-  const bool vec = H * esz % 16 == 0 && all_aligned({dout, c, weight, channel ? gate : nullptr, dy}, 16);
+  p.plan = plan_chunks(T, H, gate_kind, gate_group);
+  const bool vec = H * esz % 16 == 0 && all_aligned({dout, c, weight, channel ? gate : nullptr, channel ? dgate : nullptr, dy}, 16);
   launch_bwd(p, gate_kind, dt == MOE_BF16, vec, dweight, s);
   return check_launch("moe_post_norm_bwd");
 }

@@ -234,8 +234,8 @@ moe_status moe_unpermute_combine(const void* y_perm, moe_dtype dt, const int32_t
  *   r[t] = 1 / sqrt(mean_h x[t, h]^2 + eps),   y[t, h] = x[t, h] r[t] weight[h]
  *   x, y [T, H], weight [H], all dtype dt (F32 or BF16, rounded to nearest even)
  *   rstd [T] float32 (out, may be NULL): r, for moe_pre_norm_bwd
- * float32 arithmetic. Rows whose bytes are a multiple of 16, with 16-byte aligned pointers,
- * go through 16-byte accesses; any other H and element alignment works, slower.
+ * float32 arithmetic. Any H, and pointers aligned to their element; rows whose bytes are a
+ * multiple of 16, with 16-byte aligned pointers, are the fastest.
  * Limits: 1 <= H <= 16384, eps > 0, T < 2^31; magnitudes below 2^63 (their squares are
  * summed in float32; a row beyond that normalises to 0, one with an infinity to NaN there).
  */
