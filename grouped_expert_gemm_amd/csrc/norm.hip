@@ -481,11 +481,20 @@ __global__ __launch_bounds__(TPR) void norm_bwd_kernel(const BwdParams p) {
     store_sums<BF16, AL>(p.part + ch * H + c[i].col, c[i].cnt, GATE == GATE_CHANNEL && p.plan.pieces > 1 ? own[i] : sum[i]);
 }
 
+__device__ __forceinline__ float fold4(float s) {  // the sum of a column's 4 threads of the wavefront
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(s), __float_as_uint(s), false, false);
+  s = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(s), __float_as_uint(s), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
 // dw (and, for pieces, d_gate): 16 columns a workgroup and 64 threads a column (4 a
 // wavefront), `par` <= 16 groups of them on different gate groups at a time and 64 / par on
 // the pieces of each; sums in a fixed order. The partial rows come from other XCDs' caches,
 // so what counts is that all of a column's loads are in flight at once (512 rows x 4096
-// columns: 10.3 us with 16 threads a column).
+// columns: 10.3 us with 16 threads a column). More than 64 groups (then of few pieces each):
+// par = 64, one thread a group, as 16 at a time would wait for memory once for every 16 (131072
+// x 128 in groups of 65 tokens, the whole backward: 169 -> 62 us).
 template <bool BF16>
 __global__ __launch_bounds__(1024) void norm_join_kernel(const float* __restrict__ part, int64_t groups, int64_t pieces,
                                                          int par, int H, const void* __restrict__ w,
@@ -494,10 +503,31 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(const float* __restrict
   __shared__ float sums[16][17];
   const int cl = threadIdx.x & 15, q = threadIdx.x >> 4, wave = threadIdx.x >> 6;
   const int col = blockIdx.x * 16 + cl;
+  float total = 0.f;
+  if (par == 64) {
+    if (col < H) {
+      const float wv = BF16 ? bf16_to_f32(((const uint16_t*)w)[col]) : ((const float*)w)[col];
+#pragma unroll 4
+      for (int64_t g = q; g < groups; g += 64) {
+        const float* src = part + g * pieces * H + col;
+        float s = 0.f;
+        for (int64_t i = 0; i < pieces; ++i) s += src[i * H];
+        if (dgate) dgate[g * H + col] = wv * s;
+        total += (BF16 ? bf16_to_f32(((const uint16_t*)gate)[g * H + col]) : ((const float*)gate)[g * H + col]) * s;
+      }
+    }
+    total = fold4(total);
+    if ((q & 3) == 0) sums[wave][cl] = total;
+    __syncthreads();
+    if (q == 0 && col < H) {
+      for (int i = 1; i < 16; ++i) total += sums[i][cl];
+      dw[col] = total;
+    }
+    return;
+  }
   const int each = 64 / par, gq = q / each, sub = q % each;
   const int waves = each / 4;                            // wavefronts on one group
   const bool lead = wave % waves == 0 && (q & 3) == 0;   // the thread that finishes its group's column
-  float total = 0.f;
   for (int64_t g0 = 0; g0 < groups; g0 += par) {
     const int64_t g = g0 + gq;
     float s = 0.f;
@@ -506,11 +536,7 @@ __global__ __launch_bounds__(1024) void norm_join_kernel(const float* __restrict
 #pragma unroll 8
       for (int64_t i = sub; i < pieces; i += each) s += src[i * H];
     }
-    // the wavefront's 4 threads of a column, then the group's wavefronts in order
-    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(s), __float_as_uint(s), false, false);
-    s = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(s), __float_as_uint(s), false, false);
-    s = __uint_as_float(b[0]) + __uint_as_float(b[1]);
+    s = fold4(s);  // then the group's wavefronts in order
     if (waves > 1) {
       if ((q & 3) == 0) sums[wave][cl] = s;
       __syncthreads();
@@ -621,6 +647,7 @@ void launch_bwd(const BwdParams& p, int gate_kind, bool bf16, bool vec, float* d
   const int64_t groups = pieces ? p.plan.chunks / p.plan.pieces : 1, each = pieces ? p.plan.pieces : p.plan.chunks;
   int par = 1;
   while (par < 16 && par < groups) par *= 2;
+  if (groups > 64) par = 64;
   auto kernel = bf16 ? norm_join_kernel<true> : norm_join_kernel<false>;
   hipLaunchKernelGGL(kernel, grid, dim3(1024), 0, s, p.part, groups, each, par, p.H, p.w, pieces ? p.gate : nullptr, dw,
                      pieces ? p.dgate : nullptr);

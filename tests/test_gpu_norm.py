@@ -6,8 +6,9 @@ is rounded once (h of its value) on top of float32 arithmetic. The mean of squar
 of positive terms added pairwise or in runs of at most 64, so r is off by at most 64 u
 relative; a product of a few such factors by 80 u of the sum of the magnitudes it adds (the
 combine's k <= 16 terms included). mean(dn n) is off by 64 u of the mean of |dn n|. A column
-sum over T tokens adds runs of at most T / 512 + 4 tokens, then at most 32 + 16 partial
-sums: 128 u of the sum of magnitudes covers T <= 16384."""
+sum over T tokens adds runs of at most T / 512 + 4 tokens, then in each of 64 threads at most
+the 2 T / 256 partial sums of its share, then 64 such sums, 4 at a time and then 16: 128 u of
+the sum of magnitudes covers T <= 4096 (8 + 4 + 32 + 18, and a product's 4 roundings)."""
 import numpy as np
 import pytest
 import torch
@@ -139,6 +140,8 @@ def _post(moe, m, T, H, k, kind, group, scale, next_norm, drop=0):
     (21, 1027, 2, "channel", 21, -1.0, False),
     (700, 2048, 2, "channel", 350, 1.0, False),
     (2100, 96, 2, "channel", 700, 0.0, True),
+    (1500, 131, 1, "channel", 9, 1.0, False),
+    (3003, 24, 2, "channel", 13, 0.5, False),
     (40, 2056, 16, "token", 1, 1.0, True),
     (600, 4096, 2, "none", 1, 0.8, True),
     (18, 4104, 1, "channel", 18, 1.0, False),
