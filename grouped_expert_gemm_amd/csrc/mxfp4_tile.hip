@@ -10,9 +10,13 @@
 //   rows (Q): straight from memory into registers, two steps ahead, from codes laid out in
 //     the MFMA's own order (frag_rows below: a fragment is 1 KiB in a row), so that half of
 //     the operand bytes need neither LDS nor a barrier.
-// What the copies have to cover is the latency past L2, about 2 us when every CU streams:
-// a version with both operands in LDS had 0.75 and 1.6 steps (of ~1 us) of lead and ran at
-// 1.74 us a step; MFMA alone is 1.07 us at 1.9 GHz.
+// What bounds it is the card's power. A step is 64 MFMAs a SIMD; with random operands the card
+// lowers its clock, and the MFMAs alone take 1.34 us a step with every operand in registers
+// (6.4 PFLOP/s) and 1.48 with half of them read from LDS (5.8; all zeros: 8.9). The loop here
+// runs at 1.65 us a step, its clock at 1.8 to 1.9 GHz. 131072 rows, 8 experts of 4096 x 14336:
+// 990 us gate_up with SwiGLU, 505 down; both operands in LDS: 1045 and 500; 128 x 256 tiles, two
+// workgroups a CU: 1273 and 834 (half-line copies, more traffic); workgroups started apart in
+// time: within 2%.
 // The next tile's first loads are issued between the blocks of a tile's epilogue.
 //
 // The K loop runs all but the last three steps in groups of four and RES more, so every ring
@@ -80,7 +84,7 @@ void grouped_gemm_tile_kernel(const Params prm) {
     int beg, end, first;
   } span[2];
   int total = 0;
-  for (int h = 0, rows_before = 0; h < 2; ++h) {
+  for (int h = 0, rows_before = min(max(prm.offsets[0], 0), R); h < 2; ++h) {
     const int e = h * 64 + lane;
     int end = min(max(e < E ? prm.offsets[e + 1] : 0, rows_before), R);
 #pragma unroll

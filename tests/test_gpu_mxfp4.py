@@ -146,7 +146,7 @@ LINEAR = [
     # 16 rows in all and one more: quantised by the product's own kernel, and before it
     (768, 512, [0, 5, 1, 0, 7]),
     (2816, 256, [6, 0, 8]),
-    # every number of K steps modulo the tile kernel's ring of five, one step alone among them
+    # every number of K steps modulo the tile kernel's ring, one step alone among them
     (256, 256, [300]),
     (768, 512, [70, 400]),
     (1024, 256, [513, 64]),
@@ -179,6 +179,22 @@ def test_linear(moe, K, N, sizes, codes):
     assert np.all(bad <= 1), (float(bad.max()), np.unravel_index(bad.argmax(), bad.shape))
     again = moe.moe_grouped_linear_mxfp4(x, _dev(wc), _dev(ws), _dev(off))
     assert torch.equal(again[:R], got[:R])
+
+
+@pytest.mark.parametrize("sizes", [[3, 2], [40, 30], [300, 200]])
+def test_linear_rows_before_the_first_expert(moe, sizes):
+    """Expert e owns the rows [offsets[e], offsets[e + 1]): those before offsets[0] are left as they were."""
+    rng = np.random.default_rng(sum(sizes))
+    K, N, R, lead = 256, 256, sum(sizes) + 10, 10
+    print(f"mxfp4 linear, {lead} rows before the first expert's {sizes}", flush=True)
+    off = _offsets(sizes) + lead
+    w, wc, ws = _weights(rng, 2, N, K)
+    xf, x = _bf16(rng.standard_normal((R, K)))
+    y = torch.full((R, N), 5.0, dtype=torch.bfloat16, device="cuda")
+    g = host(moe.moe_grouped_linear_mxfp4(x, _dev(wc), _dev(ws), _dev(off.astype(np.int32)), out=y))
+    ref, mag = _product_ref(oracle.mxfp4_qdq(xf), w, off)
+    assert np.all(g[:lead] == 5.0)
+    assert np.all(np.abs(g[lead:] - ref[lead:]) <= 2.0 ** -8 * np.abs(ref[lead:]) + _steps(K) * mag[lead:] + 1e-38)
 
 
 def test_linear_not_finite_stays_in_its_rows_and_columns(moe):
