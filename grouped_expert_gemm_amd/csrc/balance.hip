@@ -28,6 +28,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMinTokens = 2;       // tokens of a group that are worth a workgroup and a partial sum of their own
 constexpr int64_t kTargetWgs = 1024;
+constexpr int64_t kMaxSeqs = 1 << 23;  // a launch holds 2^24 - 1 workgroups of 256 threads
 
 struct BalancePlan {
   int64_t S, L, nch, chunk;  // sequences, tokens of each, workgroups per sequence, tokens per workgroup
@@ -489,6 +490,7 @@ moe_status check_sizes(const char* fn, int64_t T, int E, int k, int64_t seq_len)
   if (k < 1 || k > E) return fail(MOE_ERR_INVALID_ARG, f + ": k out of [1, E]");
   if (seq_len < 1 || T % seq_len != 0) return fail(MOE_ERR_INVALID_ARG, f + ": seq_len must divide T");
   if (T > 0x7FFFFFFF / k) return fail(MOE_ERR_UNSUPPORTED, f + ": T * k exceeds int32 counts");
+  if (T / seq_len > kMaxSeqs) return fail(MOE_ERR_UNSUPPORTED, f + ": more than 2^23 sequences");
   return MOE_OK;
 }
 

@@ -142,7 +142,8 @@ moe_status moe_router_bwd(const void* x, const void* w_router, const float* d_lo
  * float32 arithmetic, sums in a fixed order. T = 0 writes loss and tokens[0] = 0.
  * workspace: moe_workspace_size(MOE_OP_BALANCE_LOSS, NULL, seq_len, T, E, 0) bytes (seq_len
  * in the place of R), 256-byte aligned.
- * Limits: 1 <= k <= E <= MOE_MAX_EXPERTS, T % seq_len == 0, T * k < 2^31.
+ * Limits: 1 <= k <= E <= MOE_MAX_EXPERTS, T % seq_len == 0, T * k < 2^31, at most 2^23
+ * sequences.
  */
 moe_status moe_balance_loss(const float* logits, const int32_t* topk_idx, const uint8_t* mask, int64_t T, int E,
                             int k, int64_t seq_len, float balance_coef, float z_coef, int32_t* counts,
@@ -293,7 +294,8 @@ moe_status moe_post_norm(const void* y, const int32_t* row_id_map, int k, const 
  *                [ceil(T / gate_group), H] over the group's tokens (float32, may be NULL)
  *   d[t]       = r (dout gate weight - n mean_h(dout gate weight n))
  *   dy[row_id_map[t*k + j]] = d[t] for every slot (rows of dropped slots and past them are
- *   not written), or dy[t] = d[t] without row_id_map
+ *   not written), or dy[t] = d[t] without row_id_map. No row may be named by two slots, as
+ *   none is in moe_permute's map.
  * The residual's gradient is residual_scale dout: moe_pre_norm_bwd adds it (dx_in, dx_in_scale).
  *   dout, c [T, H], weight [H], gate, dy: dtype dt; c, rstd of the forward
  * T = 0 writes dweight = 0. Column sums in a fixed order.

@@ -34,6 +34,7 @@ def test_balance_loss(L):
     assert fwd(seq=0) == INV and fwd(seq=63) == INV and b"seq_len" in L.moe_last_error()
     assert fwd(T=1 << 31, seq=1 << 31) == UNS
     assert fwd(T=(1 << 63) - 1, seq=1) == UNS
+    assert fwd(T=(1 << 23) + 1, seq=1) == UNS and b"sequences" in L.moe_last_error()
     assert fwd(logits=None) == INV and fwd(idx=None) == INV and fwd(counts=None) == INV and fwd(loss=None) == INV
     assert fwd(tokens=None) == INV and fwd(tokens=ODD) == INV and fwd(logits=ODD) == INV
     assert fwd(nbytes=0) == WS and fwd(ws=None) == INV and fwd(ws=ctypes.c_void_p(4100)) == INV
@@ -42,6 +43,7 @@ def test_balance_loss(L):
         return L.moe_balance_loss_bwd(logits, counts, tokens, None, T, E, k, seq, 1.0, 0.0, g, d_in, d, None)
 
     assert bwd(E=300) == INV and bwd(k=9) == INV and bwd(seq=7) == INV and bwd(logits=None) == INV
+    assert bwd(T=1 << 24, seq=1) == UNS
     assert bwd(d=None) == INV and bwd(d=ODD) == INV and bwd(g=ODD) == INV and bwd(d_in=ODD) == INV
     assert bwd(T=0, logits=None) == 0
     st, n = _size(L, _lib.MOE_OP_BALANCE_LOSS, None, 4096, 16384, 128, 0)
