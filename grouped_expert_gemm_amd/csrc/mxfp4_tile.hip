@@ -14,10 +14,11 @@
 // lowers its clock, and the MFMAs alone take 1.34 us a step with every operand in registers
 // (6.4 PFLOP/s) and 1.48 with half of them read from LDS (5.8; all zeros: 8.9). The loop here
 // runs at 1.65 us a step, its clock at 1.8 to 1.9 GHz. 131072 rows, 8 experts of 4096 x 14336:
-// 990 us gate_up with SwiGLU, 505 down; both operands in LDS: 1045 and 500; 128 x 256 tiles, two
+// 950 us gate_up with SwiGLU, 485 down; both operands in LDS: 1045 and 500; 128 x 256 tiles, two
 // workgroups a CU: 1273 and 834 (half-line copies, more traffic); workgroups started apart in
 // time: within 2%.
-// The next tile's first loads are issued between the blocks of a tile's epilogue.
+// The next tile's first loads are issued within a tile's epilogue, ahead of its stores or, with
+// SwiGLU, between the blocks of its arithmetic.
 //
 // The K loop runs all but the last three steps in groups of four and RES more, so every ring
 // slot is a constant; the last three issue no copies (an expert's product of fewer than three
@@ -53,6 +54,14 @@ typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
 __device__ __forceinline__ i32x8_t wide(i32x4_t v) { return i32x8_t{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
+
+// The lane, computed where it is used: values made from it are not kept (or spilled: a reload
+// would wait for every load and store before it) across the K loop.
+__device__ __forceinline__ int fresh_lane() {
+  int l;
+  asm volatile("v_mbcnt_lo_u32_b32 %0, -1, 0\n\tv_mbcnt_hi_u32_b32 %0, -1, %0" : "=v"(l));
+  return l;
+}
 
 template <int EP, int RES>
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(1, 1)))
@@ -137,16 +146,16 @@ void grouped_gemm_tile_kernel(const Params prm) {
     ps_tile = prm.tab_s[t.e] + (int64_t)t.nt * kTileCols * 8;
     q_tile = prm.q + (int64_t)(t.row >> 5) * slices * 1024;
     qs_tile = prm.q_s + (int64_t)t.row * 8;
+    const int ln = fresh_lane(), n32 = ln & 31, nhi = ln >> 5;
 #pragma unroll
     for (int sm = 0; sm < 2; ++sm) {  // rows past the expert: another's, their products are discarded
-      const int row = min(t.row + wave * 64 + sm * 32 + l32, R - 1);
-      q_off[sm] = (uint32_t)(((row >> 5) - (t.row >> 5)) * slices * 1024 + lhi * 512 + (row & 31) * 16);
-      qs_off[sm] = (uint32_t)(((row - t.row) * 2 + lhi) * 4);
+      const int row = min(t.row + wave * 64 + sm * 32 + n32, R - 1);
+      q_off[sm] = (uint32_t)(((row >> 5) - (t.row >> 5)) * slices * 1024 + nhi * 512 + (row & 31) * 16);
+      qs_off[sm] = (uint32_t)(((row - t.row) * 2 + nhi) * 4);
     }
   };
-  // rounds [I0, I0 + N) of step kt's weights (an empty range, zeros, past the last step)
-  auto copy_P = [&](int kt, auto V, auto I0, auto N) {
-    const uint32_t nrec = (uint32_t)__builtin_amdgcn_readfirstlane(kt < nk ? -1 : 0);
+  // rounds [I0, I0 + N) of step kt's weights; nrec: the range, 0 (zeros) past the last step
+  auto copy_P = [&](int kt, auto V, auto I0, auto N, uint32_t nrec = 0xFFFFFFFFu) {
     const __amdgpu_buffer_rsrc_t rs =
         __builtin_amdgcn_make_buffer_rsrc((void*)(p_tile + (int64_t)kt * kRowBytes), (short)0, (int)nrec, kBufferFlags);
 #pragma unroll
@@ -169,9 +178,11 @@ void grouped_gemm_tile_kernel(const Params prm) {
     kt = kt < nk ? kt : nk - 1;
     const uint8_t* ps = ps_tile + (int64_t)kt * prm.N * 8;
     const uint8_t* qs = qs_tile + (int64_t)kt * R * 8;
+    uint32_t po = ps_off;
+    asm volatile("" : "+v"(po));  // one 32-bit offset, not a 64-bit one kept for every call
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      w.p[j] = *reinterpret_cast<const uint32_t*>(ps + (j * 32 + (j >= 4 ? p_up : 0)) * 8 + ps_off);
+      w.p[j] = *reinterpret_cast<const uint32_t*>(ps + (j * 32 + (j >= 4 ? p_up : 0)) * 8 + po);
 #pragma unroll
     for (int j = 0; j < 2; ++j) w.q[j] = *reinterpret_cast<const uint32_t*>(qs + qs_off[j]);
   };
@@ -252,16 +263,20 @@ void grouped_gemm_tile_kernel(const Params prm) {
     r0 = r1;
     r1 = r2;
   };
-  // a tile's first loads, in seven parts
+  // a tile's first loads, in seven parts (a product may have fewer than three steps)
+  auto range = [&](int kt) {
+    asm volatile("" : "+s"(kt));  // compared here: made ahead of the tiles' loop, the result was spilled
+    return (uint32_t)__builtin_amdgcn_readfirstlane(kt < nk ? -1 : 0);
+  };
   auto first_loads = [&](auto I) {
     constexpr int i = decltype(I)::value;
     if constexpr (i == 0) load_scales(0, r0);
-    if constexpr (i == 1) copy_P(0, C0{}, C0{}, C8{});
+    if constexpr (i == 1) copy_P(0, C0{}, C0{}, C8{}, range(0));
     if constexpr (i == 2) static_for<4>([&](auto S) { load_Q(0, C0{}, S); });
-    if constexpr (i == 3) copy_P(1, C1{}, C0{}, C8{});
+    if constexpr (i == 3) copy_P(1, C1{}, C0{}, C8{}, range(1));
     if constexpr (i == 4) load_scales(1, r1);
-    if constexpr (i == 5) static_for<3>([&](auto S) { load_Q(1, C1{}, S); });
-    if constexpr (i == 6) copy_P(2, C2{}, C0{}, C8{});
+    if constexpr (i == 5) copy_P(2, C2{}, C0{}, C8{}, range(2));
+    if constexpr (i == 6) static_for<3>([&](auto S) { load_Q(1, C1{}, S); });
   };
   // parts [A, B), in that order among the operations around them
   auto parts = [&](auto A, auto B) {
@@ -316,8 +331,7 @@ void grouped_gemm_tile_kernel(const Params prm) {
     __builtin_amdgcn_sched_barrier(0);
 
     // ---------------- epilogue ----------------
-    int ln = lane;
-    asm volatile("" : "+v"(ln));  // keep the lane offsets inside the epilogue
+    const int ln = fresh_lane();
     const int e32 = ln & 31, ehi = ln >> 5;
     const int row0 = wave * 64;   // this wavefront's first row of the tile
     if constexpr (EP == EP_STORE) {
@@ -337,9 +351,7 @@ void grouped_gemm_tile_kernel(const Params prm) {
       for (int sm = 0; sm < 2; ++sm)
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          if (sm == 0 && b == 0) parts(C0{}, C3{});
-          if (sm == 0 && b == 1) parts(C3{}, C5{});
-          if (sm == 1 && b == 0) parts(C5{}, C7{});
+          if (sm == 0 && b == 0) parts(C0{}, C7{});
 #pragma unroll
           for (int sq = 0; sq < 4; ++sq)
 #pragma unroll
@@ -406,9 +418,11 @@ void grouped_gemm_tile_kernel(const Params prm) {
       }
     }
     cur = next;
-    // the next tile's first loads have landed; the stores of the last two blocks (four and the
-    // scales' with SwiGLU) are younger
-    wait_vm<EP == EP_STORE ? 16 : 5>();
+    // the next tile's first weights have landed. STORE: 40 more loads and all 32 stores are younger;
+    // nothing waits for a store before the end of the next tile's first step (the MLP of 131072
+    // rows, 128 experts of 2048 x 768: 665 us with the loads between the blocks of stores, 645 with
+    // them ahead). SWIGLU: four stores of the last block and the scales' are younger
+    wait_vm<EP == EP_STORE ? 63 : 5>();
   }
   wait_vm<0>();
 }
