@@ -8,7 +8,10 @@ Path (per "Efficient MoE Training for Biological Foundation Models",
 Challenges 1-3): moe_route_topk -> moe_permute -> moe_grouped_mlp_fwd
 (gate_up grouped GEMM + ScaledSwiGLU, down grouped GEMM) ->
 moe_unpermute_combine; moe_grouped_mlp_bwd for the backward; mxfp8_quantize
-for MXFP8 block quantisation.
+for MXFP8 block quantisation. Around it: moe_pre_norm before the router,
+moe_balance_loss on its logits, moe_post_norm in the place of
+moe_unpermute_combine (combine, norm, gate, residual), each with its backward,
+and MXFP4 experts for serving (mxfp4_quantize, compute="mxfp4").
 """
 from __future__ import annotations
 

@@ -13,7 +13,7 @@
 // What bounds it is the card's power. A step is 64 MFMAs a SIMD; with random operands the card
 // lowers its clock, and the MFMAs alone take 1.34 us a step with every operand in registers
 // (6.4 PFLOP/s) and 1.48 with half of them read from LDS (5.8; all zeros: 8.9). The loop here
-// runs at 1.65 us a step, its clock at 1.8 to 1.9 GHz. 131072 rows, 8 experts of 4096 x 14336:
+// runs at 1.65 us a step, its clock at 1.8 to 1.9 GHz. 16384 rows, 8 experts of 4096 x 14336:
 // 950 us gate_up with SwiGLU, 485 down; both operands in LDS: 1045 and 500; 128 x 256 tiles, two
 // workgroups a CU: 1273 and 834 (half-line copies, more traffic); workgroups started apart in
 // time: within 2%.
