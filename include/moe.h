@@ -250,7 +250,7 @@ moe_status moe_pre_norm(const void* x, const void* weight, moe_dtype dt, int64_t
  *   dweight[h] = sum_t dy[t, h] n[t, h]                       (float32)
  *   dy, x, dx [T, H], weight [H], dx_in [T, H] or NULL for 0, all dtype dt; dx may equal
  *   dx_in or dy. rstd: of the forward. T = 0 writes dweight = 0.
- * Column sums are added in a fixed order over runs of tokens (a function of T alone).
+ * Column sums are added in a fixed order over runs of tokens (a function of T and H).
  * workspace: moe_workspace_size(MOE_OP_NORM_BWD, desc with H, 0, T, 0, 0) bytes, 256-byte
  * aligned. Limits as for moe_pre_norm.
  */
