@@ -16,6 +16,7 @@ and MXFP4 experts for serving (mxfp4_quantize, compute="mxfp4").
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -93,6 +94,12 @@ def workspace_size(op, desc=None, R=0, T=0, E=1, k=1):
     check("moe_workspace_size", lib().moe_workspace_size(op, ctypes.byref(desc) if desc is not None else None,
                                                          R, T, E, k, ctypes.byref(n)))
     return n.value
+
+
+@functools.lru_cache(maxsize=1024)
+def _size(op, desc=None, R=0, T=0, E=1, k=1):
+    """workspace_size of the fields of an MlpDesc: a function of its numbers alone."""
+    return workspace_size(op, MlpDesc(*desc) if desc else None, R, T, E, k)
 
 
 def moe_route_topk(logits: torch.Tensor, k: int, renormalize: bool = True):
@@ -178,7 +185,7 @@ def moe_balance_loss(logits: torch.Tensor, topk_idx: torch.Tensor, balance_coef:
     counts = torch.empty((T // L, E), dtype=torch.int32, device=dev)
     tokens = torch.empty(T // L + 1, dtype=torch.int32, device=dev)
     loss = torch.empty(3, dtype=torch.float32, device=dev)
-    need = workspace_size(_lib.MOE_OP_BALANCE_LOSS, None, L, T, E)
+    need = _size(_lib.MOE_OP_BALANCE_LOSS, None, L, T, E)
     ws = _workspace(need, dev) if need else None
     _launch("moe_balance_loss", logits, _a(logits), _a(topk_idx), _a(mask), T, E, topk_idx.shape[1], L, balance_coef,
             z_coef, _a(counts), _a(tokens), _a(loss), _a(ws), need)
@@ -254,8 +261,7 @@ def moe_pre_norm(x: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, save_
 
 
 def _norm_workspace(T, H, kind, group, dev):
-    return _workspace(workspace_size(_lib.MOE_OP_NORM_BWD, MlpDesc(1, H, 1, 0, 0, 0, 0), 0, T, kind,
-                                     max(1, min(group, T))), dev)
+    return _workspace(_size(_lib.MOE_OP_NORM_BWD, (1, H, 1, 0, 0, 0, 0), 0, T, kind, max(1, min(group, T))), dev)
 
 
 def moe_pre_norm_bwd(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, rstd: torch.Tensor,
@@ -629,7 +635,7 @@ def moe_grouped_linear_mxfp4(x: torch.Tensor, w, w_scale, offsets: torch.Tensor,
         out = torch.empty((R, N), dtype=torch.bfloat16, device=x.device)
     elif out.dtype != torch.bfloat16 or out.shape != (R, N):
         raise ValueError(f"{fn}: out must be bfloat16 [R, N]")
-    need = workspace_size(_lib.MOE_OP_LINEAR_MXFP4, MlpDesc(E, K, N, MOE_MXFP4, act, MOE_MXFP4, 0), R)
+    need = _size(_lib.MOE_OP_LINEAR_MXFP4, (E, K, N, MOE_MXFP4, act, MOE_MXFP4, 0), R)
     if workspace is None or workspace.numel() < need:
         workspace = _workspace(need, x.device) if need else None
     _launch(fn, x, E, R, K, N, act, _a(x), _a(x_scale), t, ts, _a(offsets), _a(out), _a(workspace), need)
@@ -651,11 +657,11 @@ def _mlp_fwd_mxfp4(x, w_gate_up, w_down, offsets, prob, save_for_bwd, x_scale, w
         out = torch.empty((R, H), dtype=torch.bfloat16, device=x.device)
     elif out.dtype != torch.bfloat16 or out.shape != (R, H):
         raise ValueError(f"{fn}: out must be bfloat16 [R, H]")
-    desc = MlpDesc(E, H, I, MOE_MXFP4, act, wt, int(save_for_bwd))
-    need = workspace_size(_lib.MOE_OP_MLP_FWD, desc, R)
+    desc = (E, H, I, MOE_MXFP4, act, wt, int(save_for_bwd))
+    need = _size(_lib.MOE_OP_MLP_FWD, desc, R)
     if workspace is None or workspace.numel() < need:
         workspace = _workspace(need, x.device) if need else None
-    _launch("moe_grouped_mlp_fwd_tables", x, ctypes.byref(desc), R, _a(x), _a(x_scale), t1, t2, s1, s2, _a(offsets),
+    _launch("moe_grouped_mlp_fwd_tables", x, ctypes.byref(MlpDesc(*desc)), R, _a(x), _a(x_scale), t1, t2, s1, s2, _a(offsets),
             _a(prob), _a(out), None, None, _a(workspace), need)
     return out
 
