@@ -9,8 +9,8 @@
 // block l / 16 of the 128 values.
 //
 // grouped_gemm_rows_kernel: y = x W^T for few rows an expert, bound by the weights' bytes.
-// The weights go straight from memory to the MFMA, without LDS: a workgroup takes 32 output
-// columns (32 gate and 32 up rows with SwiGLU) of one expert, its four wavefronts every
+// The weights go straight from memory to the MFMA, without LDS: a workgroup takes 32 or 64
+// output columns (32 gate and 32 up rows with SwiGLU) of one expert, its four wavefronts every
 // fourth 256-value unit of K, and their partial products are added through LDS in wavefront
 // order. The next unit's weights are in flight while one is multiplied.
 // (Many rows: mxfp4_tile.hip.)
@@ -276,15 +276,18 @@ __device__ __forceinline__ i32x4_t quantize_block(const i32x4_t* x, int& byte) {
 // and rows in flight and four workgroups a CU; the same with bf16 rows, whose blocks each lane
 // quantises as it multiplies them (for calls of so few rows that doing it in every workgroup
 // costs less than a launch of its own); or 64 at a time, so that the weights of an expert with
-// more rows are read once, with two units of weights in flight and two workgroups a CU.
-// Eight experts of 4096 x 14336, 249 MB, 48 us at the rate of a copy: with 1, 12, 24 and 64 rows
-// each 16 at a time take 49, 58, 90 and 137 us, 64 at a time 54, 62, 74 and 109 us.
+// more rows are read once, with two units of weights in flight, two workgroups a CU and 64
+// columns a workgroup, as the rows are read once for every workgroup of columns.
+// Eight experts of 4096 x 14336, 249 MB, 48 us at the rate of a copy: with 4, 8, 12, 24 and 64
+// rows each 16 at a time take 51, 55, 60, 101 and 199 us, 64 at a time 54, 55, 57, 64 and 84 us
+// (with 32 columns 109 us at 64 rows; with 128 the registers spill: 365).
 enum { ROWS_16 = 0, ROWS_16_BF16 = 1, ROWS_64 = 2 };
 
 template <int EP, int MODE>
 __global__ __launch_bounds__(256, MODE == ROWS_64 ? 2 : 3) void grouped_gemm_rows_kernel(const Params prm) {
   constexpr bool kBF16 = MODE == ROWS_16_BF16;
-  constexpr int NA = EP == EP_SWIGLU ? 4 : 2;   // 16-row weight tiles
+  constexpr int NA = EP == EP_SWIGLU || MODE == ROWS_64 ? 4 : 2;  // 16-row weight tiles
+  constexpr int NC = EP == EP_SWIGLU ? 32 : NA * 16;              // output columns
   constexpr int NR = MODE == ROWS_64 ? 4 : 1;   // 16-row tiles of x at a time
   constexpr int D = MODE == ROWS_64 ? 2 : 1;    // units of weights in flight
   constexpr int LD = NA * 16 + 4;
@@ -305,7 +308,7 @@ __global__ __launch_bounds__(256, MODE == ROWS_64 ? 2 : 3) void grouped_gemm_row
 #pragma unroll
   for (int a = 0; a < NA; ++a) {
     const int n = EP == EP_SWIGLU ? (a >= 2 ? prm.I : 0) + blockIdx.x * 32 + (a & 1) * 16 + l16
-                                  : blockIdx.x * 32 + a * 16 + l16;
+                                  : blockIdx.x * NC + a * 16 + l16;
     wc[a] = (uint32_t)(n * ldc + g * 16);
     ws[a] = (uint32_t)(n * lds);
   }
@@ -394,11 +397,13 @@ __global__ __launch_bounds__(256, MODE == ROWS_64 ? 2 : 3) void grouped_gemm_row
       auto sum = [&](int col) {
         return (part[0][row][col] + part[1][row][col]) + (part[2][row][col] + part[3][row][col]);
       };
-      const float v0 = sum(cp), v1 = sum(cp + 1);
       if constexpr (EP == EP_STORE) {
         if (mg < end)
-          *reinterpret_cast<uint32_t*>((bf16_t*)prm.c + mg * prm.N + blockIdx.x * 32 + cp) = pack_bf16x2(v0, v1);
+#pragma unroll
+          for (int c = cp; c < NC; c += 32)
+            *reinterpret_cast<uint32_t*>((bf16_t*)prm.c + mg * prm.N + blockIdx.x * NC + c) = pack_bf16x2(sum(c), sum(c + 1));
       } else {
+        const float v0 = sum(cp), v1 = sum(cp + 1);
         const float p = prm.prob[mg < end ? mg : end - 1];
         const float h0 = silu_f(v0) * sum(32 + cp) * p, h1 = silu_f(v1) * sum(32 + cp + 1) * p;
         uint32_t top = max(__float_as_uint(h0) & 0x7FFFFFFFu, __float_as_uint(h1) & 0x7FFFFFFFu);
@@ -452,10 +457,11 @@ static moe_status launch(const Params& p, Path path, hipStream_t s) {
   if (path == Path::kTiles) return launch_tile(EP, p, s);
   const int64_t experts = p.R < p.E ? p.R : p.E;
   const dim3 grid((unsigned)((EP == EP_SWIGLU ? p.I : p.N) / 32), (unsigned)experts);
+  const dim3 wide_grid(EP == EP_SWIGLU ? grid.x : grid.x / 2, grid.y);
   if (path == Path::kRowsBF16) hipLaunchKernelGGL((grouped_gemm_rows_kernel<EP, ROWS_16_BF16>), grid, dim3(256), 0, s, p);
   else if (p.R <= 16 || p.R <= (int64_t)8 * p.E)  // 8 rows an expert on average: hardly any has more than 16
     hipLaunchKernelGGL((grouped_gemm_rows_kernel<EP, ROWS_16>), grid, dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((grouped_gemm_rows_kernel<EP, ROWS_64>), grid, dim3(256), 0, s, p);
+  else hipLaunchKernelGGL((grouped_gemm_rows_kernel<EP, ROWS_64>), wide_grid, dim3(256), 0, s, p);
   return check_launch(EP == EP_SWIGLU ? "MXFP4 gate_up + ScaledSwiGLU" : "MXFP4 grouped linear");
 }
 
