@@ -354,8 +354,8 @@ def moe_permute(x: torch.Tensor, topk_idx: torch.Tensor, topk_prob: torch.Tensor
 
     Returns a dict with x_perm [R, H], x_perm_scale (MXFP8 and MXFP4 only), prob_perm [R],
     split_sizes [E], offsets [E+1], row_id_map [T*k], src_token [R].
-    uint8 codes come with x_scale, a byte per 32 values: MXFP8 where a byte of x is one
-    value, MXFP4 where it is two.
+    uint8 codes x [T, B] come with x_scale, a byte per 32 values: MXFP4 (two values a byte)
+    where x_scale is [T, B / 16], else MXFP8 with T * B / 32 bytes of scales.
     With ``row_id_map`` given, only x is gathered with that map (topk_idx gives k).
     """
     _need_cuda(x, topk_idx, topk_prob, x_scale, row_id_map)
@@ -365,8 +365,11 @@ def moe_permute(x: torch.Tensor, topk_idx: torch.Tensor, topk_prob: torch.Tensor
     dt = _DT[x.dtype]
     dev = x.device
     x_perm = torch.empty((R, H), dtype=x.dtype, device=dev)
-    if dt == MOE_MXFP8 and x_scale is not None and x_scale.shape[-1] * 16 == H:
-        dt, H = MOE_MXFP4, 2 * H   # two codes a byte
+    if dt == MOE_MXFP8 and x_scale is not None:
+        if x_scale.shape == (T, H // 16):
+            dt, H = MOE_MXFP4, 2 * H   # two codes a byte
+        elif x_scale.numel() < T * (H // 32):
+            raise ValueError("moe_permute: x_scale must be [T, H/32] (MXFP8) or, of x's bytes a row, [T, bytes/16] (MXFP4)")
     xps = torch.empty((R, H // 32), dtype=torch.uint8, device=dev) if dt in (MOE_MXFP8, MOE_MXFP4) else None
     if row_id_map is not None:
         check("moe_permute", lib().moe_permute(_p(x), _p(x_scale), dt, T, H, E, k, None, None, 1, _p(x_perm),
