@@ -74,6 +74,7 @@ extern "C" moe_status moe_workspace_size(moe_op op, const moe_mlp_desc* desc, in
     case MOE_OP_MLP_BWD: {
       if (!desc || R < 0) return fail(MOE_ERR_INVALID_ARG, "moe_workspace_size: desc NULL or R < 0");
       moe_status s = validate_desc(*desc, op == MOE_OP_MLP_BWD);
+      if (s == MOE_OK && desc->compute == MOE_MXFP4) s = mx4::check_rows(R, desc->E, desc->H, desc->act, "moe_workspace_size(MLP_FWD)");
       if (s != MOE_OK) return s;
       *bytes = op == MOE_OP_MLP_FWD ? mlp_fwd_workspace_bytes(*desc, R) : mlp_bwd_workspace_bytes(*desc, R);
       return MOE_OK;
@@ -101,6 +102,8 @@ extern "C" moe_status moe_workspace_size(moe_op op, const moe_mlp_desc* desc, in
           (desc->act != MOE_BF16 && desc->act != MOE_MXFP4))
         return fail(MOE_ERR_INVALID_ARG, "moe_workspace_size(LINEAR_MXFP4): desc NULL or bad R/E/K/N/act");
       if (const moe_status s = mx4::check_shape(desc->E, desc->H, desc->I, "moe_workspace_size(LINEAR_MXFP4)"); s != MOE_OK)
+        return s;
+      if (const moe_status s = mx4::check_rows(R, desc->E, desc->H, desc->act, "moe_workspace_size(LINEAR_MXFP4)"); s != MOE_OK)
         return s;
       *bytes = mx4::linear_workspace_bytes(desc->E, R, desc->H, desc->I, desc->act);
       return MOE_OK;

@@ -84,6 +84,7 @@ moe_status frag_rows(const uint8_t* e2m1, const uint8_t* e8m0, int64_t rows, int
 moe_status launch_tile(int ep, const Params& p, hipStream_t s);
 
 moe_status check_shape(int E, int K, int N, const char* what);
+moe_status check_rows(int64_t R, int E, int K, moe_dtype act, const char* what);
 size_t mlp_workspace_bytes(const moe_mlp_desc& d, int64_t R);
 size_t linear_workspace_bytes(int E, int64_t R, int K, int N, moe_dtype act);
 moe_status forward(const moe_mlp_desc& d, int64_t R, const void* x_perm, const uint8_t* x_perm_scale,

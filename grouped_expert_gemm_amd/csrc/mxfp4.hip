@@ -176,27 +176,19 @@ __global__ __launch_bounds__(256) void frag_rows_kernel(const uint8_t* __restric
   if (l8 == 0) scales[step * rows + r] = lane_order(in_s[r * steps + step]);
 }
 
-static moe_status check_items(int64_t rows, int64_t cols, int64_t& blocks) {
-  blocks = ((rows + 7) / 8 * (cols / 256) + 3) / 4;
-  return blocks <= 0x7FFFFFFF ? MOE_OK : fail(MOE_ERR_UNSUPPORTED, "MXFP4 rows: too many values for one launch");
-}
+// workgroups of the two kernels above; check_rows keeps them within a launch
+static int64_t row_groups(int64_t rows, int64_t cols) { return ((rows + 7) / 8 * (cols / 256) + 3) / 4; }
 
 moe_status quantize_frag(const void* in_bf16, int64_t rows, int64_t cols, uint8_t* codes, uint8_t* scales, hipStream_t s) {
-  int64_t blocks;
-  const moe_status st = check_items(rows, cols, blocks);
-  if (st != MOE_OK) return st;
-  hipLaunchKernelGGL(quantize_frag_kernel, dim3((unsigned)blocks), dim3(256), 0, s, (const uint16_t*)in_bf16, rows, cols,
-                     codes, (uint2*)scales);
+  hipLaunchKernelGGL(quantize_frag_kernel, dim3((unsigned)row_groups(rows, cols)), dim3(256), 0, s, (const uint16_t*)in_bf16,
+                     rows, cols, codes, (uint2*)scales);
   return check_launch("MXFP4 row quantisation");
 }
 
 moe_status frag_rows(const uint8_t* e2m1, const uint8_t* e8m0, int64_t rows, int64_t cols, uint8_t* codes, uint8_t* scales,
                      hipStream_t s) {
-  int64_t blocks;
-  const moe_status st = check_items(rows, cols, blocks);
-  if (st != MOE_OK) return st;
-  hipLaunchKernelGGL(frag_rows_kernel, dim3((unsigned)blocks), dim3(256), 0, s, e2m1, (const uint2*)e8m0, rows, cols, codes,
-                     (uint2*)scales);
+  hipLaunchKernelGGL(frag_rows_kernel, dim3((unsigned)row_groups(rows, cols)), dim3(256), 0, s, e2m1, (const uint2*)e8m0, rows,
+                     cols, codes, (uint2*)scales);
   return check_launch("MXFP4 row conversion");
 }
 
@@ -442,6 +434,13 @@ static Path choose(int64_t R, int E, moe_dtype act) {
   return R <= (int64_t)64 * E ? Path::kRows : Path::kTiles;
 }
 
+moe_status check_rows(int64_t R, int E, int K, moe_dtype act, const char* what) {
+  constexpr int64_t kMaxGroups = (1 << 24) - 1;  // a launch holds fewer than 2^32 threads: workgroups of 256
+  if (choose(R, E, act) == Path::kTiles && (R > 0x7FFFFFFF || row_groups(R, K) > kMaxGroups))
+    return fail(MOE_ERR_UNSUPPORTED, std::string(what) + ": too many MXFP4 row values for one launch");
+  return MOE_OK;
+}
+
 static void fill(Params& p, int E, int64_t R, int K, int N, const uint8_t* x, const uint8_t* xs, const uint8_t* const* w,
                  const uint8_t* const* ws, const int32_t* offsets, void* c) {
   std::memset(&p, 0, sizeof(p));
@@ -546,6 +545,8 @@ moe_status forward(const moe_mlp_desc& d, int64_t R, const void* x_perm, const u
                    const void* const* w_gate_up, const void* const* w_down, const uint8_t* const* w_gate_up_scale,
                    const uint8_t* const* w_down_scale, const int32_t* offsets, const float* prob_perm, void* y_perm,
                    uint8_t* workspace, hipStream_t s) {
+  const moe_status st = check_rows(R, d.E, d.H, d.act, "moe_grouped_mlp_fwd");
+  if (st != MOE_OK) return st;
   Carver ws{workspace};
   return mlp(ws, d, R, x_perm, x_perm_scale, w_gate_up, w_down, w_gate_up_scale, w_down_scale, offsets, prob_perm,
              y_perm, s);
@@ -627,6 +628,7 @@ extern "C" moe_status moe_grouped_linear_mxfp4(int E, int64_t R, int K, int N, m
     if (!aligned(w[e], 16) || !aligned(w_scale[e], 8))
       return fail(MOE_ERR_INVALID_ARG, f + ": weights must be 16-byte and their scales 8-byte aligned");
   }
+  if ((st = mx4::check_rows(R, E, K, act, fn)) != MOE_OK) return st;
   const size_t need = mx4::linear_workspace_bytes(E, R, K, N, act);
   if (workspace_bytes < need) return fail(MOE_ERR_WORKSPACE, f + ": workspace too small");
   if (need > 0 && (!workspace || !aligned(workspace, 256)))

@@ -513,7 +513,8 @@ typedef struct {
  * With compute = MXFP4 (serving: forward only, save_for_bwd must be 0), x_perm, W1_e, h and
  * W2_e enter their GEMMs as MXFP4 (rule of mxfp4_quantize), h from its float32 value in the
  * gate_up epilogue; scales are the E8M0 bytes of mxfp4_quantize ([R, H/32], [2I, H/32],
- * [H, I/32]), 8-byte aligned. Rows past offsets[E] of y_perm are not written.
+ * [H, I/32]), 8-byte aligned. Rows past offsets[E] of y_perm are not written. R * H is at most
+ * about 2^37 (one launch lays the rows out).
  * Shapes the GEMM kernels implement: BF16 needs H % 256 == 0 and I % 128 == 0;
  * MXFP8, FP8 and MXFP4 need H % 256 == 0, I % 256 == 0 and E <= 128; F32 needs H % 4 == 0.
  */
@@ -594,7 +595,8 @@ moe_status moe_grouped_linear(int E, int64_t R, int K, int N, moe_dtype dt, cons
  *   ignored); act = MXFP4: x [R, K/2] codes with x_scale [R, K/32]
  *   w [host] E pointers to [N, K/2] codes, w_scale [host] E pointers to [N, K/32] scales
  *   y [R, N] bf16 (rounded to nearest even); rows past offsets[E] are not written
- * x, y, w 16-byte, scales 8-byte aligned. Shapes: K % 256 == 0, N % 256 == 0, E <= 128.
+ * x, y, w 16-byte, scales 8-byte aligned. Shapes: K % 256 == 0, N % 256 == 0, E <= 128; R * K at
+ * most about 2^37 (one launch lays the rows out).
  * workspace: moe_workspace_size(MOE_OP_LINEAR_MXFP4, desc with E, H = K, I = N and act, R,
  * ...) bytes, 256-byte aligned, caller-owned. Calls sharing a workspace must not overlap.
  */
