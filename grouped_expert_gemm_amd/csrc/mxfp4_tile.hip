@@ -351,7 +351,10 @@ void grouped_gemm_tile_kernel(const Params prm) {
       for (int sm = 0; sm < 2; ++sm)
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
-          if (sm == 0 && b == 0) parts(C0{}, C7{});
+          if (sm == 0 && b == 0) {  // the copies of step 0 ahead of the rest, which the last wait counts on
+            parts(C0{}, C2{});
+            parts(C2{}, C7{});
+          }
 #pragma unroll
           for (int sq = 0; sq < 4; ++sq)
 #pragma unroll
