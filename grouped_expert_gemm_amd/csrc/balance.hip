@@ -15,6 +15,11 @@
 // j, j + L, ... one at a time. A workgroup takes a run of tokens of one sequence and keeps
 // the sums of p in registers; partial sums leave through the workspace and are added in a
 // fixed order (counts are integers, whose LDS atomics commute), so results repeat bit for bit.
+//
+// 131072 tokens x 256 experts: the forward kernel takes 44 us for 138 MB, 27 us at the rate of a
+// copy. What bounds it is the vector ALU (157 instructions of a wavefront a token, busy 75 to
+// 81% of the time): two reductions over 64 lanes and the exponentials for four logits a lane.
+// The backward, 403 MB with d_in, takes 67 us right after it.
 #include <cmath>
 #include <type_traits>
 

@@ -265,14 +265,18 @@ __device__ __forceinline__ i32x4_t quantize_block(const i32x4_t* x, int& byte) {
 }
 
 // How a workgroup takes its expert's rows: 16 at a time, each wavefront with one unit of weights
-// and rows in flight and four workgroups a CU; the same with bf16 rows, whose blocks each lane
-// quantises as it multiplies them (for calls of so few rows that doing it in every workgroup
-// costs less than a launch of its own); or 64 at a time, so that the weights of an expert with
+// and rows in flight and, by its registers, seven workgroups a CU (four with SwiGLU); the same
+// with bf16 rows, whose blocks each lane quantises as it multiplies them (for calls of so few
+// rows that doing it in every workgroup costs less than a launch of its own; four workgroups a
+// CU, three with SwiGLU); or 64 at a time, so that the weights of an expert with
 // more rows are read once, with two units of weights in flight, two workgroups a CU and 64
 // columns a workgroup, as the rows are read once for every workgroup of columns.
 // Eight experts of 4096 x 14336, 249 MB, 48 us at the rate of a copy: with 4, 8, 12, 24 and 64
 // rows each 16 at a time take 51, 55, 60, 101 and 199 us, 64 at a time 54, 55, 57, 64 and 84 us
-// (with 32 columns 109 us at 64 rows; with 128 the registers spill: 365).
+// (with 32 columns 109 us at 64 rows; with 128 the registers spill: 365). Those passes repeat
+// over one set of weights, which the last-level cache holds in part; with six sets in turn 12, 24
+// and 64 rows, 64 at a time and quantised in the call, take 61, 70 and 91 us in place of 47, 54
+// and 83.
 enum { ROWS_16 = 0, ROWS_16_BF16 = 1, ROWS_64 = 2 };
 
 template <int EP, int MODE>
@@ -426,8 +430,12 @@ moe_status check_shape(int E, int K, int N, const char* what) {
 }
 
 // How a call reads its rows: few rows an expert are bound by the weights' bytes and go to the
-// row kernel, otherwise to 256-row tiles. At most 16 rows in all, given in bf16, are quantised
-// by the row kernel itself.
+// row kernel, otherwise to 256-row tiles (8 experts of 4096 x 14336: 64 rows each 83 us, 65 rows
+// 108). At most 16 rows in all, given in bf16, are quantised by the row kernel itself. The offsets
+// are on the device, so the rule sees the average alone: an expert with many more rows than that
+// is walked 16 or 64 rows at a time by its columns' workgroups, its weights read again each time
+// (128 experts of 2048 x 2048 and 8192 rows: 105 us with 64 rows each, 428 with half of all rows
+// on one, 800 with all of them).
 enum class Path { kRowsBF16, kRows, kTiles };
 static Path choose(int64_t R, int E, moe_dtype act) {
   if (act == MOE_BF16 && R <= 16) return Path::kRowsBF16;
@@ -458,7 +466,7 @@ static moe_status launch(const Params& p, Path path, hipStream_t s) {
   const dim3 grid((unsigned)((EP == EP_SWIGLU ? p.I : p.N) / 32), (unsigned)experts);
   const dim3 wide_grid(EP == EP_SWIGLU ? grid.x : grid.x / 2, grid.y);
   if (path == Path::kRowsBF16) hipLaunchKernelGGL((grouped_gemm_rows_kernel<EP, ROWS_16_BF16>), grid, dim3(256), 0, s, p);
-  else if (p.R <= 16 || p.R <= (int64_t)8 * p.E)  // 8 rows an expert on average: hardly any has more than 16
+  else if (p.R <= 16 || p.R <= (int64_t)8 * p.E)  // 8 rows an expert on average: of near-even loads hardly any has more than 16
     hipLaunchKernelGGL((grouped_gemm_rows_kernel<EP, ROWS_16>), grid, dim3(256), 0, s, p);
   else hipLaunchKernelGGL((grouped_gemm_rows_kernel<EP, ROWS_64>), wide_grid, dim3(256), 0, s, p);
   return check_launch(EP == EP_SWIGLU ? "MXFP4 gate_up + ScaledSwiGLU" : "MXFP4 grouped linear");

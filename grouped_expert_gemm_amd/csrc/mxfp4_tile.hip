@@ -17,8 +17,12 @@
 // 950 us gate_up with SwiGLU, 485 down; both operands in LDS: 1045 and 500; 128 x 256 tiles, two
 // workgroups a CU: 1273 and 834 (half-line copies, more traffic); workgroups started apart in
 // time: within 2%.
+// Besides: the epilogue, in which no MFMA runs (one workgroup a CU, one wavefront a SIMD), about a
+// fifth of that gate_up's time and most of a product of three steps'; and the last round of tiles
+// (1088 tiles of that down product are 4.25 rounds of 256 CUs and take five).
 // The next tile's first loads are issued within a tile's epilogue, ahead of its stores or, with
-// SwiGLU, between the blocks of its arithmetic.
+// SwiGLU, between the blocks of its arithmetic. (STORE: the compiler, which cannot tell sOut from
+// the slots being copied to, waits for the copies before the epilogue's first LDS store.)
 //
 // The K loop runs all but the last three steps in groups of four and RES more, so every ring
 // slot is a constant; the last three issue no copies (an expert's product of fewer than three
@@ -421,10 +425,10 @@ void grouped_gemm_tile_kernel(const Params prm) {
       }
     }
     cur = next;
-    // the next tile's first weights have landed. STORE: 40 more loads and all 32 stores are younger;
-    // nothing waits for a store before the end of the next tile's first step (the MLP of 131072
-    // rows, 128 experts of 2048 x 768: 665 us with the loads between the blocks of stores, 645 with
-    // them ahead). SWIGLU: four stores of the last block and the scales' are younger
+    // the next tile's first weights have landed. STORE: 40 more loads and all 32 stores are younger,
+    // and no store is waited for here (the MLP of 131072 rows, 128 experts of 2048 x 768: 665 us
+    // with the loads between the blocks of stores, 645 with them ahead). SWIGLU: four stores of
+    // the last block and the scales' are younger
     wait_vm<EP == EP_STORE ? 63 : 5>();
   }
   wait_vm<0>();

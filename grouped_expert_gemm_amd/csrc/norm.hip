@@ -14,6 +14,12 @@
 // next norm come from one read. A forward workgroup walks several rows with the weights
 // held in registers; a backward team walks a run of consecutive tokens and keeps the column
 // sums of a in registers, so that dw and d_gate cost one partial row per run.
+// Teams of 1024 threads have 128 registers a thread, which the widest rows exceed: the channel-gate
+// backward of more than 8192 elements spills 31 to 59 of them, the float32 post norm of more than
+// 8192 elements 37 or 40, the float32 backward without a gate of unaligned such rows 11. Whole
+// calls, 134 MB a tensor, against 8192 wide: channel-gate backward of bf16 4096 x 16384 121 us (67 MB
+// at 4096 x 8192: 49), of float32 2048 x 16384 116 (4096 x 8192: 90); float32 post norm with
+// c and the next norm 234 (141).
 #include <type_traits>
 
 #include "common.h"
