@@ -12,6 +12,9 @@ for MXFP8 block quantisation. Around it: moe_pre_norm before the router,
 moe_balance_loss on its logits, moe_post_norm in the place of
 moe_unpermute_combine (combine, norm, gate, residual), each with its backward,
 and MXFP4 experts for serving (mxfp4_quantize, compute="mxfp4").
+Activations in 8 bits: moe_add_norm_mxfp8 (combine, residual, norm, MXFP8 rows),
+mxfp8_dequantize, and moe_grouped_mlp_fwd_ckpt8 / moe_grouped_mlp_bwd_ckpt8, the
+bf16 grouped MLP whose backward works from MXFP8 checkpoints.
 """
 from __future__ import annotations
 
@@ -27,7 +30,8 @@ __all__ = [
     "moe_route_topk", "moe_router_logits", "moe_route_topk_bwd", "moe_router_bwd", "moe_balance_loss",
     "moe_balance_loss_bwd", "moe_pre_norm", "moe_pre_norm_bwd", "moe_post_norm", "moe_post_norm_bwd",
     "moe_permute", "moe_unpermute_combine", "mxfp8_quantize", "mxfp4_quantize", "mxfp4_dequantize",
-    "moe_grouped_linear_mxfp4",
+    "moe_grouped_linear_mxfp4", "moe_add_norm_mxfp8", "mxfp8_dequantize", "moe_grouped_mlp_fwd_ckpt8",
+    "moe_grouped_mlp_bwd_ckpt8",
     "fp8_tensor_quantize", "mxfp8_quantize_colwise", "fp8_tensor_quantize_colwise", "mxfp8_pack_weight_bwd",
     "fp8_tensor_pack_weight_bwd", "mxfp8_quantize_weights", "fp8_tensor_quantize_weights",
     "moe_grouped_mlp_fwd", "moe_grouped_mlp_bwd", "moe_grouped_linear", "moe_grouped_gate_up_swiglu", "gemm_workspace",
@@ -348,6 +352,43 @@ def moe_post_norm_bwd(dout: torch.Tensor, c: torch.Tensor, rstd: torch.Tensor, w
     return r
 
 
+def moe_add_norm_mxfp8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None,
+                       row_id_map: torch.Tensor | None = None, k: int = 1, eps: float = 1e-6, with_y: bool = False,
+                       save_for_bwd: bool = False, out: torch.Tensor | None = None):
+    """s = residual + x (or, through row_id_map, residual + the sum of each token's k rows of x, as
+    moe_unpermute_combine without weights), its RMS norm n = s * rstd * weight, and n's MXFP8 rows.
+
+    x [T, H] or [T * k, H], residual [T, H], weight [H]: bf16 or float32, one dtype; H % 32 == 0. Returns a dict with
+    codes uint8 [T, H], scales uint8 [T, H / 32], sum [T, H] (s as the norm read it; x itself where nothing is
+    added and out is not given), y (n in x's dtype) with with_y, and rstd [T] with save_for_bwd. out: the sum's
+    tensor, may be residual. Backward: moe_pre_norm_bwd(dy, sum, weight, rstd, dx_in=the gradient past the norm)."""
+    fn = "moe_add_norm_mxfp8"
+    _need(fn, x, weight, residual, row_id_map, out)
+    dt = _norm_dtype(fn, x, weight, residual, out)
+    if k < 1 or (row_id_map is not None and x.shape[0] % k):
+        raise ValueError(f"{fn}: k must be positive and x [T * k, H]")
+    T, H = x.shape[0] // k, x.shape[1]
+    _check_rows(fn, row_id_map, T, k)
+    if weight.shape != (H,):
+        raise ValueError(f"{fn}: weight must be [H]")
+    for t in (residual, out):
+        if t is not None and t.shape != (T, H):
+            raise ValueError(f"{fn}: residual and out must be [T, H]")
+    dev = x.device
+    added = out
+    if added is None and (residual is not None or row_id_map is not None):
+        added = torch.empty((T, H), dtype=x.dtype, device=dev)
+    r = dict(sum=added if added is not None else x, codes=torch.empty((T, H), dtype=torch.uint8, device=dev),
+             scales=torch.empty((T, H // 32), dtype=torch.uint8, device=dev))
+    if with_y:
+        r["y"] = torch.empty((T, H), dtype=x.dtype, device=dev)
+    if save_for_bwd:
+        r["rstd"] = torch.empty(T, dtype=torch.float32, device=dev)
+    _launch(fn, x, _a(x), _a(row_id_map), k, _a(residual), _a(weight), dt, T, H, eps, _a(added), _a(r.get("y")),
+            _a(r.get("rstd")), _a(r["codes"]), _a(r["scales"]))
+    return r
+
+
 def moe_permute(x: torch.Tensor, topk_idx: torch.Tensor, topk_prob: torch.Tensor | None, E: int,
                 x_scale: torch.Tensor | None = None, row_id_map: torch.Tensor | None = None):
     """Group the (token, slot) pairs by expert.
@@ -412,6 +453,33 @@ def mxfp8_quantize(x: torch.Tensor):
     scales = torch.empty((rows, cols // 32), dtype=torch.uint8, device=x.device)
     check("mxfp8_quantize", lib().mxfp8_quantize(_p(x2), rows, cols, _p(codes), _p(scales), _stream(x.device)))
     return codes.reshape(x.shape), scales.reshape(*x.shape[:-1], cols // 32)
+
+
+def mxfp8_dequantize(codes: torch.Tensor, scales: torch.Tensor, src_row: torch.Tensor | None = None,
+                     out: torch.Tensor | None = None) -> torch.Tensor:
+    """MXFP8 codes [..., cols] and scales [..., cols/32] -> their values, bf16 [..., cols].
+
+    src_row int32 [rows] (codes 2-D): out[r] = the values of row src_row[r], bf16 [rows, cols]; rows of out
+    whose index is out of range are left as they were."""
+    fn = "mxfp8_dequantize"
+    _need(fn, codes, scales, src_row, out)
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or codes.dim() < 1 \
+            or scales.shape != (*codes.shape[:-1], codes.shape[-1] // 32):
+        raise ValueError(f"{fn}: codes must be uint8 [..., cols] and scales uint8 [..., cols/32]")
+    cols = codes.shape[-1]
+    src_rows = codes.numel() // cols if cols else 0
+    shape = codes.shape
+    if src_row is not None:
+        if codes.dim() != 2 or src_row.dtype != torch.int32 or src_row.dim() != 1:
+            raise ValueError(f"{fn}: src_row must be int32 [rows], with 2-D codes")
+        shape = (src_row.shape[0], cols)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=codes.device)
+    elif out.dtype != torch.bfloat16 or out.shape != shape:
+        raise ValueError(f"{fn}: out must be bfloat16 [rows, cols]")
+    rows = src_rows if src_row is None else shape[0]
+    _launch(fn, codes, _a(codes), _a(scales), src_rows, cols, _a(src_row), rows, _a(out))
+    return out
 
 
 def mxfp4_quantize(x: torch.Tensor):
@@ -754,6 +822,107 @@ def moe_grouped_mlp_bwd(dy_perm, x_perm, z, h, prob_perm, w_gate_up, w_down, off
         ctypes.byref(desc), R, _p(dy_perm), _p(x_perm), _p(z), _p(h), _p(prob_perm), t1, t2, _p(offsets), _p(dx),
         d1, d2, _p(dprob), _p(ws), ws.numel(), _stream(dev)))
     del k1, k2, k3, k4
+    return dx, dw1, dw2, dprob
+
+
+def _bf16_weights(fn, w_gate_up, w_down, H, dev):
+    """Tables of the experts' bf16 weights [2I, H] and [H, I] -> (table, table, E, I)."""
+    t1, E, shape1, dtype1 = _weight_table(fn, w_gate_up, dev)
+    t2, E2, shape2, dtype2 = _weight_table(fn, w_down, dev)
+    if dtype1 != torch.bfloat16 or dtype2 != torch.bfloat16 or E2 != E or len(shape2) != 2 \
+            or shape1 != (2 * shape2[1], H) or shape2[0] != H:
+        raise ValueError(f"{fn}: weights must be bfloat16, [2I, H] and [H, I] for each of E experts")
+    return t1, t2, E, shape2[1]
+
+
+def _check_prob(fn, prob, R):
+    if prob.dtype != torch.float32 or prob.numel() != R:
+        raise ValueError(f"{fn}: prob_perm must be float32 [R]")
+
+
+def _bf16_out(fn, t, shape, dev):
+    if t is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    if t.dtype != torch.bfloat16 or t.shape != shape:
+        raise ValueError(f"{fn}: an output must be bfloat16 {list(shape)}")
+    return t
+
+
+def moe_grouped_mlp_fwd_ckpt8(x_perm: torch.Tensor, w_gate_up, w_down, offsets: torch.Tensor, prob_perm: torch.Tensor,
+                              out: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """moe_grouped_mlp_fwd in bf16 that keeps its gate_up output in MXFP8 for moe_grouped_mlp_bwd_ckpt8, and
+    nothing else. Returns (y_perm [R, H], z_codes uint8 [R, 2I], z_scales uint8 [R, 2I / 32]).
+
+    y_perm is that of moe_grouped_mlp_fwd, bit for bit; rows past the last expert's are not written."""
+    fn = "moe_grouped_mlp_fwd_ckpt8"
+    _need(fn, x_perm, offsets, prob_perm, out, workspace)
+    if x_perm.dtype != torch.bfloat16 or x_perm.dim() != 2:
+        raise ValueError(f"{fn}: x_perm must be bfloat16 [R, H]")
+    R, H = x_perm.shape
+    dev = x_perm.device
+    t1, t2, E, I = _bf16_weights(fn, w_gate_up, w_down, H, x_perm.get_device())
+    _check_offsets(fn, offsets, E)
+    _check_prob(fn, prob_perm, R)
+    out = _bf16_out(fn, out, (R, H), dev)
+    zc = torch.empty((R, 2 * I), dtype=torch.uint8, device=dev)
+    zs = torch.empty((R, 2 * I // 32), dtype=torch.uint8, device=dev)
+    desc = (E, H, I, MOE_BF16, MOE_BF16, MOE_BF16, 0)
+    need = _size(_lib.MOE_OP_MLP_FWD, desc, R)
+    if workspace is None or workspace.numel() < need:
+        workspace = _workspace(need, dev)
+    _launch(fn, x_perm, ctypes.byref(MlpDesc(*desc)), R, _a(x_perm), t1, t2, _a(offsets), _a(prob_perm), _a(out), _a(zc),
+            _a(zs), _a(workspace), need)
+    return out, zc, zs
+
+
+def moe_grouped_mlp_bwd_ckpt8(dy_perm: torch.Tensor, x: torch.Tensor, z_codes: torch.Tensor, z_scales: torch.Tensor,
+                              prob_perm: torch.Tensor, w_gate_up, w_down, offsets: torch.Tensor,
+                              x_scale: torch.Tensor | None = None, src_token: torch.Tensor | None = None,
+                              dx_perm: torch.Tensor | None = None, dw_gate_up: torch.Tensor | None = None,
+                              dw_down: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """Backward of moe_grouped_mlp_fwd_ckpt8 from what was kept. Returns (dx_perm [R, H], dw_gate_up [E, 2I, H],
+    dw_down [E, H, I], dprob_perm [R] float32).
+
+    x: the block's rows as kept: MXFP8 codes uint8 [T, H] with x_scale uint8 [T, H / 32], one row a token, and
+    src_token int32 [R] (moe_permute's), or codes [R, H] in expert order without src_token; or x_perm bf16 [R, H].
+    h is computed again from z. Rows of dx_perm and dprob_perm past the last expert's are not written."""
+    fn = "moe_grouped_mlp_bwd_ckpt8"
+    _need(fn, dy_perm, x, x_scale, src_token, z_codes, z_scales, prob_perm, offsets, dx_perm, dw_gate_up, dw_down, workspace)
+    if dy_perm.dtype != torch.bfloat16 or dy_perm.dim() != 2:
+        raise ValueError(f"{fn}: dy_perm must be bfloat16 [R, H]")
+    R, H = dy_perm.shape
+    dev = dy_perm.device
+    t1, t2, E, I = _bf16_weights(fn, w_gate_up, w_down, H, dy_perm.get_device())
+    _check_offsets(fn, offsets, E)
+    _check_prob(fn, prob_perm, R)
+    if z_codes.dtype != torch.uint8 or z_codes.shape != (R, 2 * I) or z_scales.dtype != torch.uint8 \
+            or z_scales.shape != (R, 2 * I // 32):
+        raise ValueError(f"{fn}: z_codes must be uint8 [R, 2I] and z_scales uint8 [R, 2I/32]")
+    if x.dim() != 2 or x.shape[1] != H:
+        raise ValueError(f"{fn}: x must have H columns")
+    T = x.shape[0]
+    if x.dtype == torch.uint8:
+        act = MOE_MXFP8
+        if x_scale is None or x_scale.dtype != torch.uint8 or x_scale.shape != (T, H // 32):
+            raise ValueError(f"{fn}: x in 8 bits needs x_scale uint8 [T, H/32]")
+        if (src_token is None and T != R) or (src_token is not None and (src_token.dtype != torch.int32
+                                                                         or src_token.numel() != R)):
+            raise ValueError(f"{fn}: x in 8 bits needs src_token int32 [R], or a row for every routed row")
+    else:
+        act = MOE_BF16
+        if x.dtype != torch.bfloat16 or T != R or x_scale is not None or src_token is not None:
+            raise ValueError(f"{fn}: x must be MXFP8 codes with x_scale, or bfloat16 [R, H] without x_scale and src_token")
+    dx = _bf16_out(fn, dx_perm, (R, H), dev)
+    dw1 = _bf16_out(fn, dw_gate_up, (E, 2 * I, H), dev)
+    dw2 = _bf16_out(fn, dw_down, (E, H, I), dev)
+    dprob = torch.empty(R, dtype=torch.float32, device=dev)
+    d1, d2 = _weight_table(fn, dw1, dy_perm.get_device())[0], _weight_table(fn, dw2, dy_perm.get_device())[0]
+    desc = (E, H, I, MOE_BF16, act, MOE_BF16, 0)
+    need = _size(_lib.MOE_OP_MLP_BWD_CKPT8, desc, R)
+    if workspace is None or workspace.numel() < need:
+        workspace = _workspace(need, dev)
+    _launch(fn, dy_perm, ctypes.byref(MlpDesc(*desc)), R, _a(dy_perm), _a(x), _a(x_scale), T, _a(src_token), _a(z_codes),
+            _a(z_scales), _a(prob_perm), t1, t2, _a(offsets), _a(dx), d1, d2, _a(dprob), _a(workspace), need)
     return dx, dw1, dw2, dprob
 
 

@@ -14,7 +14,7 @@ LIB_PATH = os.path.join(HERE, "libmoe.so")
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_LAUNCH = range(5)
 MOE_F32, MOE_BF16, MOE_MXFP8, MOE_FP8, MOE_MXFP4 = 0, 1, 2, 3, 4
 MOE_OP_PERMUTE, MOE_OP_MLP_FWD, MOE_OP_MLP_BWD, MOE_OP_GROUPED_GEMM, MOE_OP_ROUTER_BWD = 0, 1, 2, 3, 4
-MOE_OP_BALANCE_LOSS, MOE_OP_NORM_BWD, MOE_OP_LINEAR_MXFP4 = 5, 6, 7
+MOE_OP_BALANCE_LOSS, MOE_OP_NORM_BWD, MOE_OP_LINEAR_MXFP4, MOE_OP_MLP_BWD_CKPT8 = 5, 6, 7, 8
 MOE_GATE_NONE, MOE_GATE_TOKEN, MOE_GATE_CHANNEL = 0, 1, 2
 MOE_MAX_EXPERTS = 256
 
@@ -28,6 +28,7 @@ EXPORTS = (
     "moe_balance_loss", "moe_balance_loss_bwd",
     "moe_pre_norm", "moe_pre_norm_bwd", "moe_post_norm", "moe_post_norm_bwd",
     "mxfp4_quantize", "mxfp4_dequantize", "moe_grouped_linear_mxfp4", "moe_pointer_table",
+    "moe_add_norm_mxfp8", "mxfp8_dequantize", "moe_grouped_mlp_fwd_ckpt8", "moe_grouped_mlp_bwd_ckpt8",
     "moe_workspace_size",
     "moe_status_str", "moe_last_error",
 )
@@ -94,6 +95,10 @@ def _declare(lib):
         "mxfp4_dequantize": [vp, vp, i64, i64, vp, vp],
         "moe_grouped_linear_mxfp4": [c_int, i64, c_int, c_int, c_int, vp, vp, vp, vp, vp, vp, vp, sz, vp],
         "moe_pointer_table": [vp, i64, c_int, vp],
+        "moe_add_norm_mxfp8": [vp, vp, c_int, vp, vp, c_int, i64, c_int, f32, vp, vp, vp, vp, vp, vp],
+        "mxfp8_dequantize": [vp, vp, i64, i64, vp, i64, vp, vp],
+        "moe_grouped_mlp_fwd_ckpt8": [vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
+        "moe_grouped_mlp_bwd_ckpt8": [vp, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
         "moe_workspace_size": [c_int, ctypes.POINTER(MlpDesc), i64, i64, c_int, c_int, ctypes.POINTER(sz)],
     }
     for name, args in sig.items():

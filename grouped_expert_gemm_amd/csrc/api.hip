@@ -107,6 +107,12 @@ extern "C" moe_status moe_workspace_size(moe_op op, const moe_mlp_desc* desc, in
         return s;
       *bytes = mx4::linear_workspace_bytes(desc->E, R, desc->H, desc->I, desc->act);
       return MOE_OK;
+    case MOE_OP_MLP_BWD_CKPT8:
+      if (!desc || R < 0 || R > 0x7FFFFFFF)
+        return fail(MOE_ERR_INVALID_ARG, "moe_workspace_size(MLP_BWD_CKPT8): desc NULL or R out of [0, 2^31)");
+      if (const moe_status s = validate_ckpt8(*desc, true, "moe_workspace_size(MLP_BWD_CKPT8)"); s != MOE_OK) return s;
+      *bytes = mlp_bwd_ckpt8_workspace_bytes(*desc, R);
+      return MOE_OK;
   }
   return fail(MOE_ERR_INVALID_ARG, "moe_workspace_size: unknown op");
 }

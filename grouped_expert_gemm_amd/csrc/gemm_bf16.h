@@ -16,7 +16,13 @@ constexpr int kLdsBytes = kStages * kStageBytes;
 
 enum { KCONTIG = 0, MNCONTIG = 1 };
 enum { GROUP_M = 0, GROUP_K = 1 };
-enum { EPI_STORE = 0, EPI_SWIGLU = 1, EPI_DSWIGLU = 2 };
+enum {
+  EPI_STORE = 0,
+  EPI_SWIGLU = 1,
+  EPI_DSWIGLU = 2,
+  EPI_SWIGLU_MX8 = 3  // SWIGLU that also writes the gate_up output in MXFP8
+};
+constexpr bool is_swiglu(int ep) { return ep == EPI_SWIGLU || ep == EPI_SWIGLU_MX8; }
 
 struct Params {
   // GROUP_M: per-expert P operand (weights). GROUP_K: per-expert output C.
@@ -33,7 +39,7 @@ struct Params {
   int64_t R;
   int M, N, K;            // GROUP_M uses N, K; GROUP_K uses M, N
   int E, I;
-  int n_tiles;            // output column tiles (SWIGLU: I / 128, else N / 256)
+  int n_tiles;            // output column tiles (SWIGLU, SWIGLU_MX8: I / 128, else N / 256)
   // split-K tail (forward kernel): when the last round of tiles would leave at least
   // half the CUs idle, its tiles are cut into K chunks whose float32 partial tiles go
   // to `tail` (tail_cap of them at most; 0 = never split) and are finished by
@@ -42,6 +48,8 @@ struct Params {
   float* tail;
   int32_t* tail_meta;
   int tail_cap;
+  uint8_t* z8;   // SWIGLU_MX8: E4M3 codes of the gate_up output [R, 2I] (out)
+  uint8_t* z8s;  // ... and its E8M0 scales [R, 2I / 32] (out)
 };
 
 constexpr size_t kTailTileBytes = (size_t)kBM * kBN * 4;  // one float32 partial tile
@@ -51,8 +59,8 @@ inline size_t tail_ws_bytes(int units) { return kTailMetaSpace + (size_t)units *
 
 moe_status run(const Params& p, int pl, int ql, int g, int ep, int64_t max_tiles, hipStream_t s,
                const char* what);
-// forward kernel (gemm_fwd.hip): GROUP_M, both operands KCONTIG, EPI_STORE or EPI_SWIGLU,
-// K a multiple of 64
+// forward kernel (gemm_fwd.hip): GROUP_M, both operands KCONTIG, EPI_STORE, EPI_SWIGLU or
+// EPI_SWIGLU_MX8, K a multiple of 64
 moe_status run_fwd(const Params& p, int ep, int64_t max_tiles, hipStream_t s, const char* what);
 // sums the split-K partial tiles that run_fwd left in p.tail and applies the epilogue
 moe_status run_tail_reduce(const Params& p, int ep, int64_t max_tiles, hipStream_t s, const char* what);

@@ -28,6 +28,8 @@
 #include "gemm_bf16.h"
 #include "gemm_common.h"
 #include "internal.h"
+#include "lanes.h"
+#include "mxfp8.h"
 
 namespace moe {
 namespace gemm {
@@ -174,7 +176,7 @@ void grouped_gemm_fwd_kernel(const Params prm) {
     const bf16_t* pbase = reinterpret_cast<const bf16_t*>(prm.tab[e]);
     const int64_t kshift = (int64_t)k0 * kWBK * 2;
     const char* p_tile;
-    if constexpr (EP == EPI_SWIGLU) p_tile = reinterpret_cast<const char*>(pbase + (int64_t)nt * 128 * prm.p_ld);
+    if constexpr (is_swiglu(EP)) p_tile = reinterpret_cast<const char*>(pbase + (int64_t)nt * 128 * prm.p_ld);
     else p_tile = reinterpret_cast<const char*>(pbase + (int64_t)nt * kBN * prm.p_ld);
     p_tile += kshift;
     const char* q_tile = reinterpret_cast<const char*>(prm.q + (int64_t)tile_row * prm.q_ld) + kshift;
@@ -182,7 +184,7 @@ void grouped_gemm_fwd_kernel(const Params prm) {
     const uint32_t q_off0 = (uint32_t)(((int64_t)kc_row0 * prm.q_ld + kc_chunk * 8) * 2);
     const int64_t q_extent = (int64_t)(row_end - tile_row) * prm.q_ld * 2 - kshift;
     // SWIGLU: tile rows 128..255 of P are the up rows, I further down than the gate rows
-    const int p_up = (EP == EPI_SWIGLU) ? prm.I - 128 : 0;
+    const int p_up = is_swiglu(EP) ? prm.I - 128 : 0;
 
     // one operand of K step kt into a half-slot; round i's rows: i * 32 (+ up for i >= 4),
     // below 2^32 bytes from the tile origin (one expert's weight)
@@ -410,7 +412,7 @@ void grouped_gemm_fwd_kernel(const Params prm) {
         drain(wv < 2 ? sH0 : sH1, c0, prm.c_ld);
         drain(wv < 2 ? sH2 : sH3, c0 + 128, prm.c_ld);
         lds_barrier();  // read out before the next tile's copies land
-      } else {  // EPI_SWIGLU: gate columns in block 0, the matching up columns in block 1
+      } else {  // SWIGLU: gate columns in block 0, the matching up columns in block 1
         uint8_t* harr = em ? sH1 : sH0;
         // the lane's four routing weights, loaded together: one memory round trip, not four
         float pw[4];
@@ -438,10 +440,71 @@ void grouped_gemm_fwd_kernel(const Params prm) {
             }
         }
         const int64_t I = prm.I;
-        if (prm.zout) acc_block(0, sH2, sH3);
+        if constexpr (EP == EPI_SWIGLU_MX8) {
+          // z as MXFP8. A sub-tile's 32 columns are one block of each row, 16 values in this
+          // lane and 16 in lane ^ 32; its codes go to LDS rows of 128 bytes (gate: sH2, up:
+          // sH3; chunk c of row r at c ^ swz8(r)) and its scale bytes to sH4, 8 a row (4 of
+          // the gate columns, 4 of the up columns). A lane's four code words are every other
+          // word of the block; two half swaps turn them into its first or second 16 bytes.
+#pragma unroll
+          for (int sn = 0; sn < 4; ++sn)
+#pragma unroll
+            for (int sm = 0; sm < 4; ++sm) {
+              uint32_t top = 0;
+#pragma unroll
+              for (int x = 0; x < 16; ++x) {
+                const uint32_t m = __float_as_uint(acc[sn][sm][x]) & 0x7FFFFFFFu;
+                top = m > top ? m : top;
+              }
+              const auto both = __builtin_amdgcn_permlane32_swap(top, top, false, false);
+              top = both[0] > both[1] ? both[0] : both[1];
+              const int b = mx8::scale_byte(top);
+              const float inv = mx8::inverse_scale(b);
+              uint32_t w[4];
+#pragma unroll
+              for (int i4 = 0; i4 < 4; ++i4) {
+                w[i4] = e4m3_pack4(acc[sn][sm][i4 * 4 + 0] * inv, acc[sn][sm][i4 * 4 + 1] * inv,
+                                   acc[sn][sm][i4 * 4 + 2] * inv, acc[sn][sm][i4 * 4 + 3] * inv);
+                w[i4] = b == 255 ? 0 : w[i4];
+              }
+              const auto s02 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+              const auto s13 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+              const int row = em * 128 + sm * 32 + e32;
+              const int chunk = en * 4 + (sn & 1) * 2 + ehi;
+              *reinterpret_cast<uint4*>((sn >> 1 ? sH3 : sH2) + row * 128 + ((chunk ^ swz8(row)) << 4)) =
+                  make_uint4(s02[0], s02[1], s13[0], s13[1]);
+              if (ehi == 0) sH4[row * 8 + (sn >> 1) * 4 + en * 2 + (sn & 1)] = (uint8_t)b;
+            }
+        } else {
+          if (prm.zout) acc_block(0, sH2, sH3);
+        }
         lds_barrier();
         drain(wv < 2 ? sH0 : sH1, prm.c + (int64_t)nt * 128, prm.c_ld);
-        if (prm.zout) {
+        if constexpr (EP == EPI_SWIGLU_MX8) {
+          // 8 whole rows of 128 bytes per store; rows past the expert fall outside the range
+          auto drain8 = [&](const uint8_t* arr, uint8_t* dst) {
+            const int64_t ldb = 2 * I;
+            const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+                (void*)(dst + (int64_t)tile_row * ldb), (short)0, (int)(uint32_t)(valid * ldb), kBufferFlags);
+            const int pc = ln & 7;
+            const uint32_t vo = (uint32_t)((ln >> 3) * ldb + pc * 16);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int row = wv * 64 + 8 * i + (ln >> 3);
+              const v4u32 v = *reinterpret_cast<const v4u32*>(arr + row * 128 + ((pc ^ swz8(row)) << 4));
+              __builtin_amdgcn_raw_buffer_store_b128(v, rs, vo, (int)((wv * 64 + 8 * i) * ldb), 0);
+            }
+          };
+          drain8(sH2, prm.z8 + (int64_t)nt * 128);
+          drain8(sH3, prm.z8 + I + (int64_t)nt * 128);
+          const int row = wv * 64 + ln;
+          if (row < valid) {
+            uint8_t* dst = prm.z8s + (int64_t)(tile_row + row) * (I / 16) + nt * 4;
+            const uint2 v = *reinterpret_cast<const uint2*>(sH4 + row * 8);
+            *reinterpret_cast<uint32_t*>(dst) = v.x;
+            *reinterpret_cast<uint32_t*>(dst + I / 32) = v.y;
+          }
+        } else if (prm.zout) {
           drain(wv < 2 ? sH2 : sH3, prm.zout + (int64_t)nt * 128, 2 * I);
           lds_barrier();
           acc_block(1, sH0, sH1);
@@ -461,7 +524,7 @@ __global__ __launch_bounds__(256) void tail_reduce_kernel(const Params prm) {
   const int32_t* meta = prm.tail_meta;
   const int n_tail = meta[0];
   const int split = meta[1];
-  constexpr int kCols = (EP == EPI_SWIGLU) ? 128 : kBN;  // output columns of a tile
+  constexpr int kCols = is_swiglu(EP) ? 128 : kBN;  // output columns of a tile
   constexpr int kThreadsPerRow = kCols / 4;
   constexpr int kRowsPerBlock = 256 / kThreadsPerRow;
   constexpr int kBlocksPerTile = kBM / kRowsPerBlock;
@@ -496,7 +559,25 @@ __global__ __launch_bounds__(256) void tail_reduce_kernel(const Params prm) {
     *reinterpret_cast<uint2*>(prm.c + mg * prm.c_ld + col) =
         make_uint2(pack_bf16x2(silu_f(g.x) * u.x * p, silu_f(g.y) * u.y * p),
                    pack_bf16x2(silu_f(g.z) * u.z * p, silu_f(g.w) * u.w * p));
-    if (prm.zout) {
+    if constexpr (EP == EPI_SWIGLU_MX8) {  // 8 neighbouring threads hold a block of 32 columns
+      auto put = [&](const float4& v, int64_t at) {
+        const float f[4] = {v.x, v.y, v.z, v.w};
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t m = __float_as_uint(f[i]) & 0x7FFFFFFFu;
+          top = m > top ? m : top;
+        }
+        const int b = mx8::scale_byte(lanes_umax<8>(top));
+        const float inv = mx8::inverse_scale(b);
+        const uint32_t w = e4m3_pack4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+        const int64_t row = mg * (2 * (int64_t)prm.I);
+        *reinterpret_cast<uint32_t*>(prm.z8 + row + at) = b == 255 ? 0 : w;
+        if ((threadIdx.x & 7) == 0) prm.z8s[(row + at) / 32] = (uint8_t)b;
+      };
+      put(g, col);
+      put(u, prm.I + col);
+    } else if (prm.zout) {
       bf16_t* z = prm.zout + mg * (2 * (int64_t)prm.I);
       *reinterpret_cast<uint2*>(z + col) = make_uint2(pack_bf16x2(g.x, g.y), pack_bf16x2(g.z, g.w));
       *reinterpret_cast<uint2*>(z + prm.I + col) = make_uint2(pack_bf16x2(u.x, u.y), pack_bf16x2(u.z, u.w));
@@ -522,6 +603,7 @@ moe_status run_fwd(const Params& p, int ep, int64_t max_tiles, hipStream_t s, co
     return fail(MOE_ERR_INVALID_ARG, std::string(what) + ": split-K tail area missing");
   moe_status st;
   if (ep == EPI_SWIGLU) st = launch_fwd<EPI_SWIGLU>(p, max_tiles, s, what);
+  else if (ep == EPI_SWIGLU_MX8) st = launch_fwd<EPI_SWIGLU_MX8>(p, max_tiles, s, what);
   else if (ep == EPI_STORE) st = launch_fwd<EPI_STORE>(p, max_tiles, s, what);
   else return fail(MOE_ERR_UNSUPPORTED, std::string(what) + ": no forward kernel for this epilogue");
   if (st != MOE_OK || p.tail_cap <= 0 || max_tiles <= 0) return st;
@@ -536,6 +618,8 @@ moe_status run_tail_reduce(const Params& p, int ep, int64_t max_tiles, hipStream
   if (max_tail <= 0) return MOE_OK;
   if (ep == EPI_SWIGLU) {
     hipLaunchKernelGGL((tail_reduce_kernel<EPI_SWIGLU>), dim3((unsigned)(max_tail * (kBM / 8))), dim3(256), 0, s, p);
+  } else if (ep == EPI_SWIGLU_MX8) {
+    hipLaunchKernelGGL((tail_reduce_kernel<EPI_SWIGLU_MX8>), dim3((unsigned)(max_tail * (kBM / 8))), dim3(256), 0, s, p);
   } else {
     hipLaunchKernelGGL((tail_reduce_kernel<EPI_STORE>), dim3((unsigned)(max_tail * (kBM / 4))), dim3(256), 0, s, p);
   }

@@ -17,6 +17,8 @@ size_t permute_workspace_bytes(int64_t T, int E, int k);
 moe_status validate_desc(const moe_mlp_desc& d, bool backward);
 size_t mlp_fwd_workspace_bytes(const moe_mlp_desc& d, int64_t R);
 size_t mlp_bwd_workspace_bytes(const moe_mlp_desc& d, int64_t R);
+moe_status validate_ckpt8(const moe_mlp_desc& d, bool backward, const char* what);
+size_t mlp_bwd_ckpt8_workspace_bytes(const moe_mlp_desc& d, int64_t R);
 size_t grouped_gemm_workspace_bytes();  // split-K tail area of one grouped GEMM call
 size_t router_bwd_workspace_bytes(int64_t T, int H, int E);  // dW token-chunk partials
 size_t balance_workspace_bytes(int64_t T, int64_t seq_len, int E);  // partial sums of moe_balance_loss

@@ -11,6 +11,7 @@
 #include "gemm_mx.h"
 #include "internal.h"
 #include "mxfp4.h"
+#include "mxfp8.h"
 
 namespace moe {
 
@@ -86,6 +87,30 @@ size_t mlp_bwd_workspace_bytes(const moe_mlp_desc& d, int64_t R) {
   return a256(R * 2 * I * 2) + a256((size_t)2 * (I / 256) * R * 4) + grouped_gemm_workspace_bytes();
 }
 
+moe_status validate_ckpt8(const moe_mlp_desc& d, bool backward, const char* what) {
+  const std::string fn(what);
+  if (d.E < 1 || d.E > MOE_MAX_EXPERTS) return fail(MOE_ERR_INVALID_ARG, fn + ": E out of [1, 256]");
+  if (d.H < 1 || d.I < 1) return fail(MOE_ERR_INVALID_ARG, fn + ": H and I must be positive");
+  if (d.compute != MOE_BF16 || d.wt != MOE_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, fn + ": 8-bit checkpoints are built for bf16 products (compute and wt MOE_BF16)");
+  if (d.act != MOE_BF16 && !(backward && d.act == MOE_MXFP8))
+    return fail(MOE_ERR_UNSUPPORTED, fn + (backward ? ": act must be MOE_BF16 or MOE_MXFP8" : ": act must be MOE_BF16"));
+  if (d.H % 256 != 0 || d.I % 256 != 0) return fail(MOE_ERR_UNSUPPORTED, fn + ": needs H % 256 == 0 and I % 256 == 0");
+  if ((int64_t)d.H * d.I * 2 > 0x7FFFFFFFLL) return fail(MOE_ERR_UNSUPPORTED, fn + ": one expert's weight exceeds 2^31 bytes");
+  return MOE_OK;
+}
+
+// [dZ] [h, then x] [dprob partials] [split-K tail]
+static size_t ckpt8_rows_bytes(const moe_mlp_desc& d, int64_t R) {
+  const int64_t wide = d.act == MOE_MXFP8 && d.H > d.I ? d.H : d.I;
+  return a256((size_t)R * wide * 2);
+}
+
+size_t mlp_bwd_ckpt8_workspace_bytes(const moe_mlp_desc& d, int64_t R) {
+  return a256((size_t)R * 2 * d.I * 2) + ckpt8_rows_bytes(d, R) + a256((size_t)2 * (d.I / 256) * R * 4) +
+         grouped_gemm_workspace_bytes();
+}
+
 static moe_status check_table(const void* const* t, int E, size_t align, const char* what) {
   if (!t) return fail(MOE_ERR_INVALID_ARG, std::string(what) + ": pointer table is NULL");
   for (int e = 0; e < E; ++e) {
@@ -107,8 +132,9 @@ static PtrTab make_tab(const void* const* t, int E) {
 // dprob[r] = sum over j of part[j][r] in a fixed order (deterministic): 8 threads per
 // row each add the partials j = q, q + 8, ... in increasing j, then the 8 sums are added
 // in q order. 32 rows per workgroup, consecutive threads on consecutive rows.
+// rows from *end on (end != NULL) are not written.
 __global__ __launch_bounds__(256) void reduce_partials(const float* __restrict__ part, int nparts, int64_t R,
-                                                       float* __restrict__ out) {
+                                                       float* __restrict__ out, const int32_t* __restrict__ end) {
   __shared__ float sums[8][32];
   const int rl = threadIdx.x & 31, q = threadIdx.x >> 5;
   const int64_t r = (int64_t)blockIdx.x * 32 + rl;
@@ -121,11 +147,10 @@ __global__ __launch_bounds__(256) void reduce_partials(const float* __restrict__
     float t = sums[0][rl];
 #pragma unroll
     for (int i = 1; i < 8; ++i) t += sums[i][rl];
-    out[r] = t;
+    if (!end || r < *end) out[r] = t;
   }
 }
 
-// bf16 GroupedLinear(gate_up) + ScaledSwiGLU: h [R, I] (and z [R, 2I] when z != NULL)
 // split-K tail area carved from a workspace (nullptr: the kernels never split)
 struct TailArea {
   float* part = nullptr;
@@ -146,9 +171,11 @@ static void set_tail(gemm::Params& p, const TailArea& t) {
   p.tail_cap = t.cap;
 }
 
+// bf16 GroupedLinear(gate_up) + ScaledSwiGLU: h [R, I] (and z [R, 2I] when z != NULL, or its MXFP8
+// codes and scales when z8 != NULL)
 static moe_status bf16_gate_up(int E, int64_t R, int H, int I, const bf16_t* x, const PtrTab& w,
                                const int32_t* offsets, const float* prob, bf16_t* h, bf16_t* z, hipStream_t s,
-                               const TailArea& tail = TailArea()) {
+                               const TailArea& tail = TailArea(), uint8_t* z8 = nullptr, uint8_t* z8s = nullptr) {
   gemm::Params p;
   std::memset(&p, 0, sizeof(p));
   set_tail(p, tail);
@@ -161,6 +188,8 @@ static moe_status bf16_gate_up(int E, int64_t R, int H, int I, const bf16_t* x, 
   p.offsets = offsets;
   p.prob = prob;
   p.zout = z;
+  p.z8 = z8;
+  p.z8s = z8s;
   p.R = R;
   p.N = 2 * I;
   p.K = H;
@@ -168,8 +197,8 @@ static moe_status bf16_gate_up(int E, int64_t R, int H, int I, const bf16_t* x, 
   p.I = I;
   p.n_tiles = I / 128;
   const int64_t mtiles = (R + gemm::kBM - 1) / gemm::kBM + E;
-  return gemm::run(p, gemm::KCONTIG, gemm::KCONTIG, gemm::GROUP_M, gemm::EPI_SWIGLU, mtiles * p.n_tiles, s,
-                   "grouped gate_up + ScaledSwiGLU");
+  return gemm::run(p, gemm::KCONTIG, gemm::KCONTIG, gemm::GROUP_M, z8 ? gemm::EPI_SWIGLU_MX8 : gemm::EPI_SWIGLU,
+                   mtiles * p.n_tiles, s, "grouped gate_up + ScaledSwiGLU");
 }
 
 // bf16 GroupedLinear: y [R, N] = x [R, K] W_e^T
@@ -193,6 +222,105 @@ static moe_status bf16_linear(int E, int64_t R, int K, int N, const bf16_t* x, c
   const int64_t mtiles = (R + gemm::kBM - 1) / gemm::kBM + E;
   return gemm::run(q, gemm::KCONTIG, gemm::KCONTIG, gemm::GROUP_M, gemm::EPI_STORE, mtiles * q.n_tiles, s,
                    "grouped linear");
+}
+
+// The products of the bf16 backward. dH = dY W2_e (W2_e is [H][I]: K rows, I contiguous) with the
+// dSwiGLU epilogue: dz [R, 2I] from z [R, 2I] (which may be dz itself: a tile reads its part of z
+// before it writes there), and dprob (rows from *end on not written, end != NULL).
+static moe_status bf16_down_dgrad(const moe_mlp_desc& d, int64_t R, const bf16_t* dy, const PtrTab& w2,
+                                  const int32_t* offsets, const float* prob, const bf16_t* z, bf16_t* dz, float* part,
+                                  float* dprob, const int32_t* end, hipStream_t s) {
+  gemm::Params p;
+  std::memset(&p, 0, sizeof(p));
+  std::memcpy(p.tab, w2.p, sizeof(p.tab));
+  p.q = dy;
+  p.q_ld = d.H;
+  p.p_ld = d.I;
+  p.c = dz;
+  p.c_ld = 2 * (int64_t)d.I;
+  p.offsets = offsets;
+  p.prob = prob;
+  p.zin = z;
+  p.part = part;
+  p.R = R;
+  p.N = d.I;
+  p.K = d.H;
+  p.E = d.E;
+  p.I = d.I;
+  p.n_tiles = d.I / gemm::kBN;
+  const int64_t mtiles = (R + gemm::kBM - 1) / gemm::kBM + d.E;
+  moe_status st = gemm::run(p, gemm::MNCONTIG, gemm::KCONTIG, gemm::GROUP_M, gemm::EPI_DSWIGLU, mtiles * p.n_tiles, s,
+                            "moe_grouped_mlp_bwd(down dgrad)");
+  if (st != MOE_OK) return st;
+  hipLaunchKernelGGL(reduce_partials, dim3((unsigned)((R + 31) / 32)), dim3(256), 0, s, (const float*)part,
+                     2 * p.n_tiles, R, dprob, end);
+  return check_launch("moe_grouped_mlp_bwd(dprob)");
+}
+
+// dX = dZ W1_e (W1_e is [2I][H]: K rows, H contiguous)
+static moe_status bf16_gate_up_dgrad(const moe_mlp_desc& d, int64_t R, const bf16_t* dz, const PtrTab& w1,
+                                     const int32_t* offsets, bf16_t* dx, const TailArea& tail, hipStream_t s) {
+  gemm::Params q;
+  std::memset(&q, 0, sizeof(q));
+  std::memcpy(q.tab, w1.p, sizeof(q.tab));
+  q.q = dz;
+  q.q_ld = 2 * (int64_t)d.I;
+  q.p_ld = d.H;
+  q.c = dx;
+  q.c_ld = d.H;
+  q.offsets = offsets;
+  q.R = R;
+  q.N = d.H;
+  q.K = 2 * d.I;
+  q.E = d.E;
+  q.I = d.I;
+  q.n_tiles = d.H / gemm::kBN;
+  set_tail(q, tail);
+  const int64_t mtiles = (R + gemm::kBM - 1) / gemm::kBM + d.E;
+  return gemm::run(q, gemm::MNCONTIG, gemm::KCONTIG, gemm::GROUP_M, gemm::EPI_STORE, mtiles * q.n_tiles, s,
+                   "moe_grouped_mlp_bwd(gate_up dgrad)");
+}
+
+// dW_e[m][n] = sum_r a[r][m] b[r][n] over expert e's rows, a [R, M] and b [R, N]
+static moe_status bf16_wgrad(const moe_mlp_desc& d, int64_t R, const bf16_t* a, int M, const bf16_t* b, int N,
+                             const PtrTab& dw, const int32_t* offsets, hipStream_t s, const char* what) {
+  gemm::Params w;
+  std::memset(&w, 0, sizeof(w));
+  std::memcpy(w.tab, dw.p, sizeof(w.tab));
+  w.p = b;
+  w.p_ld = N;
+  w.q = a;
+  w.q_ld = M;
+  w.c_ld = N;
+  w.offsets = offsets;
+  w.R = R;
+  w.M = M;
+  w.N = N;
+  w.E = d.E;
+  w.I = d.I;
+  w.n_tiles = N / gemm::kBN;
+  return gemm::run(w, gemm::MNCONTIG, gemm::MNCONTIG, gemm::GROUP_K, gemm::EPI_STORE,
+                   (int64_t)d.E * (M / gemm::kBM) * w.n_tiles, s, what);
+}
+
+// h = silu(g) u p of the gate_up values z [R, 2I], for the rows before *end
+__global__ __launch_bounds__(256) void swiglu_rows_kernel(const uint4* __restrict__ z, const float* __restrict__ prob,
+                                                          int64_t R, uint32_t groups, const int32_t* __restrict__ end,
+                                                          uint4* __restrict__ h) {
+  const int64_t n = *end < 0 ? 0 : *end < R ? *end : R;
+  for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < n * groups; q += (int64_t)gridDim.x * 256) {
+    const int64_t r = q / groups, c = q - r * groups;
+    const uint4 g = z[r * 2 * groups + c], u = z[r * 2 * groups + groups + c];
+    const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
+    const float p = prob[r];
+    uint32_t o[4];
+    for (int i = 0; i < 4; ++i) {
+      const float g0 = bf16_to_f32(gw[i] & 0xFFFFu), g1 = bf16_to_f32(gw[i] >> 16);
+      const float u0 = bf16_to_f32(uw[i] & 0xFFFFu), u1 = bf16_to_f32(uw[i] >> 16);
+      o[i] = pack_bf16x2(g0 / (1.f + __expf(-g0)) * u0 * p, g1 / (1.f + __expf(-g1)) * u1 * p);
+    }
+    h[q] = make_uint4(o[0], o[1], o[2], o[3]);
+  }
 }
 
 }  // namespace moe
@@ -392,100 +520,125 @@ extern "C" moe_status moe_grouped_mlp_bwd(const moe_mlp_desc* desc, int64_t R, c
                                    dw_gate_up, dw_down, dprob_perm, (uint8_t*)workspace, s);
   }
 
-  const int64_t H = d.H, I = d.I;
   uint8_t* ws = (uint8_t*)workspace;
   bf16_t* dz = (bf16_t*)ws;
-  ws += a256(R * 2 * I * 2);
+  ws += a256((size_t)R * 2 * d.I * 2);
   float* part = (float*)ws;
-  ws += a256((size_t)2 * (I / 256) * R * 4);
+  ws += a256((size_t)2 * (d.I / 256) * R * 4);
   const TailArea tail = tail_area(ws);  // split-K tail of the gate_up dgrad
-  const int64_t mtiles = (R + gemm::kBM - 1) / gemm::kBM + d.E;
-
   if (R > 0) {
-    // down dgrad with the dSwiGLU / dprob epilogue: dH = dY W2_e (W2_e is [H][I]: K rows, I contiguous)
-    gemm::Params p;
-    std::memset(&p, 0, sizeof(p));
-    std::memcpy(p.tab, w2.p, sizeof(p.tab));
-    p.q = (const bf16_t*)dy_perm;
-    p.q_ld = H;
-    p.p_ld = I;
-    p.c = dz;
-    p.c_ld = 2 * I;
-    p.offsets = offsets;
-    p.prob = prob_perm;
-    p.zin = (const bf16_t*)z_save;
-    p.part = part;
-    p.R = R;
-    p.N = (int)I;
-    p.K = (int)H;
-    p.E = d.E;
-    p.I = (int)I;
-    p.n_tiles = (int)(I / gemm::kBN);
-    st = gemm::run(p, gemm::MNCONTIG, gemm::KCONTIG, gemm::GROUP_M, gemm::EPI_DSWIGLU, mtiles * p.n_tiles, s,
-                   "moe_grouped_mlp_bwd(down dgrad)");
-    if (st != MOE_OK) return st;
-    hipLaunchKernelGGL(reduce_partials, dim3((unsigned)((R + 31) / 32)), dim3(256), 0, s, (const float*)part,
-                       2 * p.n_tiles, R, dprob_perm);
-    if ((st = check_launch("moe_grouped_mlp_bwd(dprob)")) != MOE_OK) return st;
-
-    // gate_up dgrad: dX = dZ W1_e (W1_e is [2I][H]: K rows, H contiguous)
-    gemm::Params q;
-    std::memset(&q, 0, sizeof(q));
-    std::memcpy(q.tab, w1.p, sizeof(q.tab));
-    q.q = dz;
-    q.q_ld = 2 * I;
-    q.p_ld = H;
-    q.c = (bf16_t*)dx_perm;
-    q.c_ld = H;
-    q.offsets = offsets;
-    q.R = R;
-    q.N = (int)H;
-    q.K = (int)(2 * I);
-    q.E = d.E;
-    q.I = (int)I;
-    q.n_tiles = (int)(H / gemm::kBN);
-    set_tail(q, tail);
-    st = gemm::run(q, gemm::MNCONTIG, gemm::KCONTIG, gemm::GROUP_M, gemm::EPI_STORE, mtiles * q.n_tiles, s,
-                   "moe_grouped_mlp_bwd(gate_up dgrad)");
-    if (st != MOE_OK) return st;
+    if ((st = bf16_down_dgrad(d, R, (const bf16_t*)dy_perm, w2, offsets, prob_perm, (const bf16_t*)z_save, dz, part,
+                              dprob_perm, nullptr, s)) != MOE_OK)
+      return st;
+    if ((st = bf16_gate_up_dgrad(d, R, dz, w1, offsets, (bf16_t*)dx_perm, tail, s)) != MOE_OK) return st;
   }
-
-  // down wgrad: dW2_e[h][i] = sum_r dY[r][h] * Hs[r][i]
-  gemm::Params w;
-  std::memset(&w, 0, sizeof(w));
-  std::memcpy(w.tab, dw2.p, sizeof(w.tab));
-  w.p = (const bf16_t*)h_save;
-  w.p_ld = I;
-  w.q = (const bf16_t*)dy_perm;
-  w.q_ld = H;
-  w.c_ld = I;
-  w.offsets = offsets;
-  w.R = R;
-  w.M = (int)H;
-  w.N = (int)I;
-  w.E = d.E;
-  w.I = (int)I;
-  w.n_tiles = (int)(I / gemm::kBN);
-  st = gemm::run(w, gemm::MNCONTIG, gemm::MNCONTIG, gemm::GROUP_K, gemm::EPI_STORE,
-                 (int64_t)d.E * (H / gemm::kBM) * w.n_tiles, s, "moe_grouped_mlp_bwd(down wgrad)");
+  st = bf16_wgrad(d, R, (const bf16_t*)dy_perm, d.H, (const bf16_t*)h_save, d.I, dw2, offsets, s,
+                  "moe_grouped_mlp_bwd(down wgrad)");
   if (st != MOE_OK) return st;
+  return bf16_wgrad(d, R, dz, 2 * d.I, (const bf16_t*)x_perm, d.H, dw1, offsets, s, "moe_grouped_mlp_bwd(gate_up wgrad)");
+}
 
-  // gate_up wgrad: dW1_e[j][h] = sum_r dZ[r][j] * X[r][h]
-  gemm::Params v;
-  std::memset(&v, 0, sizeof(v));
-  std::memcpy(v.tab, dw1.p, sizeof(v.tab));
-  v.p = (const bf16_t*)x_perm;
-  v.p_ld = H;
-  v.q = dz;
-  v.q_ld = 2 * I;
-  v.c_ld = H;
-  v.offsets = offsets;
-  v.R = R;
-  v.M = (int)(2 * I);
-  v.N = (int)H;
-  v.E = d.E;
-  v.I = (int)I;
-  v.n_tiles = (int)(H / gemm::kBN);
-  return gemm::run(v, gemm::MNCONTIG, gemm::MNCONTIG, gemm::GROUP_K, gemm::EPI_STORE,
-                   (int64_t)d.E * (2 * I / gemm::kBM) * v.n_tiles, s, "moe_grouped_mlp_bwd(gate_up wgrad)");
+extern "C" moe_status moe_grouped_mlp_fwd_ckpt8(const moe_mlp_desc* desc, int64_t R, const void* x_perm,
+                                                const void* const* w_gate_up, const void* const* w_down,
+                                                const int32_t* offsets, const float* prob_perm, void* y_perm,
+                                                uint8_t* z_codes, uint8_t* z_scales, void* workspace,
+                                                size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_grouped_mlp_fwd_ckpt8";
+  if (!desc) return fail(MOE_ERR_INVALID_ARG, std::string(fn) + ": desc is NULL");
+  moe_mlp_desc d = *desc;
+  d.save_for_bwd = 0;
+  moe_status st = validate_ckpt8(d, false, fn);
+  if (st != MOE_OK) return st;
+  if (R < 0 || R > 0x7FFFFFFF) return fail(MOE_ERR_INVALID_ARG, std::string(fn) + ": R out of [0, 2^31)");
+  if (R == 0) return MOE_OK;
+  if (!x_perm || !offsets || !prob_perm || !y_perm || !z_codes || !z_scales)
+    return fail(MOE_ERR_INVALID_ARG, std::string(fn) + ": NULL pointer");
+  if (!aligned(x_perm, 16) || !aligned(y_perm, 16) || !aligned(z_codes, 16) || !aligned(z_scales, 4) ||
+      !aligned(offsets, 4) || !aligned(prob_perm, 4))
+    return fail(MOE_ERR_INVALID_ARG, std::string(fn) + ": misaligned tensor");
+  if ((st = check_table(w_gate_up, d.E, 16, "moe_grouped_mlp_fwd_ckpt8(w_gate_up)")) != MOE_OK) return st;
+  if ((st = check_table(w_down, d.E, 16, "moe_grouped_mlp_fwd_ckpt8(w_down)")) != MOE_OK) return st;
+  if (workspace_bytes < mlp_fwd_workspace_bytes(d, R))
+    return fail(MOE_ERR_WORKSPACE, std::string(fn) + ": workspace too small");
+  if (!workspace || !aligned(workspace, 256))
+    return fail(MOE_ERR_INVALID_ARG, std::string(fn) + ": workspace NULL or not 256-byte aligned");
+  const hipStream_t s = as_stream(stream);
+  bf16_t* h = (bf16_t*)workspace;
+  const TailArea tail = tail_area((uint8_t*)workspace + a256((size_t)R * d.I * 2));
+  st = bf16_gate_up(d.E, R, d.H, d.I, (const bf16_t*)x_perm, make_tab(w_gate_up, d.E), offsets, prob_perm, h, nullptr, s,
+                    tail, z_codes, z_scales);
+  if (st != MOE_OK) return st;
+  return bf16_linear(d.E, R, d.I, d.H, h, make_tab(w_down, d.E), offsets, (bf16_t*)y_perm, s, tail);
+}
+
+extern "C" moe_status moe_grouped_mlp_bwd_ckpt8(const moe_mlp_desc* desc, int64_t R, const void* dy_perm, const void* x,
+                                                const uint8_t* x_scale, int64_t T, const int32_t* src_token,
+                                                const uint8_t* z_codes, const uint8_t* z_scales, const float* prob_perm,
+                                                const void* const* w_gate_up, const void* const* w_down,
+                                                const int32_t* offsets, void* dx_perm, void* const* dw_gate_up,
+                                                void* const* dw_down, float* dprob_perm, void* workspace,
+                                                size_t workspace_bytes, void* stream) {
+  const char* fn = "moe_grouped_mlp_bwd_ckpt8";
+  if (!desc) return fail(MOE_ERR_INVALID_ARG, std::string(fn) + ": desc is NULL");
+  const moe_mlp_desc d = *desc;
+  moe_status st = validate_ckpt8(d, true, fn);
+  if (st != MOE_OK) return st;
+  if (R < 0 || R > 0x7FFFFFFF) return fail(MOE_ERR_INVALID_ARG, std::string(fn) + ": R out of [0, 2^31)");
+  const bool kept8 = d.act == MOE_MXFP8;
+  if (!offsets || !aligned(offsets, 4)) return fail(MOE_ERR_INVALID_ARG, std::string(fn) + ": offsets NULL or misaligned");
+  if (R > 0) {
+    if (!dy_perm || !x || !z_codes || !z_scales || !prob_perm || !dx_perm || !dprob_perm || (kept8 && !x_scale))
+      return fail(MOE_ERR_INVALID_ARG, std::string(fn) + ": NULL pointer");
+    for (const void* p : {dy_perm, x, (const void*)z_codes, (const void*)dx_perm})
+      if (!aligned(p, 16)) return fail(MOE_ERR_INVALID_ARG, std::string(fn) + ": misaligned tensor");
+    if (!aligned(z_scales, 8) || !aligned(prob_perm, 4) || !aligned(dprob_perm, 4) || !aligned(src_token, 4))
+      return fail(MOE_ERR_INVALID_ARG, std::string(fn) + ": z_scales must be 8-byte, prob, dprob and src_token 4-byte aligned");
+    if (kept8 && (T < 0 || T > 0x7FFFFFFF || (!src_token && T != R)))
+      return fail(MOE_ERR_INVALID_ARG, std::string(fn) + ": T out of [0, 2^31), or T != R without src_token");
+    if (!kept8 && (x_scale || src_token))
+      return fail(MOE_ERR_INVALID_ARG, std::string(fn) + ": x_scale and src_token belong to act = MOE_MXFP8");
+  }
+  if ((st = check_table(w_gate_up, d.E, 16, "moe_grouped_mlp_bwd_ckpt8(w_gate_up)")) != MOE_OK) return st;
+  if ((st = check_table(w_down, d.E, 16, "moe_grouped_mlp_bwd_ckpt8(w_down)")) != MOE_OK) return st;
+  if ((st = check_table((const void* const*)dw_gate_up, d.E, 16, "moe_grouped_mlp_bwd_ckpt8(dw_gate_up)")) != MOE_OK) return st;
+  if ((st = check_table((const void* const*)dw_down, d.E, 16, "moe_grouped_mlp_bwd_ckpt8(dw_down)")) != MOE_OK) return st;
+  if (workspace_bytes < mlp_bwd_ckpt8_workspace_bytes(d, R))
+    return fail(MOE_ERR_WORKSPACE, std::string(fn) + ": workspace too small");
+  if (!workspace || !aligned(workspace, 256))
+    return fail(MOE_ERR_INVALID_ARG, std::string(fn) + ": workspace NULL or not 256-byte aligned");
+  const hipStream_t s = as_stream(stream);
+  const PtrTab w1 = make_tab(w_gate_up, d.E), w2 = make_tab(w_down, d.E);
+  const PtrTab dw1 = make_tab((const void* const*)dw_gate_up, d.E), dw2 = make_tab((const void* const*)dw_down, d.E);
+
+  uint8_t* ws = (uint8_t*)workspace;
+  bf16_t* dz = (bf16_t*)ws;
+  ws += a256((size_t)R * 2 * d.I * 2);
+  bf16_t* rows = (bf16_t*)ws;  // h until its weight gradient is done, then x in expert order
+  ws += ckpt8_rows_bytes(d, R);
+  float* part = (float*)ws;
+  ws += a256((size_t)2 * (d.I / 256) * R * 4);
+  const TailArea tail = tail_area(ws);
+  const int32_t* end = offsets + d.E;
+  if (R > 0) {
+    st = mx8::launch_read(z_codes, z_scales, R, 2 * (int64_t)d.I, nullptr, R, end, false, dz, s);
+    if (st != MOE_OK) return st;
+    const int64_t want = (R * (d.I / 8) + 255) / 256, most = (int64_t)num_cus() * 16;
+    hipLaunchKernelGGL(swiglu_rows_kernel, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, s, (const uint4*)dz,
+                       prob_perm, R, (uint32_t)(d.I / 8), end, (uint4*)rows);
+    if ((st = check_launch(fn)) != MOE_OK) return st;
+    st = bf16_down_dgrad(d, R, (const bf16_t*)dy_perm, w2, offsets, prob_perm, dz, dz, part, dprob_perm, end, s);
+    if (st != MOE_OK) return st;
+    if ((st = bf16_gate_up_dgrad(d, R, dz, w1, offsets, (bf16_t*)dx_perm, tail, s)) != MOE_OK) return st;
+  }
+  st = bf16_wgrad(d, R, (const bf16_t*)dy_perm, d.H, rows, d.I, dw2, offsets, s, "moe_grouped_mlp_bwd_ckpt8(down wgrad)");
+  if (st != MOE_OK) return st;
+  const bf16_t* xp = (const bf16_t*)x;
+  if (kept8) {
+    if (R > 0) {
+      st = mx8::launch_read((const uint8_t*)x, x_scale, T, d.H, src_token, R, end, true, rows, s);
+      if (st != MOE_OK) return st;
+    }
+    xp = rows;
+  }
+  return bf16_wgrad(d, R, dz, 2 * d.I, xp, d.H, dw1, offsets, s, "moe_grouped_mlp_bwd_ckpt8(gate_up wgrad)");
 }

@@ -1,0 +1,78 @@
+// Reading MXFP8 rows back: value = code * 2^(scale byte - 127), rounded once to bf16 (exact but
+// below bf16's smallest step and past its range), optionally gathered by row.
+//
+// HBM-bound: 33/32 bytes in, 2 bytes out an element. A thread takes 16 codes (half a block) in
+// one load and writes 32 bytes.
+#include "mxfp8.h"
+
+#include "common.h"
+#include "internal.h"
+
+namespace moe {
+namespace mx8 {
+
+__global__ __launch_bounds__(256) void read_kernel(const uint4* __restrict__ codes, const uint8_t* __restrict__ scales,
+                                                   int64_t src_rows, uint32_t row16, const int32_t* __restrict__ src_row,
+                                                   int64_t rows, const int32_t* __restrict__ limit,
+                                                   bool zero_missing, uint4* __restrict__ out) {
+  int64_t n = rows;
+  if (limit) n = *limit < 0 ? 0 : *limit < rows ? *limit : rows;
+  const int64_t total = n * row16;
+  for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < total; q += (int64_t)gridDim.x * 256) {
+    const int64_t r = total <= 0xFFFFFFFFll ? (int64_t)((uint32_t)q / row16) : q / row16;
+    const int64_t c = q - r * row16;
+    const int64_t from = src_row ? src_row[r] : r;
+    if (from < 0 || from >= src_rows) {
+      if (zero_missing) out[2 * q] = out[2 * q + 1] = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+    const int64_t at = from * row16 + c;
+    const uint4 w = codes[at];
+    const float sc = scale_value(scales[at >> 1]);  // two threads a block (row16 is even)
+    const uint32_t word[4] = {w.x, w.y, w.z, w.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float v[4];
+      unpack4(word[i], sc, v);
+      o[2 * i] = pack_bf16x2(v[0], v[1]);
+      o[2 * i + 1] = pack_bf16x2(v[2], v[3]);
+    }
+    out[2 * q] = make_uint4(o[0], o[1], o[2], o[3]);
+    out[2 * q + 1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+moe_status launch_read(const uint8_t* codes, const uint8_t* scales, int64_t src_rows, int64_t cols,
+                       const int32_t* src_row, int64_t rows, const int32_t* limit, bool zero_missing, bf16_t* out,
+                       hipStream_t s) {
+  const int64_t row16 = cols / 16;
+  if (rows == 0 || cols == 0) return MOE_OK;
+  int64_t grid = (rows * row16 + 255) / 256;
+  const int64_t most = (int64_t)num_cus() * 16;
+  if (grid > most) grid = most;
+  hipLaunchKernelGGL(read_kernel, dim3((unsigned)grid), dim3(256), 0, s, (const uint4*)codes, scales, src_rows,
+                     (uint32_t)row16, src_row, rows, limit, zero_missing, (uint4*)out);
+  return check_launch("mxfp8_dequantize");
+}
+
+}  // namespace mx8
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status mxfp8_dequantize(const uint8_t* e4m3, const uint8_t* e8m0, int64_t src_rows, int64_t cols,
+                                       const int32_t* src_row, int64_t rows, void* out_bf16, void* stream) {
+  if (src_rows < 0 || rows < 0 || cols < 0) return fail(MOE_ERR_INVALID_ARG, "mxfp8_dequantize: negative size");
+  if (cols % 32 != 0) return fail(MOE_ERR_INVALID_ARG, "mxfp8_dequantize: cols % 32 != 0");
+  if (!src_row && rows != src_rows)
+    return fail(MOE_ERR_INVALID_ARG, "mxfp8_dequantize: without src_row, rows and src_rows must be equal");
+  if (cols > 0x7FFFFFFF || rows > 0x7FFFFFFF || src_rows > 0x7FFFFFFF)
+    return fail(MOE_ERR_UNSUPPORTED, "mxfp8_dequantize: a size of 2^31 or more");
+  if (rows == 0 || cols == 0) return MOE_OK;
+  if (!out_bf16 || (src_rows > 0 && (!e4m3 || !e8m0)))
+    return fail(MOE_ERR_INVALID_ARG, "mxfp8_dequantize: NULL pointer");
+  if (!aligned(e4m3, 16) || !aligned(out_bf16, 16) || !aligned(src_row, 4))
+    return fail(MOE_ERR_INVALID_ARG, "mxfp8_dequantize: codes and out must be 16-byte, src_row 4-byte aligned");
+  return mx8::launch_read(e4m3, e8m0, src_rows, cols, src_row, rows, nullptr, false, (bf16_t*)out_bf16, as_stream(stream));
+}

@@ -1,0 +1,248 @@
+// The residual's addition, the RMS norm and MXFP8 rows of its result in one pass:
+//
+//   s[t] = residual[t] + sum_j x[row(t, j)]   (float32, rounded once to the stored dtype)
+//   r[t] = 1 / sqrt(mean_h s^2 + eps),  n = s r w
+//   per 32 columns: e the smallest with max|n| <= 448 2^e, codes E4M3(n 2^-e)
+//
+// HBM-bound: k + 1 rows in, the sum, the codes and (on request) n in the stored dtype out. A
+// team of TPR threads holds one row in registers, NV groups of 8 columns a thread, so four
+// neighbouring lanes hold a block; its maximum takes two lane moves.
+#include <type_traits>
+
+#include "common.h"
+#include "internal.h"
+#include "lanes.h"
+#include "mxfp8.h"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxH = 16384;
+constexpr int kMaxSlots = 16;
+constexpr int V = 8;  // columns a thread holds side by side
+
+struct Params {
+  const void* x;        // [T, H], or [T * k, H] reached through rows
+  const int32_t* rows;  // [T * k] or NULL
+  const void* residual; // NULL or [T, H]
+  const void* w;        // [H]
+  void* sum;            // NULL or [T, H]
+  void* y;              // NULL or [T, H]
+  float* rstd;          // NULL or [T]
+  uint2* codes;         // [T, H] bytes
+  uint8_t* scales;      // [T, H / 32]
+  int64_t T;
+  int H, k;
+  float eps;
+};
+
+template <bool BF16>
+struct Raw {  // 8 columns as they are stored
+  uint4 v[BF16 ? 1 : 2];
+};
+
+template <bool BF16>
+__device__ __forceinline__ Raw<BF16> load8(const void* p, int64_t group) {
+  Raw<BF16> r;
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 1 : 2); ++i) r.v[i] = ((const uint4*)p)[group * (BF16 ? 1 : 2) + i];
+  return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store8(void* p, int64_t group, const Raw<BF16>& r) {
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 1 : 2); ++i) ((uint4*)p)[group * (BF16 ? 1 : 2) + i] = r.v[i];
+}
+
+template <bool BF16>
+__device__ __forceinline__ void unpack8(const Raw<BF16>& r, float* f) {
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 1 : 2); ++i) {
+    const uint32_t w[4] = {r.v[i].x, r.v[i].y, r.v[i].z, r.v[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (BF16) {
+        f[2 * j] = __uint_as_float(w[j] << 16);
+        f[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+      } else {
+        f[4 * i + j] = __uint_as_float(w[j]);
+      }
+    }
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ Raw<BF16> pack8(const float* f) {
+  Raw<BF16> r;
+  if constexpr (BF16) {
+    r.v[0] = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      r.v[i] = make_uint4(__float_as_uint(f[4 * i]), __float_as_uint(f[4 * i + 1]), __float_as_uint(f[4 * i + 2]),
+                          __float_as_uint(f[4 * i + 3]));
+  }
+  return r;
+}
+
+template <bool BF16, int TPR, int NV>
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_norm_kernel(const Params p) {
+  constexpr int kTeams = TPR < 256 ? 256 / TPR : 1;
+  __shared__ float red[2][TPR > 64 ? TPR / 64 : 1];  // alternating: a thread is at most one row ahead
+  const int tr = threadIdx.x % TPR;
+  const int groups = p.H / V;
+  const float inv_h = 1.f / (float)p.H;  // applied to each term: a sum of squares would overflow H times earlier
+  Raw<BF16> w[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    w[i] = Raw<BF16>{};
+    if (i * TPR + tr < groups) w[i] = load8<BF16>(p.w, i * TPR + tr);
+  }
+  const int64_t R = p.T * p.k;
+  int par = 0;
+  // every thread of a workgroup runs the same rows' loop where the workgroup is one team
+  for (int64_t t = (int64_t)blockIdx.x * kTeams + threadIdx.x / TPR; t < p.T; t += (int64_t)gridDim.x * kTeams) {
+    float acc[NV][V];
+    Raw<BF16> res[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      res[i] = Raw<BF16>{};
+      if (p.residual && i * TPR + tr < groups) res[i] = load8<BF16>(p.residual, t * groups + i * TPR + tr);
+    }
+    constexpr int kSlots = NV <= 2 ? 4 : 2;  // rows whose loads are in flight together
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[i][v] = 0.f;
+    for (int j0 = 0; j0 < p.k; j0 += kSlots) {
+      Raw<BF16> q[kSlots][NV];
+#pragma unroll
+      for (int u = 0; u < kSlots; ++u) {
+        int64_t row = -1;
+        if (j0 + u < p.k) row = p.rows ? (int64_t)p.rows[t * p.k + j0 + u] : t;
+        const bool ok = row >= 0 && row < R;  // a dropped slot adds nothing
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          q[u][i] = Raw<BF16>{};
+          if (ok && i * TPR + tr < groups) q[u][i] = load8<BF16>(p.x, row * groups + i * TPR + tr);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < kSlots; ++u)
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          float f[V];
+          unpack8<BF16>(q[u][i], f);
+#pragma unroll
+          for (int v = 0; v < V; ++v) acc[i][v] += f[v];
+        }
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float f[V];
+      unpack8<BF16>(res[i], f);
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[i][v] = f[v] + acc[i][v];
+      const Raw<BF16> o = pack8<BF16>(acc[i]);
+      if (p.sum && i * TPR + tr < groups) store8<BF16>(p.sum, t * groups + i * TPR + tr, o);
+      unpack8<BF16>(o, acc[i]);  // the norm reads the sum as it is stored
+#pragma unroll
+      for (int v = 0; v < V; ++v) ss += acc[i][v] * inv_h * acc[i][v];
+    }
+    ss = lanes_sum<64>(ss);
+    if constexpr (TPR > 64) {
+      if ((threadIdx.x & 63) == 0) red[par][threadIdx.x >> 6] = ss;
+      __syncthreads();
+      ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < TPR / 64; ++i) ss += red[par][i];
+      par ^= 1;
+    }
+    const float r = 1.f / sqrtf(ss + p.eps);
+    if (p.rstd && tr == 0) p.rstd[t] = r;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int64_t at = t * groups + i * TPR + tr;
+      const bool in = i * TPR + tr < groups;  // groups % 4 == 0: the four lanes of a block agree
+      float f[V];
+      unpack8<BF16>(w[i], f);
+      uint32_t top = 0;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        acc[i][v] = acc[i][v] * r * f[v];
+        const uint32_t m = __float_as_uint(acc[i][v]) & 0x7FFFFFFFu;
+        top = m > top ? m : top;
+      }
+      if (p.y && in) store8<BF16>(p.y, at, pack8<BF16>(acc[i]));
+      const int b = mx8::scale_byte(lanes_umax<4>(top));
+      const float inv = mx8::inverse_scale(b);
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[i][v] *= inv;
+      if (in) {
+        // a block that holds an infinity or a NaN: every code 0, its scale says NaN
+        p.codes[at] = b == 255 ? make_uint2(0, 0)
+                               : make_uint2(e4m3_pack4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]),
+                                            e4m3_pack4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]));
+        if ((threadIdx.x & 3) == 0) p.scales[at >> 2] = (uint8_t)b;
+      }
+    }
+  }
+}
+
+template <int N>
+using Int = std::integral_constant<int, N>;
+
+template <bool BF16>
+void launch(const Params& p, hipStream_t s) {
+  auto go = [&](auto Tc, auto Nc) {
+    constexpr int TPR = decltype(Tc)::value;
+    constexpr int teams = TPR < 256 ? 256 / TPR : 1;
+    int64_t grid = (p.T + teams - 1) / teams;
+    const int64_t most = (int64_t)num_cus() * 8;
+    if (grid > most) grid = most;
+    hipLaunchKernelGGL((add_norm_kernel<BF16, TPR, decltype(Nc)::value>), dim3((unsigned)grid), dim3(TPR < 256 ? 256 : TPR),
+                       0, s, p);
+  };
+  const int u = p.H / V;  // groups of a row
+  if (u <= 64) go(Int<64>{}, Int<1>{});
+  else if (u <= 128) go(Int<64>{}, Int<2>{});
+  else if (u <= 256) go(Int<256>{}, Int<1>{});
+  else if (u <= 512) go(Int<256>{}, Int<2>{});
+  else if (u <= 1024) go(Int<256>{}, Int<4>{});
+  else go(Int<1024>{}, Int<2>{});
+}
+
+}  // namespace
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" moe_status moe_add_norm_mxfp8(const void* x, const int32_t* row_id_map, int k, const void* residual,
+                                         const void* weight, moe_dtype dt, int64_t T, int H, float eps, void* sum,
+                                         void* y, float* rstd, uint8_t* codes, uint8_t* scales, void* stream) {
+  if (dt != MOE_F32 && dt != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "moe_add_norm_mxfp8: dtype must be F32 or BF16");
+  if (T < 0 || H < 1) return fail(MOE_ERR_INVALID_ARG, "moe_add_norm_mxfp8: T < 0 or H < 1");
+  if (H > kMaxH || H % 32 != 0)
+    return fail(MOE_ERR_UNSUPPORTED, "moe_add_norm_mxfp8: needs H % 32 == 0 and H <= 16384");
+  if (k < 1) return fail(MOE_ERR_INVALID_ARG, "moe_add_norm_mxfp8: k < 1");
+  if (k > kMaxSlots) return fail(MOE_ERR_UNSUPPORTED, "moe_add_norm_mxfp8: k > 16");
+  if (!row_id_map && k != 1) return fail(MOE_ERR_INVALID_ARG, "moe_add_norm_mxfp8: k > 1 needs row_id_map");
+  if (T > 0x7FFFFFFF / k) return fail(MOE_ERR_UNSUPPORTED, "moe_add_norm_mxfp8: T * k exceeds int32 rows");
+  if (!(eps > 0.f)) return fail(MOE_ERR_INVALID_ARG, "moe_add_norm_mxfp8: eps must be positive");
+  if (T == 0) return MOE_OK;
+  if (!x || !weight || !codes || !scales) return fail(MOE_ERR_INVALID_ARG, "moe_add_norm_mxfp8: NULL pointer");
+  for (const void* p : {x, residual, weight, (const void*)sum, (const void*)y})
+    if (!aligned(p, 16)) return fail(MOE_ERR_INVALID_ARG, "moe_add_norm_mxfp8: tensors must be 16-byte aligned");
+  if (!aligned(codes, 8) || !aligned(row_id_map, 4) || !aligned(rstd, 4))
+    return fail(MOE_ERR_INVALID_ARG, "moe_add_norm_mxfp8: codes must be 8-byte, row_id_map and rstd 4-byte aligned");
+  if (sum && sum == x && row_id_map)
+    return fail(MOE_ERR_INVALID_ARG, "moe_add_norm_mxfp8: sum may be x only without row_id_map");
+  Params p{};
+  p.x = x, p.rows = row_id_map, p.residual = residual, p.w = weight, p.sum = sum, p.y = y, p.rstd = rstd;
+  p.codes = (uint2*)codes, p.scales = scales, p.T = T, p.H = H, p.k = k, p.eps = eps;
+  if (dt == MOE_BF16) launch<true>(p, as_stream(stream));
+  else launch<false>(p, as_stream(stream));
+  return check_launch("moe_add_norm_mxfp8");
+}

@@ -308,6 +308,32 @@ moe_status moe_post_norm_bwd(const void* dout, const void* c, const float* rstd,
                              void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * The residual's addition, the RMS norm of the sum and MXFP8 rows of the result in one pass:
+ * the norm before a block whose rows are held in 8 bits (moe_permute and moe_grouped_mlp_fwd
+ * with MOE_MXFP8 read the codes, moe_grouped_mlp_bwd_ckpt8 keeps them for the backward).
+ *   s[t]   = residual[t] + x[t], or, with row_id_map, residual[t] + sum_j x[row_id_map[t*k + j]]
+ *            (slot order, float32; entries out of [0, T*k) skipped: the combine of
+ *            moe_unpermute_combine without weights); rounded once to dt
+ *   r[t]   = 1 / sqrt(mean_h s[t, h]^2 + eps),   n[t, h] = s[t, h] r[t] weight[h]
+ *   codes  = MXFP8 of n along the row: per 32 columns one scale 2^e, e the smallest with
+ *            max|n| <= 448 * 2^e, and the E4M3 code of n / 2^e (the rule of mxfp8_quantize on
+ *            the float32 values, which are not rounded to bf16 first). A block that holds an
+ *            infinity or a NaN gets scale byte 255 (E8M0's NaN) and codes 0.
+ *   x [T, H] (row_id_map NULL and k = 1) or [T*k, H], residual [T, H] or NULL for 0, weight [H],
+ *   sum [T, H] (out, may be NULL), y [T, H] (out, may be NULL): n rounded to dt; all dtype dt (F32
+ *   or BF16); rstd [T] float32 (out, may be NULL); codes [T, H], scales [T, H/32] (out)
+ * sum may equal residual, or x without row_id_map; no other tensors may overlap.
+ * Backward: moe_pre_norm_bwd on sum and rstd, its dx_in the gradient that reaches sum past the
+ * norm. Its dx is the gradient of the residual and of every row of x that entered the sum
+ * (moe_permute with reuse_map lays it out by rows); the rounding to 8 bits passes it unchanged.
+ * Limits: H % 32 == 0, H <= 16384, 1 <= k <= 16, T * k < 2^31, eps > 0; tensors 16-byte, codes
+ * 8-byte aligned.
+ */
+moe_status moe_add_norm_mxfp8(const void* x, const int32_t* row_id_map, int k, const void* residual,
+                              const void* weight, moe_dtype dt, int64_t T, int H, float eps, void* sum, void* y,
+                              float* rstd, uint8_t* codes, uint8_t* scales, void* stream);
+
+/*
  * MXFP8 block quantisation of a bf16 matrix along its rows. Source: Challenge 2
  * (one scaling factor per block of 32 consecutive values, 8-bit values) and
  * Challenge 3 (bf16 -> MXFP8 before the low-precision GEMM).
@@ -320,6 +346,18 @@ moe_status moe_post_norm_bwd(const void* dout, const void* c, const float* rstd,
  */
 moe_status mxfp8_quantize(const void* in_bf16, int64_t rows, int64_t cols, uint8_t* e4m3,
                           uint8_t* e8m0, void* stream);
+
+/*
+ * The values of MXFP8 rows, code * 2^s, in bf16 (exact but for magnitudes below bf16's smallest
+ * step, rounded, and past its range, which become infinities; NaN for scale byte 255).
+ *   e4m3 [src_rows, cols] (16-byte aligned, cols % 32 == 0), e8m0 [src_rows, cols/32]
+ *   src_row [rows] int32 (device) or NULL: out[r] = values of row src_row[r] (moe_permute's
+ *     src_token brings kept token rows into expert order); a row whose index is out of
+ *     [0, src_rows) is left as it was. NULL: out[r] = values of row r, rows == src_rows.
+ *   out [rows, cols] bf16 (16-byte aligned)
+ */
+moe_status mxfp8_dequantize(const uint8_t* e4m3, const uint8_t* e8m0, int64_t src_rows, int64_t cols,
+                            const int32_t* src_row, int64_t rows, void* out_bf16, void* stream);
 
 /*
  * Column-wise MXFP8 quantisation, expert by expert, along the token axis: the operand
@@ -569,6 +607,51 @@ moe_status moe_grouped_mlp_bwd(const moe_mlp_desc* desc, int64_t R, const void* 
                                void* stream);
 
 /*
+ * moe_grouped_mlp_fwd in bf16 that keeps what the backward needs in 8 bits: the gate_up output
+ * z [R, 2I] as MXFP8, made from its float32 sums in the GEMM's epilogue, and nothing of h, which
+ * moe_grouped_mlp_bwd_ckpt8 computes again. A routed row's checkpoint is 2I (1 + 1/32) bytes
+ * where z_save and h_save take 6I. y_perm is the bf16 forward's, bit for bit.
+ *   desc: compute, act and wt MOE_BF16 (save_for_bwd is ignored)
+ *   z_codes [R, 2I] (out, 16-byte aligned), z_scales [R, 2I/32] (out, 4-byte aligned): per 32
+ *     columns of a row one scale and the E4M3 codes by the rule of mxfp8_quantize; a block that
+ *     holds an infinity or a NaN gets scale byte 255 (E8M0's NaN) and codes 0. Rows from
+ *     offsets[E] on are not written.
+ * The other arguments are moe_grouped_mlp_fwd's.
+ * workspace: moe_workspace_size(MOE_OP_MLP_FWD, desc with save_for_bwd = 0, R) bytes, 256-byte
+ * aligned. Shapes: H % 256 == 0, I % 256 == 0.
+ */
+moe_status moe_grouped_mlp_fwd_ckpt8(const moe_mlp_desc* desc, int64_t R, const void* x_perm,
+                                     const void* const* w_gate_up, const void* const* w_down, const int32_t* offsets,
+                                     const float* prob_perm, void* y_perm, uint8_t* z_codes, uint8_t* z_scales,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * moe_grouped_mlp_bwd in bf16 from what was kept in 8 bits. With z = the values of z_codes, G, U
+ * its halves, p = prob_perm and x the values of the kept rows:
+ *   h = silu(G) U p                                   (rounded to bf16 for its product)
+ *   dW2_e = dY^T h,  dH = dY W2_e,  dprob[r] = sum_i dH silu(G) U      (float32)
+ *   dG = dH p U sig(G) (1 + G (1 - sig(G))),  dU = dH p silu(G)        (rounded to bf16)
+ *   dx_perm = [dG, dU] W1_e,  dW1_e = [dG, dU]^T x
+ *   desc: compute and wt MOE_BF16; act = MOE_MXFP8: x holds E4M3 codes [T, H] (16-byte aligned)
+ *     with x_scale [T, H/32], one row a token, and src_token [R] (moe_permute's) names the row of
+ *     each routed row, or src_token is NULL and T == R: the codes are in expert order. A token out
+ *     of [0, T) is read as zeros. act = MOE_BF16: x is x_perm [R, H] (x_scale and src_token NULL, T
+ *     ignored).
+ *   z_codes [R, 2I] (16-byte aligned), z_scales [R, 2I/32] (8-byte aligned): of
+ *     moe_grouped_mlp_fwd_ckpt8
+ * The other arguments are moe_grouped_mlp_bwd's. Rows from offsets[E] on of dx_perm and
+ * dprob_perm are not written; experts without rows get all-zero weight gradients.
+ * workspace: moe_workspace_size(MOE_OP_MLP_BWD_CKPT8, desc, R) bytes, 256-byte aligned: dZ and h
+ * (or x, whichever is wider) in bf16. Calls sharing a workspace must not overlap.
+ */
+moe_status moe_grouped_mlp_bwd_ckpt8(const moe_mlp_desc* desc, int64_t R, const void* dy_perm, const void* x,
+                                     const uint8_t* x_scale, int64_t T, const int32_t* src_token,
+                                     const uint8_t* z_codes, const uint8_t* z_scales, const float* prob_perm,
+                                     const void* const* w_gate_up, const void* const* w_down, const int32_t* offsets,
+                                     void* dx_perm, void* const* dw_gate_up, void* const* dw_down, float* dprob_perm,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * GroupedLinear: one grouped GEMM submission over all local experts. Source:
  * "Efficient MoE Training for Biological Foundation Models", Challenge 1 (GroupedLinear
  * applies each expert's linear map to that expert's rows in one call, with per-expert
@@ -633,7 +716,8 @@ typedef enum {
   MOE_OP_BALANCE_LOSS = 5, /* T and E used, R = seq_len; desc may be NULL */
   MOE_OP_NORM_BWD = 6,     /* moe_pre_norm_bwd / moe_post_norm_bwd: desc (H) and T used, E = gate kind,
                               k = gate_group (at most T; only with MOE_GATE_CHANNEL) */
-  MOE_OP_LINEAR_MXFP4 = 7  /* moe_grouped_linear_mxfp4: desc (E, H = K, I = N, act) and R used */
+  MOE_OP_LINEAR_MXFP4 = 7, /* moe_grouped_linear_mxfp4: desc (E, H = K, I = N, act) and R used */
+  MOE_OP_MLP_BWD_CKPT8 = 8 /* moe_grouped_mlp_bwd_ckpt8: desc and R used */
 } moe_op;
 
 /* Workspace bytes an operation needs (0 is possible). bytes is a [host] pointer. */

@@ -15,3 +15,4 @@ from .router import *  # noqa: F401,F403
 from .fp8_tensor import *  # noqa: F401,F403
 from .block import *  # noqa: F401,F403
 from .mxfp4 import *  # noqa: F401,F403
+from .act8 import *  # noqa: F401,F403
