@@ -20,7 +20,8 @@ enum {
   EPI_STORE = 0,
   EPI_SWIGLU = 1,
   EPI_DSWIGLU = 2,
-  EPI_SWIGLU_MX8 = 3  // SWIGLU that also writes the gate_up output in MXFP8
+  EPI_SWIGLU_MX8 = 3,  // SWIGLU that also writes the gate_up output in MXFP8
+  EPI_DSWIGLU_MX8 = 4  // DSWIGLU from a gate_up output in MXFP8, which also writes h
 };
 constexpr bool is_swiglu(int ep) { return ep == EPI_SWIGLU || ep == EPI_SWIGLU_MX8; }
 
@@ -31,10 +32,10 @@ struct Params {
   const bf16_t* q;        // Q operand (token rows)
   bf16_t* c;              // output (GROUP_M)
   const int32_t* offsets; // [E+1] expert row offsets
-  const float* prob;      // SWIGLU / DSWIGLU: routing weight per row
+  const float* prob;      // SWIGLU / DSWIGLU (and their MX8 forms): routing weight per row
   const bf16_t* zin;      // DSWIGLU: saved gate_up output [R, 2I]
   bf16_t* zout;           // SWIGLU: gate_up output to save [R, 2I] (or NULL)
-  float* part;            // DSWIGLU: dprob partial sums [2 * n_tiles][R]
+  float* part;            // DSWIGLU, DSWIGLU_MX8: dprob partial sums [2 * n_tiles][R]
   int64_t p_ld, q_ld, c_ld;
   int64_t R;
   int M, N, K;            // GROUP_M uses N, K; GROUP_K uses M, N
@@ -48,8 +49,9 @@ struct Params {
   float* tail;
   int32_t* tail_meta;
   int tail_cap;
-  uint8_t* z8;   // SWIGLU_MX8: E4M3 codes of the gate_up output [R, 2I] (out)
-  uint8_t* z8s;  // ... and its E8M0 scales [R, 2I / 32] (out)
+  uint8_t* z8;   // E4M3 codes of the gate_up output [R, 2I] (SWIGLU_MX8: out, DSWIGLU_MX8: in)
+  uint8_t* z8s;  // ... and its E8M0 scales [R, 2I / 32]
+  bf16_t* hout;  // DSWIGLU_MX8: h [R, I]
 };
 
 constexpr size_t kTailTileBytes = (size_t)kBM * kBN * 4;  // one float32 partial tile

@@ -42,6 +42,7 @@
 #include "gemm_bf16.h"
 #include "gemm_common.h"
 #include "internal.h"
+#include "mxfp8.h"
 
 namespace moe {
 namespace gemm {
@@ -616,6 +617,153 @@ void grouped_gemm_kernel(const Params prm) {
       }
       continue;
     }
+    if constexpr (EP == EPI_DSWIGLU_MX8) {
+      // dSwiGLU from z in MXFP8, with h computed again: three bf16 tiles (dG, dU, h) leave where
+      // one byte an element and half came in, so z's codes go straight to registers and LDS
+      // carries the results. Eight passes: pass j takes the accumulator rows of sub-tile sm =
+      // j >> 1 of every wavefront and the tile's columns 128 (j & 1) .. + 127, that is two
+      // sub-tiles of 32 columns, each one MX block of a row in G and in U. A lane reads 16 of a
+      // block's 32 codes (32 rows x 32 bytes an instruction), two half swaps against lane ^ 32
+      // give it the four words of the columns that it holds, and the next pass's codes are on
+      // their way meanwhile. Passes alternate between two LDS buffers of three 16 KiB arrays
+      // (64 rows of 256 bytes, chunk c of row r at c ^ (r & 15)), so one barrier a pass stands
+      // between writing a buffer and its whole-row stores, and the next but one writes it again.
+      // Rows past the expert read as zeros and are not stored (the descriptors' record counts).
+      int ln = lane_number(), wv = wave_u;
+      asm volatile("" : "+v"(ln));
+      asm volatile("" : "+s"(wv));
+      const int em = wv >> 1, en = wv & 1, e32 = ln & 31, ehi = ln >> 5;
+      const int tile_row = row_beg + mt * kBM;
+      const int valid_rows = min(row_end - tile_row, kBM);
+      const int64_t I = prm.I;
+      const uint32_t zrow = (uint32_t)(2 * I), srow = (uint32_t)(2 * I / 32), hrow = (uint32_t)(2 * I);  // row bytes
+      auto rsrc = [&](const void* tile, int64_t row_bytes, int64_t col_bytes) {  // from a column to the last row's end
+        return __builtin_amdgcn_make_buffer_rsrc((void*)((const char*)tile + col_bytes), (short)0,
+                                                 (int)(uint32_t)(valid_rows * row_bytes - col_bytes), kBufferFlags);
+      };
+      const uint8_t* zt = prm.z8 + (int64_t)tile_row * zrow;
+      const uint8_t* st = prm.z8s + (int64_t)tile_row * srow;
+      const __amdgpu_buffer_rsrc_t rg = rsrc(zt, zrow, (int64_t)nt * kBN), ru = rsrc(zt, zrow, I + (int64_t)nt * kBN);
+      const __amdgpu_buffer_rsrc_t sg_r = rsrc(st, srow, nt * 8), su_r = rsrc(st, srow, I / 32 + nt * 8);
+      // a row's 8 scale bytes of this tile's gate columns and of its up columns
+      typedef unsigned int v2u32 __attribute__((ext_vector_type(2)));
+      float pr[4], dpart[4];
+      v2u32 gs[4], us[4];
+#pragma unroll
+      for (int sm = 0; sm < 4; ++sm) {
+        const int row = em * 128 + sm * 32 + e32;
+        const int64_t mg = (int64_t)tile_row + row;
+        pr[sm] = prm.prob[mg < row_end ? mg : row_end - 1];  // rows past the expert: not stored
+        gs[sm] = __builtin_amdgcn_raw_buffer_load_b64(sg_r, (uint32_t)row * srow, 0, 0);
+        us[sm] = __builtin_amdgcn_raw_buffer_load_b64(su_r, (uint32_t)row * srow, 0, 0);
+        dpart[sm] = 0.f;
+      }
+      const uint32_t zlane = (uint32_t)(em * 128 + e32) * zrow + (uint32_t)(en * 64 + ehi * 16);
+      auto fetch = [&](auto J, v4u32 (&g)[2], v4u32 (&u)[2]) {
+        constexpr int sm = decltype(J)::value >> 1, b = decltype(J)::value & 1;
+#pragma unroll
+        for (int sq = 0; sq < 2; ++sq) {
+          g[sq] = __builtin_amdgcn_raw_buffer_load_b128(rg, zlane + b * 128 + sq * 32, (int)(sm * 32 * zrow), 0);
+          u[sq] = __builtin_amdgcn_raw_buffer_load_b128(ru, zlane + b * 128 + sq * 32, (int)(sm * 32 * zrow), 0);
+        }
+      };
+      // words 0..3 of 16 codes -> the words of columns i4 * 8 + ehi * 4, i4 = 0..3
+      auto own_words = [&](const v4u32& v, uint32_t (&w)[4]) {
+        const auto a = __builtin_amdgcn_permlane32_swap(v[0], v[1], false, false);
+        const auto c = __builtin_amdgcn_permlane32_swap(v[2], v[3], false, false);
+        w[0] = a[0];
+        w[2] = a[1];
+        w[1] = c[0];
+        w[3] = c[1];
+      };
+      auto buf = [&](auto B, int k) -> uint8_t* {  // 0: dG, 1: dU, 2: h
+        if constexpr (B.value == 0) return k == 0 ? sP0 : k == 1 ? sP1 : sP2;
+        else return k == 0 ? sQ0 : k == 1 ? sQ1 : sQ2;
+      };
+      auto compute = [&](auto J, const v4u32 (&gv)[2], const v4u32 (&uv)[2]) {
+        constexpr int sm = decltype(J)::value >> 1, b = decltype(J)::value & 1;
+        using B = std::integral_constant<int, b>;
+        const int rr = em * 32 + e32;  // row within the arrays
+#pragma unroll
+        for (int sq = 0; sq < 2; ++sq) {
+          const int sn = 2 * b + sq;
+          // this wavefront's block of the tile row: byte b * 4 + en * 2 + sq
+          const int shift = (en * 2 + sq) * 8;
+          const float gsc = mx8::scale_value((gs[sm][b] >> shift) & 255), usc = mx8::scale_value((us[sm][b] >> shift) & 255);
+          uint32_t gw[4], uw[4];
+          own_words(gv[sq], gw);
+          own_words(uv[sq], uw);
+#pragma unroll
+          for (int i4 = 0; i4 < 4; ++i4) {
+            float g[4], u[4], dg[4], du[4], h[4];
+            mx8::unpack4(gw[i4], gsc, g);
+            mx8::unpack4(uw[i4], usc, u);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {  // as in DSWIGLU above; h = p u sl
+              const float dh = acc[sn][sm][i4 * 4 + v];
+              const float sg = sigmoid_f(g[v]);
+              const float sl = g[v] * sg;
+              const float q = dh * u[v];
+              dpart[sm] = __builtin_fmaf(q, sl, dpart[sm]);
+              dg[v] = (pr[sm] * q) * __builtin_fmaf(-sl, sg, sg + sl);
+              du[v] = (pr[sm] * dh) * sl;
+              h[v] = sl * u[v] * pr[sm];
+            }
+            const uint32_t off = (uint32_t)(rr * 256 + (((en * 8 + sq * 4 + i4) ^ (rr & 15)) << 4) + ehi * 8);
+            *reinterpret_cast<uint2*>(buf(B{}, 0) + off) = make_uint2(pack_bf16x2(dg[0], dg[1]), pack_bf16x2(dg[2], dg[3]));
+            *reinterpret_cast<uint2*>(buf(B{}, 1) + off) = make_uint2(pack_bf16x2(du[0], du[1]), pack_bf16x2(du[2], du[3]));
+            *reinterpret_cast<uint2*>(buf(B{}, 2) + off) = make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
+          }
+        }
+        asm volatile("" : "+v"(dpart[sm]));  // the row's sum is formed here, not after the stores
+      };
+      const char* dzt = reinterpret_cast<const char*>(prm.c + (int64_t)tile_row * 2 * I);
+      const char* ht = reinterpret_cast<const char*>(prm.hout + (int64_t)tile_row * I);
+      // 64 rows of three arrays: wavefront w stores array rows 16 w + 4 i .. + 3 (i = 0..3), lane l
+      // row + (l >> 4) and chunk l & 15; array row rho is tile row 128 (rho >> 5) + 32 sm + (rho & 31)
+      auto store_out = [&](auto J) {
+        constexpr int sm = decltype(J)::value >> 1, b = decltype(J)::value & 1;
+        using B = std::integral_constant<int, b>;
+        const int lrow = ln >> 4, pch = ln & 15;
+        const int64_t colb = ((int64_t)nt * kBN + b * 128) * 2;
+        const __amdgpu_buffer_rsrc_t rs[3] = {rsrc(dzt, 4 * I, colb), rsrc(dzt, 4 * I, colb + 2 * I), rsrc(ht, 2 * I, colb)};
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const uint32_t rowb = k < 2 ? 2 * zrow : hrow;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int rho = 16 * wv + 4 * i;
+            const uint8_t* src = buf(B{}, k) + (rho + lrow) * 256 + ((pch ^ ((4 * i + lrow) & 15)) << 4);
+            const v4u32 v = *reinterpret_cast<const v4u32*>(src);
+            const uint32_t row = (uint32_t)(128 * (rho >> 5) + 32 * sm + (rho & 31));
+            __builtin_amdgcn_raw_buffer_store_b128(v, rs[k], (uint32_t)lrow * rowb + pch * 16, (int)(row * rowb), 0);
+          }
+        }
+      };
+      v4u32 g0[2], u0[2], g1[2], u1[2];
+      fetch(std::integral_constant<int, 0>{}, g0, u0);
+      static_for<4>([&](auto H) {
+        using J0 = std::integral_constant<int, 2 * decltype(H)::value>;
+        using J1 = std::integral_constant<int, 2 * decltype(H)::value + 1>;
+        fetch(J1{}, g1, u1);
+        compute(J0{}, g0, u0);
+        lds_barrier();
+        store_out(J0{});
+        if constexpr (decltype(H)::value < 3) fetch(std::integral_constant<int, J1::value + 1>{}, g0, u0);
+        compute(J1{}, g1, u1);
+        lds_barrier();
+        store_out(J1{});
+      });
+      lds_barrier();  // read out before the next tile's copies land
+#pragma unroll
+      for (int sm = 0; sm < 4; ++sm) {
+        float pt = dpart[sm];
+        pt += __shfl_xor(pt, 32);
+        const int64_t mg = (int64_t)tile_row + em * 128 + sm * 32 + e32;
+        if (mg < row_end && ehi == 0) prm.part[(int64_t)(nt * 2 + en) * prm.R + mg] = pt;
+      }
+      continue;
+    }
     if constexpr (TAIL) {  // K chunk of a tail tile: the float32 partial, all 256 rows, row-major
       float* part_tile = prm.tail + (int64_t)unit * (kBM * kBN);
 #pragma unroll
@@ -775,6 +923,8 @@ moe_status run(const Params& p, int pl, int ql, int g, int ep, int64_t max_tiles
     return launch<KCONTIG, KCONTIG, GROUP_M, EPI_STORE>(p, max_tiles, s, what);
   if (pl == MNCONTIG && ql == KCONTIG && g == GROUP_M && ep == EPI_DSWIGLU)
     return launch<MNCONTIG, KCONTIG, GROUP_M, EPI_DSWIGLU>(p, max_tiles, s, what);
+  if (pl == MNCONTIG && ql == KCONTIG && g == GROUP_M && ep == EPI_DSWIGLU_MX8)
+    return launch<MNCONTIG, KCONTIG, GROUP_M, EPI_DSWIGLU_MX8>(p, max_tiles, s, what);
   if (pl == MNCONTIG && ql == KCONTIG && g == GROUP_M && ep == EPI_STORE)
     return launch<MNCONTIG, KCONTIG, GROUP_M, EPI_STORE>(p, max_tiles, s, what);
   if (pl == MNCONTIG && ql == MNCONTIG && g == GROUP_K && ep == EPI_STORE)

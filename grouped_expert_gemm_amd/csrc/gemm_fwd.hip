@@ -450,23 +450,17 @@ void grouped_gemm_fwd_kernel(const Params prm) {
           for (int sn = 0; sn < 4; ++sn)
 #pragma unroll
             for (int sm = 0; sm < 4; ++sm) {
-              uint32_t top = 0;
+              float top = 0.f;
 #pragma unroll
-              for (int x = 0; x < 16; ++x) {
-                const uint32_t m = __float_as_uint(acc[sn][sm][x]) & 0x7FFFFFFFu;
-                top = m > top ? m : top;
-              }
-              const auto both = __builtin_amdgcn_permlane32_swap(top, top, false, false);
-              top = both[0] > both[1] ? both[0] : both[1];
-              const int b = mx8::scale_byte(top);
-              const float inv = mx8::inverse_scale(b);
+              for (int x = 0; x < 16; ++x) top = mx8::max_magnitude(top, acc[sn][sm][x]);
+              const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+              const int b = mx8::scale_byte(mx8::max_magnitude(__uint_as_float(both[0]), __uint_as_float(both[1])));
+              const float sc = mx8::scale_value(b);
               uint32_t w[4];
 #pragma unroll
-              for (int i4 = 0; i4 < 4; ++i4) {
-                w[i4] = e4m3_pack4(acc[sn][sm][i4 * 4 + 0] * inv, acc[sn][sm][i4 * 4 + 1] * inv,
-                                   acc[sn][sm][i4 * 4 + 2] * inv, acc[sn][sm][i4 * 4 + 3] * inv);
-                w[i4] = b == 255 ? 0 : w[i4];
-              }
+              for (int i4 = 0; i4 < 4; ++i4)
+                w[i4] = mx8::pack4(acc[sn][sm][i4 * 4 + 0], acc[sn][sm][i4 * 4 + 1], acc[sn][sm][i4 * 4 + 2],
+                                   acc[sn][sm][i4 * 4 + 3], sc, b);
               const auto s02 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
               const auto s13 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
               const int row = em * 128 + sm * 32 + e32;
@@ -561,18 +555,13 @@ __global__ __launch_bounds__(256) void tail_reduce_kernel(const Params prm) {
                    pack_bf16x2(silu_f(g.z) * u.z * p, silu_f(g.w) * u.w * p));
     if constexpr (EP == EPI_SWIGLU_MX8) {  // 8 neighbouring threads hold a block of 32 columns
       auto put = [&](const float4& v, int64_t at) {
-        const float f[4] = {v.x, v.y, v.z, v.w};
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t m = __float_as_uint(f[i]) & 0x7FFFFFFFu;
-          top = m > top ? m : top;
-        }
-        const int b = mx8::scale_byte(lanes_umax<8>(top));
-        const float inv = mx8::inverse_scale(b);
-        const uint32_t w = e4m3_pack4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+        float top = mx8::max_magnitude(mx8::max_magnitude(v.x, v.y), mx8::max_magnitude(v.z, v.w));
+        top = __uint_as_float(lanes_reduce<8>(__float_as_uint(top), [](uint32_t x, uint32_t y) {
+          return __float_as_uint(mx8::max_magnitude(__uint_as_float(x), __uint_as_float(y)));
+        }));
+        const int b = mx8::scale_byte(top);
         const int64_t row = mg * (2 * (int64_t)prm.I);
-        *reinterpret_cast<uint32_t*>(prm.z8 + row + at) = b == 255 ? 0 : w;
+        *reinterpret_cast<uint32_t*>(prm.z8 + row + at) = mx8::pack4(v.x, v.y, v.z, v.w, mx8::scale_value(b), b);
         if ((threadIdx.x & 7) == 0) prm.z8s[(row + at) / 32] = (uint8_t)b;
       };
       put(g, col);

@@ -225,11 +225,12 @@ static moe_status bf16_linear(int E, int64_t R, int K, int N, const bf16_t* x, c
 }
 
 // The products of the bf16 backward. dH = dY W2_e (W2_e is [H][I]: K rows, I contiguous) with the
-// dSwiGLU epilogue: dz [R, 2I] from z [R, 2I] (which may be dz itself: a tile reads its part of z
-// before it writes there), and dprob (rows from *end on not written, end != NULL).
+// dSwiGLU epilogue: dz [R, 2I] and dprob from z [R, 2I] in bf16, or (z NULL) from its MXFP8 codes
+// and scales, then with h [R, I] too and without the rows of dprob from *end on.
 static moe_status bf16_down_dgrad(const moe_mlp_desc& d, int64_t R, const bf16_t* dy, const PtrTab& w2,
                                   const int32_t* offsets, const float* prob, const bf16_t* z, bf16_t* dz, float* part,
-                                  float* dprob, const int32_t* end, hipStream_t s) {
+                                  float* dprob, hipStream_t s, const uint8_t* z8 = nullptr,
+                                  const uint8_t* z8s = nullptr, bf16_t* h = nullptr, const int32_t* end = nullptr) {
   gemm::Params p;
   std::memset(&p, 0, sizeof(p));
   std::memcpy(p.tab, w2.p, sizeof(p.tab));
@@ -241,6 +242,9 @@ static moe_status bf16_down_dgrad(const moe_mlp_desc& d, int64_t R, const bf16_t
   p.offsets = offsets;
   p.prob = prob;
   p.zin = z;
+  p.z8 = const_cast<uint8_t*>(z8);
+  p.z8s = const_cast<uint8_t*>(z8s);
+  p.hout = h;
   p.part = part;
   p.R = R;
   p.N = d.I;
@@ -249,8 +253,8 @@ static moe_status bf16_down_dgrad(const moe_mlp_desc& d, int64_t R, const bf16_t
   p.I = d.I;
   p.n_tiles = d.I / gemm::kBN;
   const int64_t mtiles = (R + gemm::kBM - 1) / gemm::kBM + d.E;
-  moe_status st = gemm::run(p, gemm::MNCONTIG, gemm::KCONTIG, gemm::GROUP_M, gemm::EPI_DSWIGLU, mtiles * p.n_tiles, s,
-                            "moe_grouped_mlp_bwd(down dgrad)");
+  moe_status st = gemm::run(p, gemm::MNCONTIG, gemm::KCONTIG, gemm::GROUP_M, z ? gemm::EPI_DSWIGLU : gemm::EPI_DSWIGLU_MX8,
+                            mtiles * p.n_tiles, s, "moe_grouped_mlp_bwd(down dgrad)");
   if (st != MOE_OK) return st;
   hipLaunchKernelGGL(reduce_partials, dim3((unsigned)((R + 31) / 32)), dim3(256), 0, s, (const float*)part,
                      2 * p.n_tiles, R, dprob, end);
@@ -301,26 +305,6 @@ static moe_status bf16_wgrad(const moe_mlp_desc& d, int64_t R, const bf16_t* a, 
   w.n_tiles = N / gemm::kBN;
   return gemm::run(w, gemm::MNCONTIG, gemm::MNCONTIG, gemm::GROUP_K, gemm::EPI_STORE,
                    (int64_t)d.E * (M / gemm::kBM) * w.n_tiles, s, what);
-}
-
-// h = silu(g) u p of the gate_up values z [R, 2I], for the rows before *end
-__global__ __launch_bounds__(256) void swiglu_rows_kernel(const uint4* __restrict__ z, const float* __restrict__ prob,
-                                                          int64_t R, uint32_t groups, const int32_t* __restrict__ end,
-                                                          uint4* __restrict__ h) {
-  const int64_t n = *end < 0 ? 0 : *end < R ? *end : R;
-  for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < n * groups; q += (int64_t)gridDim.x * 256) {
-    const int64_t r = q / groups, c = q - r * groups;
-    const uint4 g = z[r * 2 * groups + c], u = z[r * 2 * groups + groups + c];
-    const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w};
-    const float p = prob[r];
-    uint32_t o[4];
-    for (int i = 0; i < 4; ++i) {
-      const float g0 = bf16_to_f32(gw[i] & 0xFFFFu), g1 = bf16_to_f32(gw[i] >> 16);
-      const float u0 = bf16_to_f32(uw[i] & 0xFFFFu), u1 = bf16_to_f32(uw[i] >> 16);
-      o[i] = pack_bf16x2(g0 / (1.f + __expf(-g0)) * u0 * p, g1 / (1.f + __expf(-g1)) * u1 * p);
-    }
-    h[q] = make_uint4(o[0], o[1], o[2], o[3]);
-  }
 }
 
 }  // namespace moe
@@ -528,7 +512,7 @@ extern "C" moe_status moe_grouped_mlp_bwd(const moe_mlp_desc* desc, int64_t R, c
   const TailArea tail = tail_area(ws);  // split-K tail of the gate_up dgrad
   if (R > 0) {
     if ((st = bf16_down_dgrad(d, R, (const bf16_t*)dy_perm, w2, offsets, prob_perm, (const bf16_t*)z_save, dz, part,
-                              dprob_perm, nullptr, s)) != MOE_OK)
+                              dprob_perm, s)) != MOE_OK)
       return st;
     if ((st = bf16_gate_up_dgrad(d, R, dz, w1, offsets, (bf16_t*)dx_perm, tail, s)) != MOE_OK) return st;
   }
@@ -620,13 +604,8 @@ extern "C" moe_status moe_grouped_mlp_bwd_ckpt8(const moe_mlp_desc* desc, int64_
   const TailArea tail = tail_area(ws);
   const int32_t* end = offsets + d.E;
   if (R > 0) {
-    st = mx8::launch_read(z_codes, z_scales, R, 2 * (int64_t)d.I, nullptr, R, end, false, dz, s);
-    if (st != MOE_OK) return st;
-    const int64_t want = (R * (d.I / 8) + 255) / 256, most = (int64_t)num_cus() * 16;
-    hipLaunchKernelGGL(swiglu_rows_kernel, dim3((unsigned)(want < most ? want : most)), dim3(256), 0, s, (const uint4*)dz,
-                       prob_perm, R, (uint32_t)(d.I / 8), end, (uint4*)rows);
-    if ((st = check_launch(fn)) != MOE_OK) return st;
-    st = bf16_down_dgrad(d, R, (const bf16_t*)dy_perm, w2, offsets, prob_perm, dz, dz, part, dprob_perm, end, s);
+    st = bf16_down_dgrad(d, R, (const bf16_t*)dy_perm, w2, offsets, prob_perm, nullptr, dz, part, dprob_perm, s, z_codes,
+                         z_scales, rows, end);
     if (st != MOE_OK) return st;
     if ((st = bf16_gate_up_dgrad(d, R, dz, w1, offsets, (bf16_t*)dx_perm, tail, s)) != MOE_OK) return st;
   }

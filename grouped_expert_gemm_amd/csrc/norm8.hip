@@ -168,23 +168,21 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_norm_kernel(const P
       const bool in = i * TPR + tr < groups;  // groups % 4 == 0: the four lanes of a block agree
       float f[V];
       unpack8<BF16>(w[i], f);
-      uint32_t top = 0;
+      float top = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         acc[i][v] = acc[i][v] * r * f[v];
-        const uint32_t m = __float_as_uint(acc[i][v]) & 0x7FFFFFFFu;
-        top = m > top ? m : top;
+        top = mx8::max_magnitude(top, acc[i][v]);
       }
       if (p.y && in) store8<BF16>(p.y, at, pack8<BF16>(acc[i]));
-      const int b = mx8::scale_byte(lanes_umax<4>(top));
-      const float inv = mx8::inverse_scale(b);
-#pragma unroll
-      for (int v = 0; v < V; ++v) acc[i][v] *= inv;
+      top = __uint_as_float(lanes_reduce<4>(__float_as_uint(top), [](uint32_t a, uint32_t b) {
+        return __float_as_uint(mx8::max_magnitude(__uint_as_float(a), __uint_as_float(b)));
+      }));
+      const int b = mx8::scale_byte(top);
+      const float sc = mx8::scale_value(b);
       if (in) {
-        // a block that holds an infinity or a NaN: every code 0, its scale says NaN
-        p.codes[at] = b == 255 ? make_uint2(0, 0)
-                               : make_uint2(e4m3_pack4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]),
-                                            e4m3_pack4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]));
+        p.codes[at] = make_uint2(mx8::pack4(acc[i][0], acc[i][1], acc[i][2], acc[i][3], sc, b),
+                                 mx8::pack4(acc[i][4], acc[i][5], acc[i][6], acc[i][7], sc, b));
         if ((threadIdx.x & 3) == 0) p.scales[at >> 2] = (uint8_t)b;
       }
     }
