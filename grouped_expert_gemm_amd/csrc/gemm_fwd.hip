@@ -422,11 +422,33 @@ void grouped_gemm_fwd_kernel(const Params prm) {
           pw[sm] = prm.prob[mr < row_end ? mr : row_end - 1];  // rows past the expert: not stored
         }
         asm volatile("" : "+v"(pw[0]), "+v"(pw[1]), "+v"(pw[2]), "+v"(pw[3]));
+        // SWIGLU_MX8: z as MXFP8. A sub-tile's 32 columns are one block of each row, 16 values in
+        // this lane and 16 in lane ^ 32; its codes go to LDS rows of 128 bytes (gate: sH2, up: sH3;
+        // chunk c of row r at c ^ swz8(r)). A lane's four code words are every other word of the
+        // block; two half swaps turn them into its first or second 16 bytes. Returns the scale byte.
+        auto put8 = [&](const f32x16& v, uint8_t* arr, int row, int sq) -> int {
+          float top = 0.f;
+#pragma unroll
+          for (int x = 0; x < 16; ++x) top = mx8::max_magnitude(top, v[x]);
+          const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
+          const int b = mx8::scale_byte(mx8::max_magnitude(__uint_as_float(both[0]), __uint_as_float(both[1])));
+          const float sc = mx8::scale_value(b);
+          uint32_t w[4];
+#pragma unroll
+          for (int i4 = 0; i4 < 4; ++i4)
+            w[i4] = mx8::pack4(v[i4 * 4 + 0], v[i4 * 4 + 1], v[i4 * 4 + 2], v[i4 * 4 + 3], sc, b);
+          const auto s02 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+          const auto s13 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+          *reinterpret_cast<uint4*>(arr + row * 128 + (((en * 4 + sq * 2 + ehi) ^ swz8(row)) << 4)) =
+              make_uint4(s02[0], s02[1], s13[0], s13[1]);
+          return b;
+        };
 #pragma unroll
         for (int sm = 0; sm < 4; ++sm) {
           const float p = pw[sm];
+          int gb[2], ub[2];  // SWIGLU_MX8: the row's scale bytes
 #pragma unroll
-          for (int sq = 0; sq < 2; ++sq)
+          for (int sq = 0; sq < 2; ++sq) {
 #pragma unroll
             for (int i4 = 0; i4 < 4; ++i4) {
               float h[4];
@@ -438,40 +460,19 @@ void grouped_gemm_fwd_kernel(const Params prm) {
               }
               put(harr, sm, sq, i4, make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3])));
             }
+            if constexpr (EP == EPI_SWIGLU_MX8) {
+              gb[sq] = put8(acc[sq][sm], sH2, em * 128 + sm * 32 + e32, sq);
+              ub[sq] = put8(acc[sq + 2][sm], sH3, em * 128 + sm * 32 + e32, sq);
+            }
+          }
+          if constexpr (EP == EPI_SWIGLU_MX8) {  // sH4: 8 scale bytes a row, 4 of the gate columns, 4 of the up columns
+            uint8_t* at = sH4 + (em * 128 + sm * 32 + e32) * 8 + en * 2;  // both lanes of the row write the same
+            *reinterpret_cast<uint16_t*>(at) = (uint16_t)(gb[0] | gb[1] << 8);
+            *reinterpret_cast<uint16_t*>(at + 4) = (uint16_t)(ub[0] | ub[1] << 8);
+          }
         }
         const int64_t I = prm.I;
-        if constexpr (EP == EPI_SWIGLU_MX8) {
-          // z as MXFP8. A sub-tile's 32 columns are one block of each row, 16 values in this
-          // lane and 16 in lane ^ 32; its codes go to LDS rows of 128 bytes (gate: sH2, up:
-          // sH3; chunk c of row r at c ^ swz8(r)) and its scale bytes to sH4, 8 a row (4 of
-          // the gate columns, 4 of the up columns). A lane's four code words are every other
-          // word of the block; two half swaps turn them into its first or second 16 bytes.
-#pragma unroll
-          for (int sn = 0; sn < 4; ++sn)
-#pragma unroll
-            for (int sm = 0; sm < 4; ++sm) {
-              float top = 0.f;
-#pragma unroll
-              for (int x = 0; x < 16; ++x) top = mx8::max_magnitude(top, acc[sn][sm][x]);
-              const auto both = __builtin_amdgcn_permlane32_swap(__float_as_uint(top), __float_as_uint(top), false, false);
-              const int b = mx8::scale_byte(mx8::max_magnitude(__uint_as_float(both[0]), __uint_as_float(both[1])));
-              const float sc = mx8::scale_value(b);
-              uint32_t w[4];
-#pragma unroll
-              for (int i4 = 0; i4 < 4; ++i4)
-                w[i4] = mx8::pack4(acc[sn][sm][i4 * 4 + 0], acc[sn][sm][i4 * 4 + 1], acc[sn][sm][i4 * 4 + 2],
-                                   acc[sn][sm][i4 * 4 + 3], sc, b);
-              const auto s02 = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-              const auto s13 = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-              const int row = em * 128 + sm * 32 + e32;
-              const int chunk = en * 4 + (sn & 1) * 2 + ehi;
-              *reinterpret_cast<uint4*>((sn >> 1 ? sH3 : sH2) + row * 128 + ((chunk ^ swz8(row)) << 4)) =
-                  make_uint4(s02[0], s02[1], s13[0], s13[1]);
-              if (ehi == 0) sH4[row * 8 + (sn >> 1) * 4 + en * 2 + (sn & 1)] = (uint8_t)b;
-            }
-        } else {
-          if (prm.zout) acc_block(0, sH2, sH3);
-        }
+        if (EP == EPI_SWIGLU && prm.zout) acc_block(0, sH2, sH3);
         lds_barrier();
         drain(wv < 2 ? sH0 : sH1, prm.c + (int64_t)nt * 128, prm.c_ld);
         if constexpr (EP == EPI_SWIGLU_MX8) {

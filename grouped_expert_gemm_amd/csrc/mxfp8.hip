@@ -11,6 +11,9 @@
 namespace moe {
 namespace mx8 {
 
+constexpr int kItems = 4;  // loads of a thread in flight together
+
+template <bool GATHER>
 __global__ __launch_bounds__(256) void read_kernel(const uint4* __restrict__ codes, const uint8_t* __restrict__ scales,
                                                    int64_t src_rows, uint32_t row16, const int32_t* __restrict__ src_row,
                                                    int64_t rows, const int32_t* __restrict__ limit,
@@ -18,25 +21,41 @@ __global__ __launch_bounds__(256) void read_kernel(const uint4* __restrict__ cod
   int64_t n = rows;
   if (limit) n = *limit < 0 ? 0 : *limit < rows ? *limit : rows;
   const int64_t total = n * row16;
-  for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < total; q += (int64_t)gridDim.x * 256) {
-    const int64_t r = total <= 0xFFFFFFFFll ? (int64_t)((uint32_t)q / row16) : q / row16;
-    const int64_t c = q - r * row16;
-    const int64_t from = src_row ? src_row[r] : r;
-    if (from < 0 || from >= src_rows) {
+  const int64_t q0 = (int64_t)blockIdx.x * (256 * kItems) + threadIdx.x;
+  int64_t at[kItems];
+  uint4 w[kItems];
+  uint8_t sb[kItems];
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    const int64_t q = q0 + i * 256;
+    at[i] = q;
+    if constexpr (GATHER) {
+      const int64_t r = total <= 0xFFFFFFFFll ? (int64_t)((uint32_t)q / row16) : q / row16;
+      const int64_t from = q < total ? src_row[r] : -1;
+      at[i] = from < 0 || from >= src_rows ? -1 : from * row16 + (q - r * row16);
+    }
+    if (q < total && at[i] >= 0) {
+      w[i] = codes[at[i]];
+      sb[i] = scales[at[i] >> 1];  // two items a block (row16 is even)
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    const int64_t q = q0 + i * 256;
+    if (q >= total) break;
+    if (GATHER && at[i] < 0) {
       if (zero_missing) out[2 * q] = out[2 * q + 1] = make_uint4(0, 0, 0, 0);
       continue;
     }
-    const int64_t at = from * row16 + c;
-    const uint4 w = codes[at];
-    const float sc = scale_value(scales[at >> 1]);  // two threads a block (row16 is even)
-    const uint32_t word[4] = {w.x, w.y, w.z, w.w};
+    const float sc = scale_value(sb[i]);
+    const uint32_t word[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
     uint32_t o[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int j = 0; j < 4; ++j) {
       float v[4];
-      unpack4(word[i], sc, v);
-      o[2 * i] = pack_bf16x2(v[0], v[1]);
-      o[2 * i + 1] = pack_bf16x2(v[2], v[3]);
+      unpack4(word[j], sc, v);
+      o[2 * j] = pack_bf16x2(v[0], v[1]);
+      o[2 * j + 1] = pack_bf16x2(v[2], v[3]);
     }
     out[2 * q] = make_uint4(o[0], o[1], o[2], o[3]);
     out[2 * q + 1] = make_uint4(o[4], o[5], o[6], o[7]);
@@ -48,11 +67,11 @@ moe_status launch_read(const uint8_t* codes, const uint8_t* scales, int64_t src_
                        hipStream_t s) {
   const int64_t row16 = cols / 16;
   if (rows == 0 || cols == 0) return MOE_OK;
-  int64_t grid = (rows * row16 + 255) / 256;
-  const int64_t most = (int64_t)num_cus() * 16;
-  if (grid > most) grid = most;
-  hipLaunchKernelGGL(read_kernel, dim3((unsigned)grid), dim3(256), 0, s, (const uint4*)codes, scales, src_rows,
-                     (uint32_t)row16, src_row, rows, limit, zero_missing, (uint4*)out);
+  const int64_t grid = (rows * row16 + 256 * kItems - 1) / (256 * kItems);
+  if (grid > 0x7FFFFFFF) return fail(MOE_ERR_UNSUPPORTED, "mxfp8_dequantize: more elements than one launch holds");
+  const auto kernel = src_row ? read_kernel<true> : read_kernel<false>;
+  hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256), 0, s, (const uint4*)codes, scales, src_rows, (uint32_t)row16,
+                     src_row, rows, limit, zero_missing, (uint4*)out);
   return check_launch("mxfp8_dequantize");
 }
 
