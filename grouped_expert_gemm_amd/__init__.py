@@ -374,16 +374,19 @@ def moe_add_norm_mxfp8(x: torch.Tensor, weight: torch.Tensor, residual: torch.Te
     for t in (residual, out):
         if t is not None and t.shape != (T, H):
             raise ValueError(f"{fn}: residual and out must be [T, H]")
-    dev = x.device
     added = out
-    if added is None and (residual is not None or row_id_map is not None):
-        added = torch.empty((T, H), dtype=x.dtype, device=dev)
-    r = dict(sum=added if added is not None else x, codes=torch.empty((T, H), dtype=torch.uint8, device=dev),
-             scales=torch.empty((T, H // 32), dtype=torch.uint8, device=dev))
+    if added is None and residual is not None:
+        added = torch.empty_like(residual)
+    elif added is None and row_id_map is not None:
+        added = x.new_empty((T, H))
+    r = dict(sum=added if added is not None else x)
+    rows = r["sum"]
+    r["codes"] = torch.empty_like(rows, dtype=torch.uint8)
+    r["scales"] = r["codes"].new_empty((T, H // 32))
     if with_y:
-        r["y"] = torch.empty((T, H), dtype=x.dtype, device=dev)
+        r["y"] = torch.empty_like(rows)
     if save_for_bwd:
-        r["rstd"] = torch.empty(T, dtype=torch.float32, device=dev)
+        r["rstd"] = torch.empty(T, dtype=torch.float32, device=x.device)
     _launch(fn, x, _a(x), _a(row_id_map), k, _a(residual), _a(weight), dt, T, H, eps, _a(added), _a(r.get("y")),
             _a(r.get("rstd")), _a(r["codes"]), _a(r["scales"]))
     return r
@@ -463,18 +466,18 @@ def mxfp8_dequantize(codes: torch.Tensor, scales: torch.Tensor, src_row: torch.T
     whose index is out of range are left as they were."""
     fn = "mxfp8_dequantize"
     _need(fn, codes, scales, src_row, out)
-    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or codes.dim() < 1 \
-            or scales.shape != (*codes.shape[:-1], codes.shape[-1] // 32):
-        raise ValueError(f"{fn}: codes must be uint8 [..., cols] and scales uint8 [..., cols/32]")
-    cols = codes.shape[-1]
-    src_rows = codes.numel() // cols if cols else 0
     shape = codes.shape
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or not shape or scales.dim() != len(shape) \
+            or scales.shape[:-1] != shape[:-1] or scales.shape[-1] != shape[-1] // 32:
+        raise ValueError(f"{fn}: codes must be uint8 [..., cols] and scales uint8 [..., cols/32]")
+    cols = shape[-1]
+    src_rows = codes.numel() // cols if cols else 0
     if src_row is not None:
-        if codes.dim() != 2 or src_row.dtype != torch.int32 or src_row.dim() != 1:
+        if len(shape) != 2 or src_row.dtype != torch.int32 or src_row.dim() != 1:
             raise ValueError(f"{fn}: src_row must be int32 [rows], with 2-D codes")
         shape = (src_row.shape[0], cols)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=codes.device)
+        out = codes.new_empty(shape, dtype=torch.bfloat16)
     elif out.dtype != torch.bfloat16 or out.shape != shape:
         raise ValueError(f"{fn}: out must be bfloat16 [rows, cols]")
     rows = src_rows if src_row is None else shape[0]

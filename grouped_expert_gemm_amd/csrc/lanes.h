@@ -38,6 +38,31 @@ __device__ __forceinline__ float lanes_sum(float v) {
       __float_as_uint(v), [](uint32_t a, uint32_t b) { return __float_as_uint(__uint_as_float(a) + __uint_as_float(b)); }));
 }
 
+// the sum of a float64 over the wavefront: both halves move, the additions are the ALU's own
+__device__ __forceinline__ double wave_sum(double v) {
+  auto add = [&](uint32_t lo, uint32_t hi) { v += __hiloint2double((int)hi, (int)lo); };
+  auto step = [&](auto move) {
+    const uint32_t lo = (uint32_t)__double2loint(v), hi = (uint32_t)__double2hiint(v);
+    add(move(lo), move(hi));
+  };
+  step([](uint32_t x) { return lane_move<0xB1>(x); });
+  step([](uint32_t x) { return lane_move<0x4E>(x); });
+  step([](uint32_t x) { return lane_move<0x141>(x); });
+  step([](uint32_t x) { return lane_move<0x140>(x); });
+  const auto swapped = [&](auto a, auto b) { return __hiloint2double((int)b, (int)a); };
+  {
+    const uint32_t lo = (uint32_t)__double2loint(v), hi = (uint32_t)__double2hiint(v);
+    const auto l = __builtin_amdgcn_permlane16_swap(lo, lo, false, false), h = __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
+    v = swapped(l[0], h[0]) + swapped(l[1], h[1]);
+  }
+  {
+    const uint32_t lo = (uint32_t)__double2loint(v), hi = (uint32_t)__double2hiint(v);
+    const auto l = __builtin_amdgcn_permlane32_swap(lo, lo, false, false), h = __builtin_amdgcn_permlane32_swap(hi, hi, false, false);
+    v = swapped(l[0], h[0]) + swapped(l[1], h[1]);
+  }
+  return v;
+}
+
 template <int L>
 __device__ __forceinline__ float lanes_max(float v) {
   return __uint_as_float(lanes_reduce<L>(__float_as_uint(v), [](uint32_t a, uint32_t b) {

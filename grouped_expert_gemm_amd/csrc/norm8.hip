@@ -7,6 +7,9 @@
 // HBM-bound: k + 1 rows in, the sum, the codes and (on request) n in the stored dtype out. A
 // team of TPR threads holds one row in registers, NV groups of 8 columns a thread, so four
 // neighbouring lanes hold a block; its maximum takes two lane moves.
+// The sums of 8 squares are added up in float64 and r is kept as two float32 words, so that n is the
+// exact product rounded about once: of the values next to a border between two codes, most that
+// float32 sums and products would push across it stay on their side.
 #include <type_traits>
 
 #include "common.h"
@@ -89,10 +92,10 @@ __device__ __forceinline__ Raw<BF16> pack8(const float* f) {
 template <bool BF16, int TPR, int NV>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_norm_kernel(const Params p) {
   constexpr int kTeams = TPR < 256 ? 256 / TPR : 1;
-  __shared__ float red[2][TPR > 64 ? TPR / 64 : 1];  // alternating: a thread is at most one row ahead
+  __shared__ double red[2][TPR > 64 ? TPR / 64 : 1];  // alternating: a thread is at most one row ahead
   const int tr = threadIdx.x % TPR;
   const int groups = p.H / V;
-  const float inv_h = 1.f / (float)p.H;  // applied to each term: a sum of squares would overflow H times earlier
+  const double inv_h = 1.0 / p.H;
   Raw<BF16> w[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -110,7 +113,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_norm_kernel(const P
       res[i] = Raw<BF16>{};
       if (p.residual && i * TPR + tr < groups) res[i] = load8<BF16>(p.residual, t * groups + i * TPR + tr);
     }
-    constexpr int kSlots = NV <= 2 ? 4 : 2;  // rows whose loads are in flight together
+    constexpr int kSlots = BF16 || NV <= 2 ? 4 : 2;  // rows whose loads are in flight together
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -138,7 +141,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_norm_kernel(const P
           for (int v = 0; v < V; ++v) acc[i][v] += f[v];
         }
     }
-    float ss = 0.f;
+    double ss = 0.0;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       float f[V];
@@ -149,19 +152,23 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_norm_kernel(const P
       if (p.sum && i * TPR + tr < groups) store8<BF16>(p.sum, t * groups + i * TPR + tr, o);
       unpack8<BF16>(o, acc[i]);  // the norm reads the sum as it is stored
 #pragma unroll
-      for (int v = 0; v < V; ++v) ss += acc[i][v] * inv_h * acc[i][v];
+      for (int v = 0; v < V; ++v) f[v] = acc[i][v] * acc[i][v];  // exact for bf16
+      ss += (double)(((f[0] + f[1]) + (f[2] + f[3])) + ((f[4] + f[5]) + (f[6] + f[7])));
     }
-    ss = lanes_sum<64>(ss);
+    ss = wave_sum(ss);
     if constexpr (TPR > 64) {
       if ((threadIdx.x & 63) == 0) red[par][threadIdx.x >> 6] = ss;
       __syncthreads();
-      ss = 0.f;
+      ss = 0.0;
 #pragma unroll
       for (int i = 0; i < TPR / 64; ++i) ss += red[par][i];
       par ^= 1;
     }
-    const float r = 1.f / sqrtf(ss + p.eps);
-    if (p.rstd && tr == 0) p.rstd[t] = r;
+    // r to float64 by one Newton step from its float32 value (0 and NaN stay as they are)
+    const double m = ss * inv_h + (double)p.eps, r0 = (double)(1.f / sqrtf((float)m));
+    const double r = r0 > 0.0 ? r0 * (1.5 - 0.5 * m * r0 * r0) : r0;
+    const float rh = (float)r, rl = (float)(r - (double)rh);
+    if (p.rstd && tr == 0) p.rstd[t] = rh;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int64_t at = t * groups + i * TPR + tr;
@@ -171,7 +178,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_norm_kernel(const P
       float top = 0.f;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        acc[i][v] = acc[i][v] * r * f[v];
+        const float a = acc[i][v], q = a * rh;
+        const float e = __builtin_fmaf(a, rl, __builtin_fmaf(a, rh, -q));  // s r - q
+        acc[i][v] = __builtin_fmaf(q, f[v], e * f[v]);
         top = mx8::max_magnitude(top, acc[i][v]);
       }
       if (p.y && in) store8<BF16>(p.y, at, pack8<BF16>(acc[i]));

@@ -327,7 +327,8 @@ moe_status moe_post_norm_bwd(const void* dout, const void* c, const float* rstd,
  * norm. Its dx is the gradient of the residual and of every row of x that entered the sum
  * (moe_permute with reuse_map lays it out by rows); the rounding to 8 bits passes it unchanged.
  * Limits: H % 32 == 0, H <= 16384, 1 <= k <= 16, T * k < 2^31, eps > 0; tensors 16-byte, codes
- * 8-byte aligned.
+ * 8-byte aligned; magnitudes of s below 2^62 (squares are summed eight at a time in float32; a row
+ * beyond that normalises to 0, one with an infinity to NaN there).
  */
 moe_status moe_add_norm_mxfp8(const void* x, const int32_t* row_id_map, int k, const void* residual,
                               const void* weight, moe_dtype dt, int64_t T, int H, float eps, void* sum, void* y,
