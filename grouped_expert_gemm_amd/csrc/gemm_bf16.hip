@@ -740,17 +740,20 @@ void grouped_gemm_kernel(const Params prm) {
           }
         }
       };
+      // codes of pass j + 2 are asked for before pass j's stores: loads and stores retire in order,
+      // so a wait for the codes leaves two passes' stores under way
       v4u32 g0[2], u0[2], g1[2], u1[2];
       fetch(std::integral_constant<int, 0>{}, g0, u0);
+      fetch(std::integral_constant<int, 1>{}, g1, u1);
       static_for<4>([&](auto H) {
         using J0 = std::integral_constant<int, 2 * decltype(H)::value>;
         using J1 = std::integral_constant<int, 2 * decltype(H)::value + 1>;
-        fetch(J1{}, g1, u1);
         compute(J0{}, g0, u0);
+        if constexpr (decltype(H)::value < 3) fetch(std::integral_constant<int, J0::value + 2>{}, g0, u0);
         lds_barrier();
         store_out(J0{});
-        if constexpr (decltype(H)::value < 3) fetch(std::integral_constant<int, J1::value + 1>{}, g0, u0);
         compute(J1{}, g1, u1);
+        if constexpr (decltype(H)::value < 3) fetch(std::integral_constant<int, J1::value + 2>{}, g1, u1);
         lds_barrier();
         store_out(J1{});
       });
