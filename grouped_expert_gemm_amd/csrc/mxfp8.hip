@@ -68,7 +68,7 @@ moe_status launch_read(const uint8_t* codes, const uint8_t* scales, int64_t src_
   const int64_t row16 = cols / 16;
   if (rows == 0 || cols == 0) return MOE_OK;
   const int64_t grid = (rows * row16 + 256 * kItems - 1) / (256 * kItems);
-  if (grid > 0x7FFFFFFF) return fail(MOE_ERR_UNSUPPORTED, "mxfp8_dequantize: more elements than one launch holds");
+  if (grid > 0xFFFFFFFF / 256) return fail(MOE_ERR_UNSUPPORTED, "mxfp8_dequantize: more elements than one launch holds");
   const auto kernel = src_row ? read_kernel<true> : read_kernel<false>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256), 0, s, (const uint4*)codes, scales, src_rows, (uint32_t)row16,
                      src_row, rows, limit, zero_missing, (uint4*)out);

@@ -118,7 +118,7 @@ def _backward_check(moe, c, zc, zs, got, xv, what):
 # fill the launch's last round, so nothing is split along K, and others leave it half empty
 CASES = [([600], 256, 256, 0), ([1], 256, 256, 0), ([0, 3, 0, 0, 257, 0], 256, 512, 0), ([256, 255, 1], 512, 256, 5),
          ([0, 0], 256, 256, 4), ([40, 300, 17, 0], 1024, 256, 0), ([513, 64], 768, 768, 31), ([64] * 16, 256, 256, 0),
-         ([700], 512, 1024, 0)]
+         ([700], 512, 1024, 0), ([1, 0, 3, 2] * 64, 256, 256, 3)]
 
 
 @pytest.mark.parametrize("counts,H,I,behind", CASES)
