@@ -856,7 +856,7 @@ def moe_grouped_mlp_fwd_ckpt8(x_perm: torch.Tensor, w_gate_up, w_down, offsets: 
     """moe_grouped_mlp_fwd in bf16 that keeps its gate_up output in MXFP8 for moe_grouped_mlp_bwd_ckpt8, and
     nothing else. Returns (y_perm [R, H], z_codes uint8 [R, 2I], z_scales uint8 [R, 2I / 32]).
 
-    y_perm is that of moe_grouped_mlp_fwd, bit for bit; rows past the last expert's are not written."""
+    y_perm is that of moe_grouped_mlp_fwd up to the order of its sums; rows past the last expert's are not written."""
     fn = "moe_grouped_mlp_fwd_ckpt8"
     _need(fn, x_perm, offsets, prob_perm, out, workspace)
     if x_perm.dtype != torch.bfloat16 or x_perm.dim() != 2:

@@ -49,6 +49,7 @@ struct Params {
   float* tail;
   int32_t* tail_meta;
   int tail_cap;
+  int spread;    // with a tail: one workgroup per CU also where there are fewer tiles, so that those are split
   uint8_t* z8;   // E4M3 codes of the gate_up output [R, 2I] (SWIGLU_MX8: out, DSWIGLU_MX8: in)
   uint8_t* z8s;  // ... and its E8M0 scales [R, 2I / 32]
   bf16_t* hout;  // DSWIGLU_MX8: h [R, I]
@@ -58,6 +59,11 @@ constexpr size_t kTailTileBytes = (size_t)kBM * kBN * 4;  // one float32 partial
 constexpr size_t kTailMetaSpace = 8192;                   // header + up to 511 tail tiles
 // bytes of a split-K tail area (meta, then `units` partial tiles)
 inline size_t tail_ws_bytes(int units) { return kTailMetaSpace + (size_t)units * kTailTileBytes; }
+
+// workgroups of a launch over at most max_tiles tiles
+inline int64_t grid_size(const Params& p, int64_t max_tiles, int cus) {
+  return (p.spread && p.tail_cap > 0) || max_tiles > cus ? cus : max_tiles;
+}
 
 moe_status run(const Params& p, int pl, int ql, int g, int ep, int64_t max_tiles, hipStream_t s,
                const char* what);

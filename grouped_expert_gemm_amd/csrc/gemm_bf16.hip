@@ -901,8 +901,7 @@ void grouped_gemm_kernel(const Params prm) {
 template <int PL, int QL, int G, int EP>
 static moe_status launch(const Params& p, int64_t max_tiles, hipStream_t s, const char* what) {
   if (max_tiles <= 0) return MOE_OK;
-  int64_t grid = num_cus();
-  if (max_tiles < grid) grid = max_tiles;
+  const int64_t grid = grid_size(p, max_tiles, num_cus());
   hipLaunchKernelGGL((grouped_gemm_kernel<PL, QL, G, EP, false>), dim3((unsigned)grid), dim3(256), 0, s, p);
   moe_status st = check_launch(what);
   if constexpr (G == GROUP_M && EP == EPI_STORE) {

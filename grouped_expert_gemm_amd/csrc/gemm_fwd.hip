@@ -578,8 +578,7 @@ __global__ __launch_bounds__(256) void tail_reduce_kernel(const Params prm) {
 template <int EP>
 static moe_status launch_fwd(const Params& p, int64_t max_tiles, hipStream_t s, const char* what) {
   if (max_tiles <= 0) return MOE_OK;
-  int64_t grid = num_cus();
-  if (max_tiles < grid) grid = max_tiles;
+  const int64_t grid = grid_size(p, max_tiles, num_cus());
   hipLaunchKernelGGL((grouped_gemm_fwd_kernel<EP, false>), dim3((unsigned)grid), dim3(256), 0, s, p);
   moe_status st = check_launch(what);
   if (st != MOE_OK || p.tail_cap <= 0) return st;
@@ -602,9 +601,8 @@ moe_status run_fwd(const Params& p, int ep, int64_t max_tiles, hipStream_t s, co
 
 moe_status run_tail_reduce(const Params& p, int ep, int64_t max_tiles, hipStream_t s, const char* what) {
   // at most half a round of tiles is ever split: the grid covers that many
-  int64_t nwg = num_cus();
-  if (max_tiles < nwg) nwg = max_tiles;
-  const int64_t max_tail = nwg / 2;
+  int64_t max_tail = grid_size(p, max_tiles, num_cus()) / 2;
+  if (max_tail > max_tiles) max_tail = max_tiles;
   if (max_tail <= 0) return MOE_OK;
   if (ep == EPI_SWIGLU) {
     hipLaunchKernelGGL((tail_reduce_kernel<EPI_SWIGLU>), dim3((unsigned)(max_tail * (kBM / 8))), dim3(256), 0, s, p);

@@ -156,6 +156,7 @@ struct TailArea {
   float* part = nullptr;
   int32_t* meta = nullptr;
   int cap = 0;
+  bool spread = false;
 };
 static TailArea tail_area(uint8_t* base) {
   TailArea t;
@@ -165,10 +166,20 @@ static TailArea tail_area(uint8_t* base) {
   t.cap = num_cus();
   return t;
 }
+// The 8-bit checkpoint calls' tails: a product of K <= 512 is not split (the two launches of a tail
+// take about what its chunks save: one tile of 256 columns, K = 512, 20.3 us split and 15.9 not, K = 1024
+// 24.1 and 25.0), a longer one also where its tiles are fewer than the CUs (16 tiles of K = 4096: 82 us
+// with one workgroup a tile).
+static TailArea tail_for(const TailArea& t, int K) {
+  TailArea r = K > 512 ? t : TailArea();
+  r.spread = true;
+  return r;
+}
 static void set_tail(gemm::Params& p, const TailArea& t) {
   p.tail = t.part;
   p.tail_meta = t.meta;
   p.tail_cap = t.cap;
+  p.spread = t.spread;
 }
 
 // bf16 GroupedLinear(gate_up) + ScaledSwiGLU: h [R, I] (and z [R, 2I] when z != NULL, or its MXFP8
@@ -550,9 +561,9 @@ extern "C" moe_status moe_grouped_mlp_fwd_ckpt8(const moe_mlp_desc* desc, int64_
   bf16_t* h = (bf16_t*)workspace;
   const TailArea tail = tail_area((uint8_t*)workspace + a256((size_t)R * d.I * 2));
   st = bf16_gate_up(d.E, R, d.H, d.I, (const bf16_t*)x_perm, make_tab(w_gate_up, d.E), offsets, prob_perm, h, nullptr, s,
-                    tail, z_codes, z_scales);
+                    tail_for(tail, d.H), z_codes, z_scales);
   if (st != MOE_OK) return st;
-  return bf16_linear(d.E, R, d.I, d.H, h, make_tab(w_down, d.E), offsets, (bf16_t*)y_perm, s, tail);
+  return bf16_linear(d.E, R, d.I, d.H, h, make_tab(w_down, d.E), offsets, (bf16_t*)y_perm, s, tail_for(tail, d.I));
 }
 
 extern "C" moe_status moe_grouped_mlp_bwd_ckpt8(const moe_mlp_desc* desc, int64_t R, const void* dy_perm, const void* x,
@@ -607,7 +618,7 @@ extern "C" moe_status moe_grouped_mlp_bwd_ckpt8(const moe_mlp_desc* desc, int64_
     st = bf16_down_dgrad(d, R, (const bf16_t*)dy_perm, w2, offsets, prob_perm, nullptr, dz, part, dprob_perm, s, z_codes,
                          z_scales, rows, end);
     if (st != MOE_OK) return st;
-    if ((st = bf16_gate_up_dgrad(d, R, dz, w1, offsets, (bf16_t*)dx_perm, tail, s)) != MOE_OK) return st;
+    if ((st = bf16_gate_up_dgrad(d, R, dz, w1, offsets, (bf16_t*)dx_perm, tail_for(tail, 2 * d.I), s)) != MOE_OK) return st;
   }
   st = bf16_wgrad(d, R, (const bf16_t*)dy_perm, d.H, rows, d.I, dw2, offsets, s, "moe_grouped_mlp_bwd_ckpt8(down wgrad)");
   if (st != MOE_OK) return st;

@@ -611,7 +611,7 @@ moe_status moe_grouped_mlp_bwd(const moe_mlp_desc* desc, int64_t R, const void* 
  * moe_grouped_mlp_fwd in bf16 that keeps what the backward needs in 8 bits: the gate_up output
  * z [R, 2I] as MXFP8, made from its float32 sums in the GEMM's epilogue, and nothing of h, which
  * moe_grouped_mlp_bwd_ckpt8 computes again. A routed row's checkpoint is 2I (1 + 1/32) bytes
- * where z_save and h_save take 6I. y_perm is the bf16 forward's, bit for bit.
+ * where z_save and h_save take 6I. y_perm is the bf16 forward's, up to the order of its float32 sums.
  *   desc: compute, act and wt MOE_BF16 (save_for_bwd is ignored)
  *   z_codes [R, 2I] (out, 16-byte aligned), z_scales [R, 2I/32] (out, 4-byte aligned): per 32
  *     columns of a row one scale and the E4M3 codes by the rule of mxfp8_quantize; a block that

@@ -55,8 +55,6 @@ class Case:
 
 def _forward_check(moe, c):
     y, zc, zs = moe.moe_grouped_mlp_fwd_ckpt8(c.x, c.w1, c.w2, c.offsets, c.prob)
-    plain = moe.moe_grouped_mlp_fwd(c.x, c.w1, c.w2, c.offsets, c.prob)
-    assert torch.equal(y[:c.used], plain[:c.used]), "y differs from the bf16 forward's"
     codes, scales = host(zc)[:c.used], host(zs)[:c.used]
     x, w1 = host(c.x), host(c.w1)
     z, mag = np.zeros((c.used, 2 * c.I)), np.zeros((c.used, 2 * c.I))
@@ -68,6 +66,18 @@ def _forward_check(moe, c):
         v = oracle.mxfp8_dequantize(codes, scales)
         assert ok.all(), "scale bytes of z"
         assert np.all((lo <= v) & (v <= hi)), "codes of z"
+    got, w2, p = host(y), host(c.w2), host(c.prob).astype(np.float64)
+    for e in range(c.E):
+        r = slice(c.off_host[e], c.off_host[e + 1])
+        g, u, pe = z[r, :c.I], z[r, c.I:], p[r, None]
+        sig = 1 / (1 + np.exp(-np.clip(g, -700, None)))
+        h, ez = g * sig * u * pe, c.H * U * mag[r]
+        slope = sig + np.abs(g) * sig * (1 - sig)                       # of silu; h moves with z's error
+        eh = (HALF + 20 * U) * np.abs(h) + (1 + HALF) * pe * (slope * np.abs(u) * ez[:, :c.I] + np.abs(g * sig) * ez[:, c.I:])
+        ref, w = h @ w2[e].T, np.abs(w2[e]).T
+        tol = HALF * np.abs(ref) + (1 + HALF) * (eh @ w + c.I * U * (np.abs(h) + eh) @ w) + 1e-30
+        assert np.all(np.abs(got[r] - ref) <= tol), f"y of expert {e}"
+        assert np.linalg.norm(got[r] - ref) <= 2 * HALF * np.linalg.norm(ref), f"y of expert {e} (norm)"
     return zc, zs
 
 
@@ -114,11 +124,11 @@ def _backward_check(moe, c, zc, zs, got, xv, what):
 
 
 # an expert of many row tiles (the last ones whole and ragged), one row, idle ones first, in the
-# middle and last; K of few and of many steps; H wider and narrower than I; one expert's tiles
-# fill the launch's last round, so nothing is split along K, and others leave it half empty
+# middle and last; K of few and of many steps (above 512 the tiles are split along K, but where they
+# fill more than half of the card, as [1000] does); H wider and narrower than I
 CASES = [([600], 256, 256, 0), ([1], 256, 256, 0), ([0, 3, 0, 0, 257, 0], 256, 512, 0), ([256, 255, 1], 512, 256, 5),
          ([0, 0], 256, 256, 4), ([40, 300, 17, 0], 1024, 256, 0), ([513, 64], 768, 768, 31), ([64] * 16, 256, 256, 0),
-         ([700], 512, 1024, 0), ([1, 0, 3, 2] * 64, 256, 256, 3)]
+         ([700], 512, 1024, 0), ([1000], 768, 4352, 0), ([5, 0, 9], 2048, 768, 0), ([1, 0, 3, 2] * 64, 256, 256, 3)]
 
 
 @pytest.mark.parametrize("counts,H,I,behind", CASES)
