@@ -68,36 +68,36 @@ void grouped_gemm_kernel(const Params prm) {
   const int wm = wave >> 1, wn = wave & 1;
   const int E = prm.E;
 
-  for (int e = tid; e <= E; e += 256) s_off[e] = prm.offsets[e];
-  __syncthreads();
-  if (tid == 0) {  // make the offsets a nondecreasing sequence inside [0, R]: no access leaves the tensors
-    int prev = 0;
-    for (int e = 0; e <= E; ++e) {
-      int v = s_off[e];
-      v = v < prev ? prev : v;
-      v = v > (int)prm.R ? (int)prm.R : v;
-      s_off[e] = v;
-      prev = v;
+  // The offsets as a nondecreasing sequence inside [0, R] (no access leaves the tensors), and each
+  // expert's first tile: one wavefront scans 64 at a time.
+  if (wave == 0) {
+    const int R = (int)prm.R;
+    int top = 0;
+    for (int e0 = 0; e0 <= E; e0 += 64) {
+      const int e = e0 + lane;
+      int v = e <= E ? prm.offsets[e] : 0;
+      v = v < 0 ? 0 : v > R ? R : v;
+      v = wave_scan_max(v);
+      v = v > top ? v : top;
+      top = __builtin_amdgcn_readlane(v, 63);
+      if (e <= E) s_off[e] = e == 0 ? 0 : v;
     }
-    s_off[0] = 0;
+    if constexpr (G == GROUP_M) {
+      int first = 0;
+      for (int e0 = 0; e0 < E; e0 += 64) {
+        const int e = e0 + lane;
+        const int n = e < E ? ((s_off[e + 1] - s_off[e] + kBM - 1) / kBM) * prm.n_tiles : 0;
+        const int run = wave_scan_sum(n);
+        if (e < E) s_tstart[e] = first + run - n;
+        first += __builtin_amdgcn_readlane(run, 63);
+      }
+      if (lane == 0) s_tstart[E] = first;
+    }
   }
   __syncthreads();
   int total;
-  if constexpr (G == GROUP_M) {
-    if (tid == 0) {
-      int run = 0;
-      for (int e = 0; e < E; ++e) {
-        s_tstart[e] = run;
-        const int me = s_off[e + 1] - s_off[e];
-        run += ((me + kBM - 1) / kBM) * prm.n_tiles;
-      }
-      s_tstart[E] = run;
-    }
-    __syncthreads();
-    total = s_tstart[E];
-  } else {
-    total = E * (prm.M / kBM) * prm.n_tiles;
-  }
+  if constexpr (G == GROUP_M) total = s_tstart[E];
+  else total = E * (prm.M / kBM) * prm.n_tiles;
 
   const int nwg = gridDim.x;
   const int logical = (nwg % 8 == 0) ? (blockIdx.x % 8) * (nwg / 8) + blockIdx.x / 8 : blockIdx.x;

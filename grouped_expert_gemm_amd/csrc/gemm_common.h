@@ -91,6 +91,24 @@ __host__ __device__ __forceinline__ void tile_in_expert(int local, int mte, int 
   nt = rem / gm;
 }
 
+// Scans over the lanes of a wavefront (every lane active): lane l gets op over lanes 0..l.
+template <typename F>
+__device__ __forceinline__ int wave_scan(int v, F op) {
+  const int lane = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int o = __shfl_up(v, d);
+    if (lane >= d) v = op(v, o);
+  }
+  return v;
+}
+__device__ __forceinline__ int wave_scan_max(int v) {
+  return wave_scan(v, [](int a, int b) { return a > b ? a : b; });
+}
+__device__ __forceinline__ int wave_scan_sum(int v) {
+  return wave_scan(v, [](int a, int b) { return a + b; });
+}
+
 __device__ __forceinline__ void lds_barrier() {
   __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0); vmcnt, expcnt unconstrained
   __atomic_signal_fence(__ATOMIC_SEQ_CST);

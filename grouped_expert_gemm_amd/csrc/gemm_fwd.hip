@@ -71,33 +71,49 @@ void grouped_gemm_fwd_kernel(const Params prm) {
   };
 
   // Tile order: expert-major, ceil(rows_e / 256) row tiles x n_tiles per expert, row
-  // tiles fastest within groups of at most 16 (tile_in_expert). A workgroup's tiles only move forward, so it walks the expert
-  // offsets once (wavefront-uniform loads), making them a nondecreasing sequence inside
-  // [0, R] on the way: no access leaves the tensors.
+  // tiles fastest within groups of at most 16 (tile_in_expert). The expert offsets become a
+  // nondecreasing sequence inside [0, R]: no access leaves the tensors. Each wavefront scans
+  // them by itself, 64 experts at a time, for the number of tiles and its first tile's expert
+  // (one expert after the other, each a scalar load, took 13 us a launch at E = 128); from there
+  // a workgroup's tiles only move forward, so it walks the offsets (wavefront-uniform loads).
   auto clamp_off = [&](int v, int prev) -> int {
     v = v < prev ? prev : v;
     return v > R ? R : v;
   };
-  int e_w = 0;
-  int ob = 0;
-  int oe = clamp_off(load_const(prm.offsets, 1), 0);
-  int ts_w = 0;
-  int nt_w = ((oe - ob + kBM - 1) / kBM) * prm.n_tiles;
+  int e_w = E, ob = 0, oe = 0, ts_w = 0, nt_w = 0;  // the expert of the tile looked for (none: E)
+  auto scan = [&](int t) -> int {  // returns the number of tiles
+    int top = 0, first = 0;
+#pragma unroll 1
+    for (int e0 = 0; e0 < E; e0 += 64) {
+      int v = 0;
+      if (e0 + lane < E) v = clamp_off(prm.offsets[e0 + lane + 1], 0);
+      v = wave_scan_max(v);
+      const int end = v > top ? v : top;
+      const int before = __shfl_up(end, 1);
+      const int beg = lane == 0 ? top : before;
+      const int n = ((end - beg + kBM - 1) / kBM) * prm.n_tiles;
+      const int run = wave_scan_sum(n);
+      const int ts = first + run - n;
+      const uint64_t hit = __ballot(t >= ts && t < ts + n);
+      if (hit) {
+        const int l = __builtin_ctzll(hit);
+        e_w = e0 + l;
+        ob = __builtin_amdgcn_readlane(beg, l);
+        oe = __builtin_amdgcn_readlane(end, l);
+        ts_w = __builtin_amdgcn_readlane(ts, l);
+        nt_w = __builtin_amdgcn_readlane(n, l);
+      }
+      top = __builtin_amdgcn_readlane(end, 63);
+      first += __builtin_amdgcn_readlane(run, 63);
+    }
+    return first;
+  };
+  const int total = scan(TAIL ? -1 : logical);
   const int nk = prm.K / kWBK;
 
-  // Split-K tail. All tiles are counted first; when the last round would leave at
-  // least half the workgroups idle, its `rem` tiles are cut into `split` K chunks, one
-  // per workgroup after the data-parallel rounds, each writing a float32 partial tile
-  // for run_tail_reduce to sum.
-  int total = 0;
-  {
-    int prev = 0;
-    for (int x = 0; x < E; ++x) {
-      const int en = clamp_off(load_const(prm.offsets, x + 1), prev);
-      total += ((en - prev + kBM - 1) / kBM) * prm.n_tiles;
-      prev = en;
-    }
-  }
+  // Split-K tail. When the last round would leave at least half the workgroups idle, its
+  // `rem` tiles are cut into `split` K chunks, one per workgroup after the data-parallel
+  // rounds, each writing a float32 partial tile for run_tail_reduce to sum.
   const int rem = total % nwg;
   int split = 0;
   if (prm.tail_cap > 0 && rem > 0 && rem * 2 <= nwg) {
@@ -140,6 +156,8 @@ void grouped_gemm_fwd_kernel(const Params prm) {
   const int k0 = TAIL ? (int)((int64_t)nk * (unit % split) / split) : 0;
   const int k1 = TAIL ? (int)((int64_t)nk * (unit % split + 1) / split) : nk;
   const int nkl = k1 - k0;
+
+  if (TAIL) scan(t_first);
 
   for (int t = t_first; t < t_end; t += nwg) {
     // ---------------- tile decode ----------------
