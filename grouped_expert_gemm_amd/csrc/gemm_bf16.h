@@ -49,7 +49,8 @@ struct Params {
   float* tail;
   int32_t* tail_meta;
   int tail_cap;
-  int spread;    // with a tail: one workgroup per CU also where there are fewer tiles, so that those are split
+  int spread;    // 1, with a tail: one workgroup per CU also where there are fewer tiles, so that those are
+                 // split; 2 (set by the launch): so few that all are tail tiles, which the tail launch lists
   uint8_t* z8;   // E4M3 codes of the gate_up output [R, 2I] (SWIGLU_MX8: out, DSWIGLU_MX8: in)
   uint8_t* z8s;  // ... and its E8M0 scales [R, 2I / 32]
   bf16_t* hout;  // DSWIGLU_MX8: h [R, I]
@@ -63,6 +64,12 @@ inline size_t tail_ws_bytes(int units) { return kTailMetaSpace + (size_t)units *
 // workgroups of a launch over at most max_tiles tiles
 inline int64_t grid_size(const Params& p, int64_t max_tiles, int cus) {
   return (p.spread && p.tail_cap > 0) || max_tiles > cus ? cus : max_tiles;
+}
+
+// whether a spread launch's tiles are all tail tiles, whatever the offsets: at most half a round of them,
+// cut into two chunks or more
+inline bool all_tail(const Params& p, int64_t max_tiles, int cus) {
+  return p.spread && p.tail_cap >= cus && max_tiles * 2 <= cus && p.K >= 128;
 }
 
 moe_status run(const Params& p, int pl, int ql, int g, int ep, int64_t max_tiles, hipStream_t s,

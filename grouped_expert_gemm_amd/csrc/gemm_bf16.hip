@@ -116,7 +116,7 @@ void grouped_gemm_kernel(const Params prm) {
   }
   const int dp_total = split ? total - rem : total;
   const int units = split ? rem * split : 0;
-  if (kCanSplit && !TAIL && prm.tail_meta && blockIdx.x == 0 && tid == 0) {
+  if (kCanSplit && (TAIL ? prm.spread == 2 : prm.tail_meta != nullptr) && blockIdx.x == 0 && tid == 0) {
     prm.tail_meta[0] = split ? rem : 0;
     prm.tail_meta[1] = split;
     prm.tail_meta[2] = dp_total;
@@ -901,17 +901,24 @@ void grouped_gemm_kernel(const Params prm) {
 template <int PL, int QL, int G, int EP>
 static moe_status launch(const Params& p, int64_t max_tiles, hipStream_t s, const char* what) {
   if (max_tiles <= 0) return MOE_OK;
-  const int64_t grid = grid_size(p, max_tiles, num_cus());
-  hipLaunchKernelGGL((grouped_gemm_kernel<PL, QL, G, EP, false>), dim3((unsigned)grid), dim3(256), 0, s, p);
-  moe_status st = check_launch(what);
-  if constexpr (G == GROUP_M && EP == EPI_STORE) {
+  const int cus = num_cus();
+  const int64_t grid = grid_size(p, max_tiles, cus);
+  Params q = p;
+  if (G == GROUP_M && EP == EPI_STORE && all_tail(p, max_tiles, cus)) {
+    q.spread = 2;
+  } else {
+    hipLaunchKernelGGL((grouped_gemm_kernel<PL, QL, G, EP, false>), dim3((unsigned)grid), dim3(256), 0, s, p);
+    const moe_status st = check_launch(what);
     if (st != MOE_OK || p.tail_cap <= 0) return st;
+  }
+  if constexpr (G == GROUP_M && EP == EPI_STORE) {
     if (!p.tail || !p.tail_meta) return fail(MOE_ERR_INVALID_ARG, std::string(what) + ": split-K tail area missing");
-    hipLaunchKernelGGL((grouped_gemm_kernel<PL, QL, G, EP, true>), dim3((unsigned)grid), dim3(256), 0, s, p);
-    if ((st = check_launch(what)) != MOE_OK) return st;
+    hipLaunchKernelGGL((grouped_gemm_kernel<PL, QL, G, EP, true>), dim3((unsigned)grid), dim3(256), 0, s, q);
+    const moe_status st = check_launch(what);
+    if (st != MOE_OK) return st;
     return run_tail_reduce(p, EP, max_tiles, s, what);
   }
-  return st;
+  return MOE_OK;
 }
 
 moe_status run(const Params& p, int pl, int ql, int g, int ep, int64_t max_tiles, hipStream_t s,

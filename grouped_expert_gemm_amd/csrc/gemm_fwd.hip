@@ -125,7 +125,7 @@ void grouped_gemm_fwd_kernel(const Params prm) {
   }
   const int dp_total = split ? total - rem : total;
   const int units = split ? rem * split : 0;
-  if (!TAIL && prm.tail_meta && blockIdx.x == 0 && tid == 0) {
+  if ((TAIL ? prm.spread == 2 : prm.tail_meta != nullptr) && blockIdx.x == 0 && tid == 0) {
     prm.tail_meta[0] = split ? rem : 0;
     prm.tail_meta[1] = split;
     prm.tail_meta[2] = dp_total;
@@ -596,11 +596,17 @@ __global__ __launch_bounds__(256) void tail_reduce_kernel(const Params prm) {
 template <int EP>
 static moe_status launch_fwd(const Params& p, int64_t max_tiles, hipStream_t s, const char* what) {
   if (max_tiles <= 0) return MOE_OK;
-  const int64_t grid = grid_size(p, max_tiles, num_cus());
-  hipLaunchKernelGGL((grouped_gemm_fwd_kernel<EP, false>), dim3((unsigned)grid), dim3(256), 0, s, p);
-  moe_status st = check_launch(what);
-  if (st != MOE_OK || p.tail_cap <= 0) return st;
-  hipLaunchKernelGGL((grouped_gemm_fwd_kernel<EP, true>), dim3((unsigned)grid), dim3(256), 0, s, p);
+  const int cus = num_cus();
+  const int64_t grid = grid_size(p, max_tiles, cus);
+  Params q = p;
+  if (all_tail(p, max_tiles, cus)) {
+    q.spread = 2;
+  } else {
+    hipLaunchKernelGGL((grouped_gemm_fwd_kernel<EP, false>), dim3((unsigned)grid), dim3(256), 0, s, p);
+    const moe_status st = check_launch(what);
+    if (st != MOE_OK || p.tail_cap <= 0) return st;
+  }
+  hipLaunchKernelGGL((grouped_gemm_fwd_kernel<EP, true>), dim3((unsigned)grid), dim3(256), 0, s, q);
   return check_launch(what);
 }
 

@@ -175,6 +175,11 @@ static TailArea tail_for(const TailArea& t, int K) {
   r.spread = true;
   return r;
 }
+// row tiles of E experts that share R rows, at most (an expert without rows has none)
+static int64_t most_row_tiles(int E, int64_t R, const TailArea& t) {
+  if (t.spread && R < E) E = (int)R;
+  return (t.spread ? R : R + gemm::kBM - 1) / gemm::kBM + E;
+}
 static void set_tail(gemm::Params& p, const TailArea& t) {
   p.tail = t.part;
   p.tail_meta = t.meta;
@@ -207,7 +212,7 @@ static moe_status bf16_gate_up(int E, int64_t R, int H, int I, const bf16_t* x, 
   p.E = E;
   p.I = I;
   p.n_tiles = I / 128;
-  const int64_t mtiles = (R + gemm::kBM - 1) / gemm::kBM + E;
+  const int64_t mtiles = most_row_tiles(E, R, tail);
   return gemm::run(p, gemm::KCONTIG, gemm::KCONTIG, gemm::GROUP_M, z8 ? gemm::EPI_SWIGLU_MX8 : gemm::EPI_SWIGLU,
                    mtiles * p.n_tiles, s, "grouped gate_up + ScaledSwiGLU");
 }
@@ -230,7 +235,7 @@ static moe_status bf16_linear(int E, int64_t R, int K, int N, const bf16_t* x, c
   q.K = K;
   q.E = E;
   q.n_tiles = N / gemm::kBN;
-  const int64_t mtiles = (R + gemm::kBM - 1) / gemm::kBM + E;
+  const int64_t mtiles = most_row_tiles(E, R, tail);
   return gemm::run(q, gemm::KCONTIG, gemm::KCONTIG, gemm::GROUP_M, gemm::EPI_STORE, mtiles * q.n_tiles, s,
                    "grouped linear");
 }
@@ -291,7 +296,7 @@ static moe_status bf16_gate_up_dgrad(const moe_mlp_desc& d, int64_t R, const bf1
   q.I = d.I;
   q.n_tiles = d.H / gemm::kBN;
   set_tail(q, tail);
-  const int64_t mtiles = (R + gemm::kBM - 1) / gemm::kBM + d.E;
+  const int64_t mtiles = most_row_tiles(d.E, R, tail);
   return gemm::run(q, gemm::MNCONTIG, gemm::KCONTIG, gemm::GROUP_M, gemm::EPI_STORE, mtiles * q.n_tiles, s,
                    "moe_grouped_mlp_bwd(gate_up dgrad)");
 }
