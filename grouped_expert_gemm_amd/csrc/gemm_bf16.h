@@ -24,6 +24,8 @@ enum {
   EPI_DSWIGLU_MX8 = 4  // DSWIGLU from a gate_up output in MXFP8, which also writes h
 };
 constexpr bool is_swiglu(int ep) { return ep == EPI_SWIGLU || ep == EPI_SWIGLU_MX8; }
+// epilogues of the general kernel (rows grouped by expert) whose last tiles may be split along K
+constexpr bool can_split(int ep) { return ep == EPI_STORE || ep == EPI_DSWIGLU_MX8; }
 
 struct Params {
   // GROUP_M: per-expert P operand (weights). GROUP_K: per-expert output C.

@@ -47,7 +47,7 @@
 namespace moe {
 namespace gemm {
 
-// TAIL (GROUP_M, EPI_STORE only): one K chunk of a split-K tail tile per workgroup,
+// TAIL (GROUP_M, can_split only): one K chunk of a split-K tail tile per workgroup,
 // written as a float32 partial tile (see the forward kernel); launched after the
 // TAIL = false kernel, which skips those tiles.
 template <int PL, int QL, int G, int EP, bool TAIL>
@@ -102,8 +102,8 @@ void grouped_gemm_kernel(const Params prm) {
   const int nwg = gridDim.x;
   const int logical = (nwg % 8 == 0) ? (blockIdx.x % 8) * (nwg / 8) + blockIdx.x / 8 : blockIdx.x;
 
-  // split-K tail (GROUP_M, EPI_STORE): the same rule as the forward kernel's
-  constexpr bool kCanSplit = G == GROUP_M && EP == EPI_STORE;
+  // split-K tail (GROUP_M, can_split): the same rule as the forward kernel's
+  constexpr bool kCanSplit = G == GROUP_M && can_split(EP);
   const int nk_all = (G == GROUP_M) ? prm.K / kBK : 0;
   const int rem = total % nwg;
   int split = 0;
@@ -617,7 +617,7 @@ void grouped_gemm_kernel(const Params prm) {
       }
       continue;
     }
-    if constexpr (EP == EPI_DSWIGLU_MX8) {
+    if constexpr (EP == EPI_DSWIGLU_MX8 && !TAIL) {
       // dSwiGLU from z in MXFP8, with h computed again: three bf16 tiles (dG, dU, h) leave where
       // one byte an element and half came in, so z's codes go straight to registers and LDS
       // carries the results. Eight passes: pass j takes the accumulator rows of sub-tile sm =
@@ -904,16 +904,17 @@ static moe_status launch(const Params& p, int64_t max_tiles, hipStream_t s, cons
   const int cus = num_cus();
   const int64_t grid = grid_size(p, max_tiles, cus);
   Params q = p;
-  if (G == GROUP_M && EP == EPI_STORE && all_tail(p, max_tiles, cus)) {
+  if (G == GROUP_M && can_split(EP) && all_tail(p, max_tiles, cus)) {
     q.spread = 2;
   } else {
     hipLaunchKernelGGL((grouped_gemm_kernel<PL, QL, G, EP, false>), dim3((unsigned)grid), dim3(256), 0, s, p);
     const moe_status st = check_launch(what);
     if (st != MOE_OK || p.tail_cap <= 0) return st;
   }
-  if constexpr (G == GROUP_M && EP == EPI_STORE) {
+  if constexpr (G == GROUP_M && can_split(EP)) {
     if (!p.tail || !p.tail_meta) return fail(MOE_ERR_INVALID_ARG, std::string(what) + ": split-K tail area missing");
-    hipLaunchKernelGGL((grouped_gemm_kernel<PL, QL, G, EP, true>), dim3((unsigned)grid), dim3(256), 0, s, q);
+    // (a partial tile does not depend on what is done with the sum)
+    hipLaunchKernelGGL((grouped_gemm_kernel<PL, QL, G, EPI_STORE, true>), dim3((unsigned)grid), dim3(256), 0, s, q);
     const moe_status st = check_launch(what);
     if (st != MOE_OK) return st;
     return run_tail_reduce(p, EP, max_tiles, s, what);

@@ -561,7 +561,31 @@ __global__ __launch_bounds__(256) void tail_reduce_kernel(const Params prm) {
     }
     return a;
   };
-  if constexpr (EP == EPI_STORE) {
+  if constexpr (EP == EPI_DSWIGLU_MX8) {  // a wavefront holds a row of the tile: 4 columns of I a lane
+    const float4 dh4 = sum4(c);
+    const float dh[4] = {dh4.x, dh4.y, dh4.z, dh4.w};
+    const int64_t I = prm.I, col = (int64_t)nt * kBN + c, row = mg * 2 * I;
+    float g[4], u[4], dg[4], du[4], h[4];
+    mx8::unpack4(*reinterpret_cast<const uint32_t*>(prm.z8 + row + col), mx8::scale_value(prm.z8s[(row + col) / 32]), g);
+    mx8::unpack4(*reinterpret_cast<const uint32_t*>(prm.z8 + row + I + col),
+                 mx8::scale_value(prm.z8s[(row + I + col) / 32]), u);
+    const float p = prm.prob[mg];
+    float dp = 0.f;
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {  // as in the general kernel's epilogue
+      const float sg = sigmoid_f(g[v]), sl = g[v] * sg, q = dh[v] * u[v];
+      dp = __builtin_fmaf(q, sl, dp);
+      dg[v] = (p * q) * __builtin_fmaf(-sl, sg, sg + sl);
+      du[v] = (p * dh[v]) * sl;
+      h[v] = sl * u[v] * p;
+    }
+    *reinterpret_cast<uint2*>(prm.c + row + col) = make_uint2(pack_bf16x2(dg[0], dg[1]), pack_bf16x2(dg[2], dg[3]));
+    *reinterpret_cast<uint2*>(prm.c + row + I + col) = make_uint2(pack_bf16x2(du[0], du[1]), pack_bf16x2(du[2], du[3]));
+    *reinterpret_cast<uint2*>(prm.hout + mg * I + col) = make_uint2(pack_bf16x2(h[0], h[1]), pack_bf16x2(h[2], h[3]));
+    dp = lanes_sum<64>(dp);
+    if ((threadIdx.x & 63) < 2)  // the tile's two partial sums of the row
+      prm.part[(int64_t)(nt * 2 + (threadIdx.x & 63)) * prm.R + mg] = (threadIdx.x & 63) == 0 ? dp : 0.f;
+  } else if constexpr (EP == EPI_STORE) {
     const float4 a = sum4(c);
     *reinterpret_cast<uint2*>(prm.c + mg * prm.c_ld + (int64_t)nt * kBN + c) =
         make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
@@ -632,6 +656,8 @@ moe_status run_tail_reduce(const Params& p, int ep, int64_t max_tiles, hipStream
     hipLaunchKernelGGL((tail_reduce_kernel<EPI_SWIGLU>), dim3((unsigned)(max_tail * (kBM / 8))), dim3(256), 0, s, p);
   } else if (ep == EPI_SWIGLU_MX8) {
     hipLaunchKernelGGL((tail_reduce_kernel<EPI_SWIGLU_MX8>), dim3((unsigned)(max_tail * (kBM / 8))), dim3(256), 0, s, p);
+  } else if (ep == EPI_DSWIGLU_MX8) {
+    hipLaunchKernelGGL((tail_reduce_kernel<EPI_DSWIGLU_MX8>), dim3((unsigned)(max_tail * (kBM / 4))), dim3(256), 0, s, p);
   } else {
     hipLaunchKernelGGL((tail_reduce_kernel<EPI_STORE>), dim3((unsigned)(max_tail * (kBM / 4))), dim3(256), 0, s, p);
   }

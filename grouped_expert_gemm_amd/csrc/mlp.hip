@@ -246,7 +246,8 @@ static moe_status bf16_linear(int E, int64_t R, int K, int N, const bf16_t* x, c
 static moe_status bf16_down_dgrad(const moe_mlp_desc& d, int64_t R, const bf16_t* dy, const PtrTab& w2,
                                   const int32_t* offsets, const float* prob, const bf16_t* z, bf16_t* dz, float* part,
                                   float* dprob, hipStream_t s, const uint8_t* z8 = nullptr,
-                                  const uint8_t* z8s = nullptr, bf16_t* h = nullptr, const int32_t* end = nullptr) {
+                                  const uint8_t* z8s = nullptr, bf16_t* h = nullptr, const int32_t* end = nullptr,
+                                  const TailArea& tail = TailArea()) {
   gemm::Params p;
   std::memset(&p, 0, sizeof(p));
   std::memcpy(p.tab, w2.p, sizeof(p.tab));
@@ -268,7 +269,8 @@ static moe_status bf16_down_dgrad(const moe_mlp_desc& d, int64_t R, const bf16_t
   p.E = d.E;
   p.I = d.I;
   p.n_tiles = d.I / gemm::kBN;
-  const int64_t mtiles = (R + gemm::kBM - 1) / gemm::kBM + d.E;
+  set_tail(p, tail);
+  const int64_t mtiles = most_row_tiles(d.E, R, tail);
   moe_status st = gemm::run(p, gemm::MNCONTIG, gemm::KCONTIG, gemm::GROUP_M, z ? gemm::EPI_DSWIGLU : gemm::EPI_DSWIGLU_MX8,
                             mtiles * p.n_tiles, s, "moe_grouped_mlp_bwd(down dgrad)");
   if (st != MOE_OK) return st;
@@ -621,7 +623,7 @@ extern "C" moe_status moe_grouped_mlp_bwd_ckpt8(const moe_mlp_desc* desc, int64_
   const int32_t* end = offsets + d.E;
   if (R > 0) {
     st = bf16_down_dgrad(d, R, (const bf16_t*)dy_perm, w2, offsets, prob_perm, nullptr, dz, part, dprob_perm, s, z_codes,
-                         z_scales, rows, end);
+                         z_scales, rows, end, tail_for(tail, d.H));
     if (st != MOE_OK) return st;
     if ((st = bf16_gate_up_dgrad(d, R, dz, w1, offsets, (bf16_t*)dx_perm, tail_for(tail, 2 * d.I), s)) != MOE_OK) return st;
   }
