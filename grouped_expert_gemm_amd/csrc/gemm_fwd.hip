@@ -352,20 +352,23 @@ void grouped_gemm_fwd_kernel(const Params prm) {
     lds_barrier();
 
     // ---------------- epilogue ----------------
-    if constexpr (TAIL) {  // K chunk of a tail tile: the float32 partial, all 256 rows, row-major
+    if constexpr (TAIL) {  // K chunk of a tail tile: the float32 partial of the expert's rows, row-major
       float* part = prm.tail + (int64_t)unit * (kBM * kBN);
 #pragma unroll
-      for (int sm = 0; sm < 4; ++sm)
+      for (int sm = 0; sm < 4; ++sm) {
+        const int r = wm * 128 + sm * 32 + l32;
+        if (r < row_end - tile_row) {
 #pragma unroll
-        for (int sn = 0; sn < 4; ++sn)
+          for (int sn = 0; sn < 4; ++sn)
 #pragma unroll
-          for (int i4 = 0; i4 < 4; ++i4) {
-            const int r = wm * 128 + sm * 32 + l32;
-            const int c = sub_n(sn, wn) + i4 * 8 + lhi * 4;
-            *reinterpret_cast<float4*>(part + r * kBN + c) =
-                make_float4(acc[sn][sm][i4 * 4 + 0], acc[sn][sm][i4 * 4 + 1], acc[sn][sm][i4 * 4 + 2],
-                            acc[sn][sm][i4 * 4 + 3]);
-          }
+            for (int i4 = 0; i4 < 4; ++i4) {
+              const int c = sub_n(sn, wn) + i4 * 8 + lhi * 4;
+              *reinterpret_cast<float4*>(part + r * kBN + c) =
+                  make_float4(acc[sn][sm][i4 * 4 + 0], acc[sn][sm][i4 * 4 + 1], acc[sn][sm][i4 * 4 + 2],
+                              acc[sn][sm][i4 * 4 + 3]);
+            }
+        }
+      }
       if (unit % split == 0 && tid == 0) {
         int32_t* m = prm.tail_meta + 4 + 4 * (unit / split);
         m[0] = tile_row;

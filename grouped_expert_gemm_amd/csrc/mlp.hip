@@ -166,19 +166,22 @@ static TailArea tail_area(uint8_t* base) {
   t.cap = num_cus();
   return t;
 }
-// The 8-bit checkpoint calls' tails: a product of K <= 512 is not split (the two launches of a tail
-// take about what its chunks save: one tile of 256 columns, K = 512, 20.3 us split and 15.9 not, K = 1024
-// 24.1 and 25.0), a longer one also where its tiles are fewer than the CUs (16 tiles of K = 4096: 82 us
-// with one workgroup a tile).
-static TailArea tail_for(const TailArea& t, int K) {
-  TailArea r = K > 512 ? t : TailArea();
-  r.spread = true;
-  return r;
-}
 // row tiles of E experts that share R rows, at most (an expert without rows has none)
 static int64_t most_row_tiles(int E, int64_t R, const TailArea& t) {
   if (t.spread && R < E) E = (int)R;
   return (t.spread ? R : R + gemm::kBM - 1) / gemm::kBM + E;
+}
+// The tail of a product of R rows by n_tiles column tiles in the 8-bit checkpoint calls: tiles
+// fewer than the CUs are cut along K as well (16 tiles of K = 4096: 82 us with one workgroup a tile),
+// but not for K <= 512 (one tile of 256 columns, K = 512: 20.3 us split and 15.9 not, K = 1024 24.1
+// and 25.0) unless its epilogue is long and no launch of whole tiles has to come first: then the join,
+// which spreads the epilogue over the card, pays for itself.
+static TailArea tail_for(const TailArea& t, int E, int64_t R, int K, int n_tiles, bool long_epilogue) {
+  TailArea r = t;
+  r.spread = true;
+  if (K <= 512 && !(long_epilogue && most_row_tiles(E, R, r) * n_tiles * 2 <= r.cap))
+    r.cap = 0, r.part = nullptr, r.meta = nullptr;
+  return r;
 }
 static void set_tail(gemm::Params& p, const TailArea& t) {
   p.tail = t.part;
@@ -568,9 +571,10 @@ extern "C" moe_status moe_grouped_mlp_fwd_ckpt8(const moe_mlp_desc* desc, int64_
   bf16_t* h = (bf16_t*)workspace;
   const TailArea tail = tail_area((uint8_t*)workspace + a256((size_t)R * d.I * 2));
   st = bf16_gate_up(d.E, R, d.H, d.I, (const bf16_t*)x_perm, make_tab(w_gate_up, d.E), offsets, prob_perm, h, nullptr, s,
-                    tail_for(tail, d.H), z_codes, z_scales);
+                    tail_for(tail, d.E, R, d.H, d.I / 128, true), z_codes, z_scales);
   if (st != MOE_OK) return st;
-  return bf16_linear(d.E, R, d.I, d.H, h, make_tab(w_down, d.E), offsets, (bf16_t*)y_perm, s, tail_for(tail, d.I));
+  return bf16_linear(d.E, R, d.I, d.H, h, make_tab(w_down, d.E), offsets, (bf16_t*)y_perm, s,
+                     tail_for(tail, d.E, R, d.I, d.H / gemm::kBN, false));
 }
 
 extern "C" moe_status moe_grouped_mlp_bwd_ckpt8(const moe_mlp_desc* desc, int64_t R, const void* dy_perm, const void* x,
@@ -623,9 +627,10 @@ extern "C" moe_status moe_grouped_mlp_bwd_ckpt8(const moe_mlp_desc* desc, int64_
   const int32_t* end = offsets + d.E;
   if (R > 0) {
     st = bf16_down_dgrad(d, R, (const bf16_t*)dy_perm, w2, offsets, prob_perm, nullptr, dz, part, dprob_perm, s, z_codes,
-                         z_scales, rows, end, tail_for(tail, d.H));
+                         z_scales, rows, end, tail_for(tail, d.E, R, d.H, d.I / gemm::kBN, true));
     if (st != MOE_OK) return st;
-    if ((st = bf16_gate_up_dgrad(d, R, dz, w1, offsets, (bf16_t*)dx_perm, tail_for(tail, 2 * d.I), s)) != MOE_OK) return st;
+    st = bf16_gate_up_dgrad(d, R, dz, w1, offsets, (bf16_t*)dx_perm, tail_for(tail, d.E, R, 2 * d.I, d.H / gemm::kBN, false), s);
+    if (st != MOE_OK) return st;
   }
   st = bf16_wgrad(d, R, (const bf16_t*)dy_perm, d.H, rows, d.I, dw2, offsets, s, "moe_grouped_mlp_bwd_ckpt8(down wgrad)");
   if (st != MOE_OK) return st;
