@@ -82,7 +82,10 @@ void grouped_gemm_kernel(const Params prm) {
       top = __builtin_amdgcn_readlane(v, 63);
       if (e <= E) s_off[e] = e == 0 ? 0 : v;
     }
-    if constexpr (G == GROUP_M) {
+  }
+  __syncthreads();
+  if constexpr (G == GROUP_M) {
+    if (wave == 0) {
       int first = 0;
       for (int e0 = 0; e0 < E; e0 += 64) {
         const int e = e0 + lane;
@@ -93,8 +96,8 @@ void grouped_gemm_kernel(const Params prm) {
       }
       if (lane == 0) s_tstart[E] = first;
     }
+    __syncthreads();
   }
-  __syncthreads();
   int total;
   if constexpr (G == GROUP_M) total = s_tstart[E];
   else total = E * (prm.M / kBM) * prm.n_tiles;
