@@ -632,6 +632,10 @@ void grouped_gemm_kernel(const Params prm) {
       // (64 rows of 256 bytes, chunk c of row r at c ^ (r & 15)), so one barrier a pass stands
       // between writing a buffer and its whole-row stores, and the next but one writes it again.
       // Rows past the expert read as zeros and are not stored (the descriptors' record counts).
+      // 16384 tokens x 8 rows, 128 experts of 2048 x 768: 571 us, 0.72 PFLOP/s; 8192 rows, 8 experts
+      // of 4096 x 14336: 1050 us, 0.92 PFLOP/s (MFMA busy 40 and 51%). A tile's epilogue runs beside
+      // no MFMA and is the sum of its parts: the large case without z's loads takes 94 us less, without
+      // the stores 79, without exponential and reciprocal 10. Workgroups started apart in time: no gain.
       int ln = lane_number(), wv = wave_u;
       asm volatile("" : "+v"(ln));
       asm volatile("" : "+s"(wv));
