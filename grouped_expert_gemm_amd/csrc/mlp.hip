@@ -173,9 +173,10 @@ static int64_t most_row_tiles(int E, int64_t R, const TailArea& t) {
 }
 // The tail of a product of R rows by n_tiles column tiles in the 8-bit checkpoint calls: tiles
 // fewer than the CUs are cut along K as well (16 tiles of K = 4096: 82 us with one workgroup a tile),
-// but not for K <= 512 (one tile of 256 columns, K = 512: 20.3 us split and 15.9 not, K = 1024 24.1
-// and 25.0) unless its epilogue is long and no launch of whole tiles has to come first: then the join,
-// which spreads the epilogue over the card, pays for itself.
+// but not for K <= 512 (forwards whose down product has K = 512: 12 to 129 rows 32 to 43 us, at most 2 less
+// when it is cut, 600 rows 53.6 and 62.0, 1500 rows 52.6 and 64.8) unless its epilogue is long and no
+// launch of whole tiles has to come first: then the join, which spreads the epilogue over the card, pays
+// for itself.
 static TailArea tail_for(const TailArea& t, int E, int64_t R, int K, int n_tiles, bool long_epilogue) {
   TailArea r = t;
   r.spread = true;
