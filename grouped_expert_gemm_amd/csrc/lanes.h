@@ -63,6 +63,16 @@ __device__ __forceinline__ double wave_sum(double v) {
   return v;
 }
 
+// The end of the last expert's rows as the grouped GEMMs, which take the offsets as their running
+// maximum inside [0, R], have it: the largest of offsets[0..E], clamped. Every lane active.
+__device__ __forceinline__ int64_t routed_end(const int32_t* __restrict__ offsets, int E, int64_t R) {
+  const int lane = (int)__builtin_amdgcn_mbcnt_hi(~0u, __builtin_amdgcn_mbcnt_lo(~0u, 0u));
+  int top = 0;
+  for (int e = lane; e <= E; e += 64) top = max(top, offsets[e]);
+  top = (int)lanes_reduce<64>((uint32_t)top, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+  return top < R ? top : R;
+}
+
 template <int L>
 __device__ __forceinline__ float lanes_max(float v) {
   return __uint_as_float(lanes_reduce<L>(__float_as_uint(v), [](uint32_t a, uint32_t b) {

@@ -10,6 +10,7 @@
 #include "gemm_f32.h"
 #include "gemm_mx.h"
 #include "internal.h"
+#include "lanes.h"
 #include "mxfp4.h"
 #include "mxfp8.h"
 
@@ -132,10 +133,11 @@ static PtrTab make_tab(const void* const* t, int E) {
 // dprob[r] = sum over j of part[j][r] in a fixed order (deterministic): 8 threads per
 // row each add the partials j = q, q + 8, ... in increasing j, then the 8 sums are added
 // in q order. 32 rows per workgroup, consecutive threads on consecutive rows.
-// rows from *end on (end != NULL) are not written.
+// With offsets, rows past the last expert's are not written.
 __global__ __launch_bounds__(256) void reduce_partials(const float* __restrict__ part, int nparts, int64_t R,
-                                                       float* __restrict__ out, const int32_t* __restrict__ end) {
+                                                       float* __restrict__ out, const int32_t* __restrict__ offsets, int E) {
   __shared__ float sums[8][32];
+  const int64_t end = offsets ? routed_end(offsets, E, R) : R;
   const int rl = threadIdx.x & 31, q = threadIdx.x >> 5;
   const int64_t r = (int64_t)blockIdx.x * 32 + rl;
   float s = 0.f;
@@ -147,7 +149,7 @@ __global__ __launch_bounds__(256) void reduce_partials(const float* __restrict__
     float t = sums[0][rl];
 #pragma unroll
     for (int i = 1; i < 8; ++i) t += sums[i][rl];
-    if (!end || r < *end) out[r] = t;
+    if (r < end) out[r] = t;
   }
 }
 
@@ -246,11 +248,11 @@ static moe_status bf16_linear(int E, int64_t R, int K, int N, const bf16_t* x, c
 
 // The products of the bf16 backward. dH = dY W2_e (W2_e is [H][I]: K rows, I contiguous) with the
 // dSwiGLU epilogue: dz [R, 2I] and dprob from z [R, 2I] in bf16, or (z NULL) from its MXFP8 codes
-// and scales, then with h [R, I] too and without the rows of dprob from *end on.
+// and scales, then with h [R, I] too and without dprob's rows past the last expert's.
 static moe_status bf16_down_dgrad(const moe_mlp_desc& d, int64_t R, const bf16_t* dy, const PtrTab& w2,
                                   const int32_t* offsets, const float* prob, const bf16_t* z, bf16_t* dz, float* part,
                                   float* dprob, hipStream_t s, const uint8_t* z8 = nullptr,
-                                  const uint8_t* z8s = nullptr, bf16_t* h = nullptr, const int32_t* end = nullptr,
+                                  const uint8_t* z8s = nullptr, bf16_t* h = nullptr,
                                   const TailArea& tail = TailArea()) {
   gemm::Params p;
   std::memset(&p, 0, sizeof(p));
@@ -279,7 +281,7 @@ static moe_status bf16_down_dgrad(const moe_mlp_desc& d, int64_t R, const bf16_t
                             mtiles * p.n_tiles, s, "moe_grouped_mlp_bwd(down dgrad)");
   if (st != MOE_OK) return st;
   hipLaunchKernelGGL(reduce_partials, dim3((unsigned)((R + 31) / 32)), dim3(256), 0, s, (const float*)part,
-                     2 * p.n_tiles, R, dprob, end);
+                     2 * p.n_tiles, R, dprob, z ? nullptr : offsets, d.E);
   return check_launch("moe_grouped_mlp_bwd(dprob)");
 }
 
@@ -625,10 +627,9 @@ extern "C" moe_status moe_grouped_mlp_bwd_ckpt8(const moe_mlp_desc* desc, int64_
   float* part = (float*)ws;
   ws += a256((size_t)2 * (d.I / 256) * R * 4);
   const TailArea tail = tail_area(ws);
-  const int32_t* end = offsets + d.E;
   if (R > 0) {
     st = bf16_down_dgrad(d, R, (const bf16_t*)dy_perm, w2, offsets, prob_perm, nullptr, dz, part, dprob_perm, s, z_codes,
-                         z_scales, rows, end, tail_for(tail, d.E, R, d.H, d.I / gemm::kBN, true));
+                         z_scales, rows, tail_for(tail, d.E, R, d.H, d.I / gemm::kBN, true));
     if (st != MOE_OK) return st;
     st = bf16_gate_up_dgrad(d, R, dz, w1, offsets, (bf16_t*)dx_perm, tail_for(tail, d.E, R, 2 * d.I, d.H / gemm::kBN, false), s);
     if (st != MOE_OK) return st;
@@ -638,7 +639,7 @@ extern "C" moe_status moe_grouped_mlp_bwd_ckpt8(const moe_mlp_desc* desc, int64_
   const bf16_t* xp = (const bf16_t*)x;
   if (kept8) {
     if (R > 0) {
-      st = mx8::launch_read((const uint8_t*)x, x_scale, T, d.H, src_token, R, end, true, rows, s);
+      st = mx8::launch_read((const uint8_t*)x, x_scale, T, d.H, src_token, R, offsets, d.E, true, rows, s);
       if (st != MOE_OK) return st;
     }
     xp = rows;

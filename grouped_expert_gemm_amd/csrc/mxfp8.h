@@ -51,11 +51,11 @@ __device__ __forceinline__ void unpack4(uint32_t w, float scale, float* v) {
 }
 
 // Reads of MXFP8 rows [src_rows, cols] as bf16 rows: out[r] = values of row src_row[r] (of row r
-// where src_row is NULL), for r < rows and, with limit, r < *limit (a device word, clamped to
-// [0, rows]). A row whose src_row is out of [0, src_rows) is left as it was, or zeros with
+// where src_row is NULL), for r < rows and, with offsets [E + 1], the rows of E experts alone
+// (routed_end). A row whose src_row is out of [0, src_rows) is left as it was, or zeros with
 // zero_missing. cols % 32 == 0, codes and out 16-byte aligned.
 moe_status launch_read(const uint8_t* codes, const uint8_t* scales, int64_t src_rows, int64_t cols,
-                       const int32_t* src_row, int64_t rows, const int32_t* limit, bool zero_missing, bf16_t* out,
+                       const int32_t* src_row, int64_t rows, const int32_t* offsets, int E, bool zero_missing, bf16_t* out,
                        hipStream_t s);
 
 }  // namespace mx8

@@ -8,6 +8,7 @@
 
 #include "common.h"
 #include "internal.h"
+#include "lanes.h"
 
 namespace moe {
 namespace mx8 {
@@ -17,10 +18,9 @@ constexpr int kItems = 4;  // loads of a thread in flight together
 template <bool GATHER>
 __global__ __launch_bounds__(256) void read_kernel(const uint4* __restrict__ codes, const uint8_t* __restrict__ scales,
                                                    int64_t src_rows, uint32_t row16, const int32_t* __restrict__ src_row,
-                                                   int64_t rows, const int32_t* __restrict__ limit,
+                                                   int64_t rows, const int32_t* __restrict__ offsets, int E,
                                                    bool zero_missing, uint4* __restrict__ out) {
-  int64_t n = rows;
-  if (limit) n = *limit < 0 ? 0 : *limit < rows ? *limit : rows;
+  const int64_t n = offsets ? routed_end(offsets, E, rows) : rows;
   const int64_t total = n * row16;
   const int64_t q0 = (int64_t)blockIdx.x * (256 * kItems) + threadIdx.x;
   int64_t at[kItems];
@@ -64,7 +64,7 @@ __global__ __launch_bounds__(256) void read_kernel(const uint4* __restrict__ cod
 }
 
 moe_status launch_read(const uint8_t* codes, const uint8_t* scales, int64_t src_rows, int64_t cols,
-                       const int32_t* src_row, int64_t rows, const int32_t* limit, bool zero_missing, bf16_t* out,
+                       const int32_t* src_row, int64_t rows, const int32_t* offsets, int E, bool zero_missing, bf16_t* out,
                        hipStream_t s) {
   const int64_t row16 = cols / 16;
   if (rows == 0 || cols == 0) return MOE_OK;
@@ -72,7 +72,7 @@ moe_status launch_read(const uint8_t* codes, const uint8_t* scales, int64_t src_
   if (grid > 0xFFFFFFFF / 256) return fail(MOE_ERR_UNSUPPORTED, "mxfp8_dequantize: more elements than one launch holds");
   const auto kernel = src_row ? read_kernel<true> : read_kernel<false>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(256), 0, s, (const uint4*)codes, scales, src_rows, (uint32_t)row16,
-                     src_row, rows, limit, zero_missing, (uint4*)out);
+                     src_row, rows, offsets, E, zero_missing, (uint4*)out);
   return check_launch("mxfp8_dequantize");
 }
 
@@ -94,5 +94,5 @@ extern "C" moe_status mxfp8_dequantize(const uint8_t* e4m3, const uint8_t* e8m0,
     return fail(MOE_ERR_INVALID_ARG, "mxfp8_dequantize: NULL pointer");
   if (!aligned(e4m3, 16) || !aligned(out_bf16, 16) || !aligned(src_row, 4))
     return fail(MOE_ERR_INVALID_ARG, "mxfp8_dequantize: codes and out must be 16-byte, src_row 4-byte aligned");
-  return mx8::launch_read(e4m3, e8m0, src_rows, cols, src_row, rows, nullptr, false, (bf16_t*)out_bf16, as_stream(stream));
+  return mx8::launch_read(e4m3, e8m0, src_rows, cols, src_row, rows, nullptr, 0, false, (bf16_t*)out_bf16, as_stream(stream));
 }
