@@ -712,7 +712,7 @@ void grouped_gemm_kernel(const Params prm) {
               const float sl = g[v] * sg;
               const float q = dh * u[v];
               dpart[sm] = __builtin_fmaf(q, sl, dpart[sm]);
-              dg[v] = (pr[sm] * q) * __builtin_fmaf(-sl, sg, sg + sl);
+              dg[v] = (pr[sm] * q) * silu_slope(sg, sl);
               du[v] = (pr[sm] * dh) * sl;
               h[v] = sl * u[v] * pr[sm];
             }

@@ -147,6 +147,9 @@ __device__ __forceinline__ void wait_vm_le(int n) {  // n: a multiple of 4 in [0
 __device__ __forceinline__ float silu_f(float g) { return g * __builtin_amdgcn_rcpf(1.f + __expf(-g)); }
 // sigmoid(g) = 1 / (1 + e^-g), the same way
 __device__ __forceinline__ float sigmoid_f(float g) { return __builtin_amdgcn_rcpf(1.f + __expf(-g)); }
+// d silu(g) / dg = sg + g sg (1 - sg) from sg = sigmoid(g) and sl = silu(g) = g sg. Where g is large, sg is
+// 1 and 1 - sg exactly 0, so the slope is 1; (sg + sl) - sl sg would lose the 1 beside g, from 2^24 on all of it.
+__device__ __forceinline__ float silu_slope(float sg, float sl) { return __builtin_fmaf(sl, 1.f - sg, sg); }
 
 
 }  // namespace gemm

@@ -602,7 +602,7 @@ __global__ __launch_bounds__(256) void tail_reduce_kernel(const Params prm) {
     for (int v = 0; v < 4; ++v) {  // as in the general kernel's epilogue
       const float sg = sigmoid_f(g[v]), sl = g[v] * sg, q = dh[v] * u[v];
       dp = __builtin_fmaf(q, sl, dp);
-      dg[v] = (p * q) * __builtin_fmaf(-sl, sg, sg + sl);
+      dg[v] = (p * q) * silu_slope(sg, sl);
       du[v] = (p * dh[v]) * sl;
       h[v] = sl * u[v] * p;
     }

@@ -2,7 +2,8 @@
 import pytest
 import torch
 
-from test_gpu_ckpt8 import Case
+from gpu_util import host
+from test_gpu_ckpt8 import Case, _backward_check
 
 pytestmark = pytest.mark.gpu
 
@@ -48,3 +49,20 @@ def test_offsets_that_decrease_are_read_as_their_running_maximum(moe, bad, good)
         for a, b, name in zip(*got, ("dx", "dw1", "dw2", "dprob")):
             assert torch.equal(a, b), name
             assert not bool(torch.isnan(a.float()).any()), name
+
+
+@pytest.mark.parametrize("counts", [[40, 0, 9], [1] * 129 + [5]])
+def test_slope_of_the_gate_at_any_magnitude(moe, counts):
+    """Gates from 2^-36 to 2^52 on both sides: silu' = sig + g sig (1 - sig) goes to 1 above (where float32's 1 beside
+    g vanishes from 2^24 on) and to 0 below. W1 is the identity, so that dx is dZ itself, each column apart. The
+    second case's tiles are too many to be split along K: the down gradient's own epilogue, else the join's."""
+    print(f"ckpt8 gates of any magnitude {len(counts)} experts", flush=True)
+    c = Case(counts, 512, 256, seed=51)
+    c.w1 = torch.eye(512, dtype=torch.bfloat16, device="cuda").repeat(c.E, 1, 1)
+    g = torch.Generator(device="cuda").manual_seed(52)
+    zc = torch.randint(0, 127, (c.R, 512), generator=g, device="cuda") + 128 * torch.randint(0, 2, (c.R, 512), generator=g, device="cuda")
+    zs = torch.randint(100, 171, (c.R, 16), generator=g, device="cuda")
+    zs[:, 8:] = torch.randint(118, 128, (c.R, 8), generator=g, device="cuda")
+    zc, zs = zc.to(torch.uint8), zs.to(torch.uint8)
+    got = moe.moe_grouped_mlp_bwd_ckpt8(c.dy, c.x, zc, zs, c.prob, c.w1, c.w2, c.offsets)
+    _backward_check(moe, c, zc, zs, got, host(c.x), "gates of any magnitude")
