@@ -550,7 +550,7 @@ void grouped_gemm_kernel(const Params prm) {
               float dg[4], du[4];
 #pragma unroll
               for (int v = 0; v < 4; ++v) {
-                // dG = p dh u sg (1 + g (1 - sg)) = p (dh u) (sg + sl - sl sg), dU = p dh sl,
+                // dG = p dh u sg (1 + g (1 - sg)) = p (dh u) (sg + sl (1 - sg)), dU = p dh sl,
                 // dprob += dh u sl, with sl = g sg
                 const float dh = acc[sn][sm][i4 * 4 + v];
                 const float gg = gv[v], u = uv[v];
@@ -558,7 +558,7 @@ void grouped_gemm_kernel(const Params prm) {
                 const float sl = gg * sg;
                 const float q = dh * u;
                 dpart[sm] = __builtin_fmaf(q, sl, dpart[sm]);
-                dg[v] = (pr[sm] * q) * __builtin_fmaf(-sl, sg, sg + sl);
+                dg[v] = (pr[sm] * q) * silu_slope(sg, sl);
                 du[v] = (pr[sm] * dh) * sl;
               }
               *reinterpret_cast<uint2*>(gP + off) = make_uint2(pack_bf16x2(dg[0], dg[1]), pack_bf16x2(dg[2], dg[3]));
