@@ -90,8 +90,7 @@ void grouped_gemm_fwd_kernel(const Params prm) {
       if (e0 + lane < E) v = clamp_off(prm.offsets[e0 + lane + 1], 0);
       v = wave_scan_max(v);
       const int end = v > top ? v : top;
-      const int before = __shfl_up(end, 1);
-      const int beg = lane == 0 ? top : before;
+      const int beg = lane_from<0x138>(end, top);  // the lane before (wave_shr 1), lane 0: top
       const int n = ((end - beg + kBM - 1) / kBM) * prm.n_tiles;
       const int run = wave_scan_sum(n);
       const int ts = first + run - n;
@@ -134,7 +133,10 @@ void grouped_gemm_fwd_kernel(const Params prm) {
   }
   if (TAIL && logical >= units) return;
 
-  const int l32 = lane & 31, lhi = lane >> 5;
+  // a lane number of their own: with the one that the scan used, the gate_up kernel reloads fragment
+  // addresses from scratch in its K loop (994 for 870 us, 131072 rows over 128 experts of 2048 x 768)
+  const int lf = lane_number();
+  const int l32 = lf & 31, lhi = lf >> 5;
   // fragment addresses: sub-tile rows start at multiples of 32, where swz8 depends on
   // the lane's row within the sub-tile only; k16 slice sl is logical chunk 2*sl + lhi
   const uint32_t fragP = (uint32_t)((wn * 64 + l32) * 128);
