@@ -462,8 +462,8 @@ def mxfp8_dequantize(codes: torch.Tensor, scales: torch.Tensor, src_row: torch.T
                      out: torch.Tensor | None = None) -> torch.Tensor:
     """MXFP8 codes [..., cols] and scales [..., cols/32] -> their values, bf16 [..., cols].
 
-    src_row int32 [rows] (codes 2-D): out[r] = the values of row src_row[r], bf16 [rows, cols]; rows of out
-    whose index is out of range are left as they were."""
+    src_row int32 [rows] (codes 2-D): out[r] = the values of row src_row[r], bf16 [rows, cols]; rows whose
+    index is out of range are zeros, or, where out is given, left as they were."""
     fn = "mxfp8_dequantize"
     _need(fn, codes, scales, src_row, out)
     shape = codes.shape
@@ -476,12 +476,14 @@ def mxfp8_dequantize(codes: torch.Tensor, scales: torch.Tensor, src_row: torch.T
         if len(shape) != 2 or src_row.dtype != torch.int32 or src_row.dim() != 1:
             raise ValueError(f"{fn}: src_row must be int32 [rows], with 2-D codes")
         shape = (src_row.shape[0], cols)
+    entry = fn
     if out is None:
         out = codes.new_empty(shape, dtype=torch.bfloat16)
+        entry = fn if src_row is None else "mxfp8_dequantize_gather"
     elif out.dtype != torch.bfloat16 or out.shape != shape:
         raise ValueError(f"{fn}: out must be bfloat16 [rows, cols]")
     rows = src_rows if src_row is None else shape[0]
-    _launch(fn, codes, _a(codes), _a(scales), src_rows, cols, _a(src_row), rows, _a(out))
+    _launch(entry, codes, _a(codes), _a(scales), src_rows, cols, _a(src_row), rows, _a(out))
     return out
 
 

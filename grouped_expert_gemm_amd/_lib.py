@@ -28,7 +28,7 @@ EXPORTS = (
     "moe_balance_loss", "moe_balance_loss_bwd",
     "moe_pre_norm", "moe_pre_norm_bwd", "moe_post_norm", "moe_post_norm_bwd",
     "mxfp4_quantize", "mxfp4_dequantize", "moe_grouped_linear_mxfp4", "moe_pointer_table",
-    "moe_add_norm_mxfp8", "mxfp8_dequantize", "moe_grouped_mlp_fwd_ckpt8", "moe_grouped_mlp_bwd_ckpt8",
+    "moe_add_norm_mxfp8", "mxfp8_dequantize", "mxfp8_dequantize_gather", "moe_grouped_mlp_fwd_ckpt8", "moe_grouped_mlp_bwd_ckpt8",
     "moe_workspace_size",
     "moe_status_str", "moe_last_error",
 )
@@ -97,6 +97,7 @@ def _declare(lib):
         "moe_pointer_table": [vp, i64, c_int, vp],
         "moe_add_norm_mxfp8": [vp, vp, c_int, vp, vp, c_int, i64, c_int, f32, vp, vp, vp, vp, vp, vp],
         "mxfp8_dequantize": [vp, vp, i64, i64, vp, i64, vp, vp],
+        "mxfp8_dequantize_gather": [vp, vp, i64, i64, vp, i64, vp, vp],
         "moe_grouped_mlp_fwd_ckpt8": [vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
         "moe_grouped_mlp_bwd_ckpt8": [vp, i64, vp, vp, vp, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
         "moe_workspace_size": [c_int, ctypes.POINTER(MlpDesc), i64, i64, c_int, c_int, ctypes.POINTER(sz)],

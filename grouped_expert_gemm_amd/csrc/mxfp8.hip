@@ -81,18 +81,28 @@ moe_status launch_read(const uint8_t* codes, const uint8_t* scales, int64_t src_
 
 using namespace moe;
 
+static moe_status read_rows(const char* fn, const uint8_t* e4m3, const uint8_t* e8m0, int64_t src_rows, int64_t cols,
+                            const int32_t* src_row, int64_t rows, bool zero_missing, void* out_bf16, void* stream) {
+  auto bad = [&](const char* what) { return fail(MOE_ERR_INVALID_ARG, std::string(fn) + ": " + what); };
+  if (src_rows < 0 || rows < 0 || cols < 0) return bad("negative size");
+  if (cols % 32 != 0) return bad("cols % 32 != 0");
+  if (!src_row && rows != src_rows) return bad("without src_row, rows and src_rows must be equal");
+  if (cols > 0x7FFFFFFF || rows > 0x7FFFFFFF || src_rows > 0x7FFFFFFF)
+    return fail(MOE_ERR_UNSUPPORTED, std::string(fn) + ": a size of 2^31 or more");
+  if (rows == 0 || cols == 0) return MOE_OK;
+  if (!out_bf16 || (zero_missing && !src_row) || (src_rows > 0 && (!e4m3 || !e8m0))) return bad("NULL pointer");
+  if (!aligned(e4m3, 16) || !aligned(out_bf16, 16) || !aligned(src_row, 4))
+    return bad("codes and out must be 16-byte, src_row 4-byte aligned");
+  return mx8::launch_read(e4m3, e8m0, src_rows, cols, src_row, rows, nullptr, 0, zero_missing, (bf16_t*)out_bf16,
+                          as_stream(stream));
+}
+
 extern "C" moe_status mxfp8_dequantize(const uint8_t* e4m3, const uint8_t* e8m0, int64_t src_rows, int64_t cols,
                                        const int32_t* src_row, int64_t rows, void* out_bf16, void* stream) {
-  if (src_rows < 0 || rows < 0 || cols < 0) return fail(MOE_ERR_INVALID_ARG, "mxfp8_dequantize: negative size");
-  if (cols % 32 != 0) return fail(MOE_ERR_INVALID_ARG, "mxfp8_dequantize: cols % 32 != 0");
-  if (!src_row && rows != src_rows)
-    return fail(MOE_ERR_INVALID_ARG, "mxfp8_dequantize: without src_row, rows and src_rows must be equal");
-  if (cols > 0x7FFFFFFF || rows > 0x7FFFFFFF || src_rows > 0x7FFFFFFF)
-    return fail(MOE_ERR_UNSUPPORTED, "mxfp8_dequantize: a size of 2^31 or more");
-  if (rows == 0 || cols == 0) return MOE_OK;
-  if (!out_bf16 || (src_rows > 0 && (!e4m3 || !e8m0)))
-    return fail(MOE_ERR_INVALID_ARG, "mxfp8_dequantize: NULL pointer");
-  if (!aligned(e4m3, 16) || !aligned(out_bf16, 16) || !aligned(src_row, 4))
-    return fail(MOE_ERR_INVALID_ARG, "mxfp8_dequantize: codes and out must be 16-byte, src_row 4-byte aligned");
-  return mx8::launch_read(e4m3, e8m0, src_rows, cols, src_row, rows, nullptr, 0, false, (bf16_t*)out_bf16, as_stream(stream));
+  return read_rows("mxfp8_dequantize", e4m3, e8m0, src_rows, cols, src_row, rows, false, out_bf16, stream);
+}
+
+extern "C" moe_status mxfp8_dequantize_gather(const uint8_t* e4m3, const uint8_t* e8m0, int64_t src_rows, int64_t cols,
+                                              const int32_t* src_row, int64_t rows, void* out_bf16, void* stream) {
+  return read_rows("mxfp8_dequantize_gather", e4m3, e8m0, src_rows, cols, src_row, rows, true, out_bf16, stream);
 }

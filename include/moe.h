@@ -361,6 +361,14 @@ moe_status mxfp8_dequantize(const uint8_t* e4m3, const uint8_t* e8m0, int64_t sr
                             const int32_t* src_row, int64_t rows, void* out_bf16, void* stream);
 
 /*
+ * mxfp8_dequantize by row into a tensor that holds nothing yet: a row whose index is out of
+ * [0, src_rows) becomes zeros, as moe_grouped_mlp_bwd_ckpt8 reads such a token, so that every row
+ * of out is written. src_row is required; the other arguments are mxfp8_dequantize's.
+ */
+moe_status mxfp8_dequantize_gather(const uint8_t* e4m3, const uint8_t* e8m0, int64_t src_rows, int64_t cols,
+                                   const int32_t* src_row, int64_t rows, void* out_bf16, void* stream);
+
+/*
  * Column-wise MXFP8 quantisation, expert by expert, along the token axis: the operand
  * layout of the weight-gradient GEMMs of an MXFP8 backward, whose reduction runs over
  * each expert's rows. Source: Challenge 2 (one scaling factor per 32 consecutive
