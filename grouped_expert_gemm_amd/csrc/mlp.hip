@@ -596,7 +596,8 @@ extern "C" moe_status moe_grouped_mlp_bwd_ckpt8(const moe_mlp_desc* desc, int64_
   const bool kept8 = d.act == MOE_MXFP8;
   if (!offsets || !aligned(offsets, 4)) return fail(MOE_ERR_INVALID_ARG, std::string(fn) + ": offsets NULL or misaligned");
   if (R > 0) {
-    if (!dy_perm || !x || !z_codes || !z_scales || !prob_perm || !dx_perm || !dprob_perm || (kept8 && !x_scale))
+    const bool has_x = x && (!kept8 || x_scale);
+    if (!dy_perm || !z_codes || !z_scales || !prob_perm || !dx_perm || !dprob_perm || (!has_x && (!kept8 || T > 0)))
       return fail(MOE_ERR_INVALID_ARG, std::string(fn) + ": NULL pointer");
     for (const void* p : {dy_perm, x, (const void*)z_codes, (const void*)dx_perm})
       if (!aligned(p, 16)) return fail(MOE_ERR_INVALID_ARG, std::string(fn) + ": misaligned tensor");

@@ -644,8 +644,8 @@ moe_status moe_grouped_mlp_fwd_ckpt8(const moe_mlp_desc* desc, int64_t R, const 
  *   desc: compute and wt MOE_BF16; act = MOE_MXFP8: x holds E4M3 codes [T, H] (16-byte aligned)
  *     with x_scale [T, H/32], one row a token, and src_token [R] (moe_permute's) names the row of
  *     each routed row, or src_token is NULL and T == R: the codes are in expert order. A token out
- *     of [0, T) is read as zeros. act = MOE_BF16: x is x_perm [R, H] (x_scale and src_token NULL, T
- *     ignored).
+ *     of [0, T) is read as zeros (x and x_scale may be NULL for T = 0). act = MOE_BF16: x is
+ *     x_perm [R, H] (x_scale and src_token NULL, T ignored).
  *   z_codes [R, 2I] (16-byte aligned), z_scales [R, 2I/32] (8-byte aligned): of
  *     moe_grouped_mlp_fwd_ckpt8
  * The other arguments are moe_grouped_mlp_bwd's. Rows from offsets[E] on of dx_perm and

@@ -66,3 +66,14 @@ def test_slope_of_the_gate_at_any_magnitude(moe, counts):
     zc, zs = zc.to(torch.uint8), zs.to(torch.uint8)
     got = moe.moe_grouped_mlp_bwd_ckpt8(c.dy, c.x, zc, zs, c.prob, c.w1, c.w2, c.offsets)
     _backward_check(moe, c, zc, zs, got, host(c.x), "gates of any magnitude")
+
+
+def test_no_kept_token(moe):
+    """T = 0: every token is out of [0, T) and read as zeros, x has no row and may be NULL."""
+    c = Case([30, 0, 9], 256, 256, seed=14)
+    _, zc, zs = moe.moe_grouped_mlp_fwd_ckpt8(c.x, c.w1, c.w2, c.offsets, c.prob)
+    none = torch.zeros((0, 256), dtype=torch.uint8, device="cuda")
+    got = moe.moe_grouped_mlp_bwd_ckpt8(c.dy, none, zc, zs, c.prob, c.w1, c.w2, c.offsets, x_scale=none.view(0, 256)[:, :8].contiguous(),
+                                        src_token=c.src)
+    want = moe.moe_grouped_mlp_bwd_ckpt8(c.dy, torch.zeros_like(c.x), zc, zs, c.prob, c.w1, c.w2, c.offsets)
+    assert all(torch.equal(a, b) for a, b in zip(got, want)) and not got[1].any() and bool(got[2].any())
