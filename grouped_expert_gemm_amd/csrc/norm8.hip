@@ -10,8 +10,10 @@
 // residual, sum and y: 773 MB in 154 us (5.0 TB/s; a copy reaches 5.2); 8192 x 4096, one row: 303 MB in
 // 50 to 57 us. One wavefront a row of 2048 takes as long (155 us).
 // The sums of 8 squares are added up in float64 and r is kept as two float32 words, so that n is the
-// exact product rounded about once: of the values next to a border between two codes, most that
-// float32 sums and products would push across it stay on their side.
+// exact product rounded about once. Where that rounding lands on a border (the middle between two codes,
+// or between two bf16 values), the side that it came from is put into its last bit (round_to_odd), so
+// that the codes, their scales and a bf16 y are those of the product itself: of 33.5 M values about 20
+// would land on the wrong side. One value in 2^15 to 2^19 needs it, so the others only look.
 #include <type_traits>
 
 #include "common.h"
@@ -91,6 +93,15 @@ __device__ __forceinline__ Raw<BF16> pack8(const float* f) {
   return r;
 }
 
+// n = x + d, |d| at most half a step of n, as n with an odd last bit where d is not 0: it lies on
+// x + d's side of every value that has fewer bits, so rounding it further rounds x + d itself.
+// Infinities and NaN (d no less than n, or NaN) stay as they are.
+__device__ __forceinline__ float round_to_odd(float n, float d) {
+  const int32_t u = __float_as_int(n);
+  const bool even = (u & 1) == 0 && (d < 0.f || d > 0.f) && __builtin_fabsf(d) < __builtin_fabsf(n);
+  return __int_as_float(even ? u + (((u ^ __float_as_int(d)) >> 31) | 1) : u);
+}
+
 template <bool BF16, int TPR, int NV>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_norm_kernel(const Params p) {
   constexpr int kTeams = TPR < 256 ? 256 / TPR : 1;
@@ -105,6 +116,9 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_norm_kernel(const P
     if (i * TPR + tr < groups) w[i] = load8<BF16>(p.w, i * TPR + tr);
   }
   const int64_t R = p.T * p.k;
+  // bits that are all 0 in the middle between two codes and where a block's scale changes, and, for a
+  // bf16 y, in the middle between two bf16 values
+  const uint32_t border = BF16 && p.y ? 0x7FFFu : 0x7FFFFu;
   int par = 0;
   // every thread of a workgroup runs the same rows' loop where the workgroup is one team
   for (int64_t t = (int64_t)blockIdx.x * kTeams + threadIdx.x / TPR; t < p.T; t += (int64_t)gridDim.x * kTeams) {
@@ -134,7 +148,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_norm_kernel(const P
         }
       }
 #pragma unroll
-      for (int u = 0; u < kSlots; ++u)
+      for (int u = 0; u < kSlots; ++u) {
+        if (j0 + u >= p.k) break;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           float f[V];
@@ -142,6 +157,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_norm_kernel(const P
 #pragma unroll
           for (int v = 0; v < V; ++v) acc[i][v] += f[v];
         }
+      }
     }
     double ss = 0.0;
 #pragma unroll
@@ -169,31 +185,50 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_norm_kernel(const P
     // r to float64 by one Newton step from its float32 value (0 and NaN stay as they are)
     const double m = ss * inv_h + (double)p.eps, r0 = (double)(1.f / sqrtf((float)m));
     const double r = r0 > 0.0 ? r0 * (1.5 - 0.5 * m * r0 * r0) : r0;
-    const float rh = (float)r, rl = (float)(r - (double)rh);
-    if (p.rstd && tr == 0) p.rstd[t] = rh;
+    // in two words, for bf16 rows the first of 16 bits: s times it is exact
+    const float rf = (float)r, rh = BF16 ? __uint_as_float(__float_as_uint(rf) & 0xFFFFFF00u) : rf;
+    const float rl = (float)(r - (double)rh);
+    if (p.rstd && tr == 0) p.rstd[t] = rf;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int64_t at = t * groups + i * TPR + tr;
       const bool in = i * TPR + tr < groups;  // groups % 4 == 0: the four lanes of a block agree
-      float f[V];
+      float f[V], n[V], top = 0.f;
       unpack8<BF16>(w[i], f);
-      float top = 0.f;
+      auto product = [&](int v, float& q, float& t) {  // s r w = q w + t
+        const float a = acc[i][v];
+        q = a * rh;
+        t = (BF16 ? a * rl : __builtin_fmaf(a, rl, __builtin_fmaf(a, rh, -q))) * f[v];
+      };
+      uint32_t low = ~0u;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const float a = acc[i][v], q = a * rh;
-        const float e = __builtin_fmaf(a, rl, __builtin_fmaf(a, rh, -q));  // s r - q
-        acc[i][v] = __builtin_fmaf(q, f[v], e * f[v]);
-        top = mx8::max_magnitude(top, acc[i][v]);
+        float q, t;
+        product(v, q, t);
+        n[v] = __builtin_fmaf(q, f[v], t);
+        low = min(low, __float_as_uint(n[v]) & border);
+        top = mx8::max_magnitude(top, n[v]);
       }
-      if (p.y && in) store8<BF16>(p.y, at, pack8<BF16>(acc[i]));
+      if (!BF16 && p.y && in) store8<BF16>(p.y, at, pack8<BF16>(n));
+      if (low == 0) {
+        top = 0.f;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          float q, t;
+          product(v, q, t);
+          n[v] = round_to_odd(n[v], __builtin_fmaf(q, f[v], -n[v]) + t);
+          top = mx8::max_magnitude(top, n[v]);
+        }
+      }
+      if (BF16 && p.y && in) store8<BF16>(p.y, at, pack8<BF16>(n));
       top = __uint_as_float(lanes_reduce<4>(__float_as_uint(top), [](uint32_t a, uint32_t b) {
         return __float_as_uint(mx8::max_magnitude(__uint_as_float(a), __uint_as_float(b)));
       }));
       const int b = mx8::scale_byte(top);
       const float sc = mx8::scale_value(b);
       if (in) {
-        p.codes[at] = make_uint2(mx8::pack4(acc[i][0], acc[i][1], acc[i][2], acc[i][3], sc, b),
-                                 mx8::pack4(acc[i][4], acc[i][5], acc[i][6], acc[i][7], sc, b));
+        p.codes[at] = make_uint2(mx8::pack4(n[0], n[1], n[2], n[3], sc, b),
+                                 mx8::pack4(n[4], n[5], n[6], n[7], sc, b));
         if ((threadIdx.x & 3) == 0) p.scales[at >> 2] = (uint8_t)b;
       }
     }

@@ -1,11 +1,12 @@
 """The norm to MXFP8 rows where its results are known to (almost) the last bit.
 
-The product s r w is rounded once, and little more: s r is kept in two float32 words, r in two, and the sums of
-squares in float64 beside float32 sums of eight. With integers of up to 255 those sums of eight are exact
+The product s r w is rounded once, and little more: r is kept in two float32 words (s times the first is exact
+for bf16 rows, and has a second word for float32 rows), and the sums of squares in float64 beside float32 sums of
+eight. With integers of up to 255 those sums of eight are exact
 (8 * 255^2 < 2^24). r is one Newton step in float64 from a float32 value off by at most 8 u (u = 2^-24: a
 rounding each of the mean, the root and the quotient, correctly rounded or nearly): off by 1.5 (8 u)^2 < 2^-17 u.
-The two words of r, the second word of s r and its product with w add less than 8 u^2. What is left is the
-product's own rounding: u (1 + 2^-16) of the value in all."""
+The second words and their products with w add less than 2^-39. What is left is the product's own rounding:
+u (1 + 2^-13) of the value in all."""
 import numpy as np
 import pytest
 import torch
@@ -16,7 +17,7 @@ from moe_inputs import bf16_bits_to_f32, f32_to_bf16_bits
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
-ONCE = U * (1 + 2.0 ** -16)
+ONCE = U * (1 + 2.0 ** -13)
 
 
 @pytest.fixture(scope="module")
@@ -98,3 +99,40 @@ def test_codes_of_exact_values(moe, H, dtype):
 def f32_to_bf16_f(a):
     """values rounded to bf16: products with 1/2 and 3/2 are then exact in float32"""
     return bf16_bits_to_f32(f32_to_bf16_bits(np.ascontiguousarray(a, np.float32)))
+
+
+@pytest.mark.parametrize("H", [512, 4096, 16384])
+def test_codes_next_to_a_border(moe, H):
+    """Products within a float32 step or two of the middle between two codes, on either side: the codes are
+    those of the product, not of its float32 rounding, which often is the middle itself. Known to 2^-40: r to
+    1.5 (8 u)^2 < 2^-41, the second words to a few u^2 each."""
+    g, eps = np.random.default_rng(H), 2.0 ** -20
+    wrong_after_rounding = 0
+    for _ in range(4):
+        s = g.integers(1, 256, (1, H)).astype(np.float64) * g.choice([-1.0, 1.0], (1, H))
+        rstd = 1 / np.sqrt((s * s).mean() + eps)
+        middle = (2 * g.integers(8, 16, H) + 1) / 16 * np.exp2(g.integers(-2, 1, H))
+        wf, w = _put(middle / (np.abs(s[0]) * rstd) * (1 + U * g.integers(-1, 2, H)), False)
+        n = s * rstd * wf
+        _, x = _put(s, False)
+        r = moe.moe_add_norm_mxfp8(x, w, eps=eps, with_y=True)
+        lo, hi, ok = oracle.mxfp8_bounds(n, 2.0 ** -40 * np.abs(n), host(r["scales"]))
+        v = oracle.mxfp8_dequantize(host(r["codes"]), host(r["scales"]))
+        assert ok.all() and np.all((lo <= v) & (v <= hi)), f"{int(((v < lo) | (v > hi)).sum())} of {H} codes"
+        assert np.all(np.abs(host(r["y"]) - n) <= ONCE * np.abs(n))          # y is rounded to nearest
+        lo, hi, _ = oracle.mxfp8_bounds(n.astype(np.float32).astype(np.float64), 0 * n, host(r["scales"]))
+        wrong_after_rounding += int((lo != v).sum())
+    assert wrong_after_rounding > H // 16      # the inputs are what they are meant to be
+
+
+def test_bf16_output_next_to_a_border(moe):
+    """A bf16 y is the product rounded once: half a bf16 step off, and 2^-38 for what the product is known to (r's
+    second word, and its product with w, are each rounded 2^-16 below: 2^-40 and 2^-40, and r's 2^-41)."""
+    g, eps = np.random.default_rng(3), 2.0 ** -20
+    for H in (2048, 8192, 16384):
+        sf, x = _put(g.integers(-255, 256, (64, H)), True)
+        wf, w = _put(1 + 0.2 * g.standard_normal(H), True)
+        y = host(moe.moe_add_norm_mxfp8(x, w, eps=eps, with_y=True)["y"])
+        n = sf / np.sqrt((sf * sf).mean(1, keepdims=True) + eps) * wf
+        half = np.exp2(np.floor(np.log2(np.maximum(np.abs(n), 1e-30))) - 8)
+        assert np.all(np.abs(y - n) <= half + 2.0 ** -38 * np.abs(n))
