@@ -91,7 +91,7 @@ __host__ __device__ __forceinline__ void tile_in_expert(int local, int mte, int 
   nt = rem / gm;
 }
 
-// The value of the lane that CTRL names, 0 where there is none and in rows outside ROWS (of 16 lanes each).
+// The value of the lane that CTRL names; `none` where there is none and in rows outside ROWS (of 16 lanes each).
 template <int CTRL, int ROWS = 0xF>
 __device__ __forceinline__ int lane_from(int v, int none = 0) {
   return __builtin_amdgcn_update_dpp(none, v, CTRL, ROWS, 0xF, false);
@@ -99,7 +99,8 @@ __device__ __forceinline__ int lane_from(int v, int none = 0) {
 
 // Scans over the lanes of a wavefront (every lane active): lane l gets op over lanes 0..l, op(v, 0) = v.
 // Within rows of 16 by lane moves of the vector ALU, then each row's last lane to the next row and lane
-// 31 to the upper half. Shuffles through LDS, six a scan, cost a launch over one expert 1.2 us.
+// 31 to the upper half. A grouped linear of one expert's 4885 rows, 512 x 256: 21.0 us; with shuffles
+// through LDS, six a scan, 21.9.
 template <typename F>
 __device__ __forceinline__ int wave_scan(int v, F op) {
   v = op(v, lane_from<0x111>(v));       // row_shr 1, 2, 4, 8

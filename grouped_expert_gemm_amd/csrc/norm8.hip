@@ -7,8 +7,8 @@
 // HBM-bound: k + 1 rows in, the sum, the codes and (on request) n in the stored dtype out. A
 // team of TPR threads holds one row in registers, NV groups of 8 columns a thread, so four
 // neighbouring lanes hold a block; its maximum takes two lane moves. 16384 x 2048, 8 rows a token,
-// residual, sum and y: 773 MB in 154 us (5.0 TB/s; a copy reaches 5.2); 8192 x 4096, one row: 303 MB in
-// 50 to 57 us. One wavefront a row of 2048 takes as long (155 us).
+// residual, sum and y: 773 MB in 156 to 160 us (4.9 TB/s; a copy reaches 5.2); 8192 x 4096, one row:
+// 303 MB in 55 to 60 us (5.1 TB/s). One wavefront a row of 2048 takes as long.
 // The sums of 8 squares are added up in float64 and r is kept as two float32 words, so that n is the
 // exact product rounded about once. Where that rounding lands on a border (the middle between two codes,
 // or between two bf16 values), the side that it came from is put into its last bit (round_to_odd), so
@@ -116,8 +116,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_norm_kernel(const P
     if (i * TPR + tr < groups) w[i] = load8<BF16>(p.w, i * TPR + tr);
   }
   const int64_t R = p.T * p.k;
-  // bits that are all 0 in the middle between two codes and where a block's scale changes, and, for a
-  // bf16 y, in the middle between two bf16 values
+  // bits that are all 0 (in normal numbers) in the middle between two codes and where a block's scale
+  // changes, and, for a bf16 y, in the middle between two bf16 values
   const uint32_t border = BF16 && p.y ? 0x7FFFu : 0x7FFFFu;
   int par = 0;
   // every thread of a workgroup runs the same rows' loop where the workgroup is one team
@@ -210,7 +210,7 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void add_norm_kernel(const P
         top = mx8::max_magnitude(top, n[v]);
       }
       if (!BF16 && p.y && in) store8<BF16>(p.y, at, pack8<BF16>(n));
-      if (low == 0) {
+      if (__builtin_expect(__any(low == 0), 0)) {
         top = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) {
