@@ -317,8 +317,9 @@ moe_status moe_post_norm_bwd(const void* dout, const void* c, const float* rstd,
  *   r[t]   = 1 / sqrt(mean_h s[t, h]^2 + eps),   n[t, h] = s[t, h] r[t] weight[h]
  *   codes  = MXFP8 of n along the row: per 32 columns one scale 2^e, e the smallest with
  *            max|n| <= 448 * 2^e, and the E4M3 code of n / 2^e (the rule of mxfp8_quantize on
- *            the float32 values, which are not rounded to bf16 first). A block that holds an
- *            infinity or a NaN gets scale byte 255 (E8M0's NaN) and codes 0.
+ *            the products themselves, which are rounded neither to bf16 nor onto a border of two
+ *            codes first). A block that holds an infinity or a NaN gets scale byte 255 (E8M0's
+ *            NaN) and codes 0.
  *   x [T, H] (row_id_map NULL and k = 1) or [T*k, H], residual [T, H] or NULL for 0, weight [H],
  *   sum [T, H] (out, may be NULL), y [T, H] (out, may be NULL): n rounded to dt; all dtype dt (F32
  *   or BF16); rstd [T] float32 (out, may be NULL); codes [T, H], scales [T, H/32] (out)
